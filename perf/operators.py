@@ -37,35 +37,35 @@ TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 def listed():
     return [
         # one token through one expert-sized layer: generation at batch one, latency counts
-        {"name": "gated, one token", "op": "gated", "form": "dense", "m": 1, "k": 7168, "f": 2048, "groups": 1,
+        {"name": "gated one token", "op": "gated", "form": "dense", "m": 1, "k": 7168, "f": 2048, "groups": 1,
          "out": "bf16", "checkpoint": False, "activation": "silu"},
         # a short prompt through a narrow layer whose width fills no tile
-        {"name": "gated, odd sizes", "op": "gated", "form": "dense", "m": 333, "k": 1536, "f": 1000, "groups": 1,
+        {"name": "gated odd sizes", "op": "gated", "form": "dense", "m": 333, "k": 1536, "f": 1000, "groups": 1,
          "out": "bf16", "checkpoint": False, "activation": "gelu_tanh"},
         # a decode batch routed to 16 experts of capacity 256, counts only known on the device
-        {"name": "gated, masked experts", "op": "gated", "form": "masked", "m": 256, "k": 7168, "f": 2048,
+        {"name": "gated masked experts", "op": "gated", "form": "masked", "m": 256, "k": 7168, "f": 2048,
          "groups": 16, "out": "fp8", "checkpoint": False, "activation": "silu"},
         # a training step's forward pass over 4096 tokens, with the checkpoint for its backward pass
-        {"name": "gated, training", "op": "gated", "form": "dense", "m": 4096, "k": 7168, "f": 2048, "groups": 1,
+        {"name": "gated training", "op": "gated", "form": "dense", "m": 4096, "k": 7168, "f": 2048, "groups": 1,
          "out": "fp8", "checkpoint": True, "activation": "silu"},
         # a prefill batch over 8 experts, 256 to 8192 tokens each
-        {"name": "gated, experts", "op": "gated", "form": "contiguous", "m": 8192, "k": 7168, "f": 2048, "groups": 8,
+        {"name": "gated experts", "op": "gated", "form": "contiguous", "m": 8192, "k": 7168, "f": 2048, "groups": 8,
          "out": "fp8", "checkpoint": False, "activation": "silu"},
         # the backward pass of a short batch whose rows fill no block of 128
-        {"name": "gated backward, odd rows", "op": "gated backward", "form": "dense", "m": 77, "f": 384, "groups": 1,
+        {"name": "gated backward odd rows", "op": "gated backward", "form": "dense", "m": 77, "f": 384, "groups": 1,
          "activation": "gelu_tanh"},
         # the backward pass of the experts' training step
-        {"name": "gated backward, experts", "op": "gated backward", "form": "contiguous", "m": 8192, "f": 2048,
+        {"name": "gated backward experts", "op": "gated backward", "form": "contiguous", "m": 8192, "f": 2048,
          "groups": 8, "activation": "silu"},
         # saving the activations of 4096 tokens in 8 bits
-        {"name": "checkpoint, save", "op": "save", "m": 4096, "k": 7168},
+        {"name": "checkpoint save", "op": "save", "m": 4096, "k": 7168},
         # the saved activations as an operand of the weights' gradient, over a ragged number of tokens
-        {"name": "checkpoint, use", "op": "use", "form": "contiguous", "m": 4097, "k": 7168, "groups": 8},
+        {"name": "checkpoint use", "op": "use", "form": "contiguous", "m": 4097, "k": 7168, "groups": 8},
         # a short batch of odd width in single precision
-        {"name": "layer norm, odd width", "op": "layer norm", "m": 197, "n": 1001, "type": "fp32", "out": "same",
+        {"name": "layer norm odd width", "op": "layer norm", "m": 197, "n": 1001, "type": "fp32", "out": "same",
          "bias": True},
         # the norm before the feed-forward block, its result as the product's 8-bit operand
-        {"name": "layer norm, to 8 bits", "op": "layer norm", "m": 16384, "n": 7168, "type": "bf16", "out": "fp8",
+        {"name": "layer norm to 8 bits", "op": "layer norm", "m": 16384, "n": 7168, "type": "bf16", "out": "fp8",
          "bias": True},
         # its backward pass with the weight's and the bias's gradients
         {"name": "layer norm backward", "op": "layer norm backward", "m": 16384, "n": 7168, "type": "bf16"},
