@@ -73,6 +73,14 @@ typedef enum dg_sf_format {
   DG_SF_UE8M0_PACKED = 1  /* int32, [G, ceil(K/512), align(MN, 4)], the layout described above */
 } dg_sf_format;
 
+/* Element type of a tensor, where an entry point takes several. */
+typedef enum dg_dtype { DG_DTYPE_FP32 = 0, DG_DTYPE_BF16 = 1, DG_DTYPE_FP16 = 2 } dg_dtype;
+
+/* Activation of the gated feed-forward product, h = act(g) * u:
+ *   SILU       act(g) = g / (1 + exp(-g))
+ *   GELU_TANH  act(g) = g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+typedef enum dg_activation { DG_ACT_SILU = 0, DG_ACT_GELU_TANH = 1 } dg_activation;
+
 /* ------------------------------------------------------------------------ */
 /* GEMMs                                                                     */
 /* ------------------------------------------------------------------------ */
@@ -322,6 +330,101 @@ dg_status dg_quantize_fp8_cols(const float* x, void* q, void* sf, int64_t rows, 
  * (transform_sf_into_required_layout). */
 dg_status dg_transform_sf(const float* sf, int32_t* packed, int64_t groups, int64_t mn, int64_t k,
                           int32_t block_rows, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit activation checkpoints                                              */
+/* ------------------------------------------------------------------------ */
+
+/* Save: BF16 rows -> E4M3 + packed scales, dg_quantize_fp8's rule and layout
+ * with block_rows = 1 (bitwise what it gives for the same numbers in FP32).
+ *   x   BF16 [groups, rows, cols] (contiguous), cols % 128 == 0
+ *   q   E4M3 [groups, rows, cols] (contiguous)
+ *   sf  int32 [groups, ceil(cols/512), align(rows, 4)] */
+dg_status dg_quantize_fp8_bf16(const void* x, void* q, int32_t* sf, int64_t groups, int64_t rows,
+                               int64_t cols, void* stream);
+
+/* Restore: E4M3 + packed row-group scales -> the values they stand for, in
+ * out_dtype DG_DTYPE_FP32 or DG_DTYPE_BF16 (exact in both, except scales
+ * below 2^-117, whose smallest values BF16 rounds).
+ *   q, sf  as dg_quantize_fp8_bf16 writes them;  x [groups, rows, cols] */
+dg_status dg_dequantize_fp8(const void* q, const int32_t* sf, void* x, int32_t out_dtype,
+                            int64_t groups, int64_t rows, int64_t cols, void* stream);
+
+/* Use in the backward pass: the saved rows as an operand whose reduction axis
+ * is the row axis (A or B of dg_k_grouped_fp8_gemm_tn_contiguous), requantised
+ * from the values the codes stand for with one scale per 128 rows of each
+ * column.
+ *   q         E4M3 [rows, cols] (contiguous), cols % 128 == 0, any rows
+ *   sf        packed row-group scales, int32 [ceil(cols/512), align(rows, 4)]
+ *   m_indices int32 [rows] on the device or NULL: a row whose entry is
+ *             negative (padding of the contiguous layout) counts as zero,
+ *             whatever its codes and scales hold
+ *   q_cols    E4M3 [align(rows, 128), cols]; rows past `rows` are zero
+ *   sf_cols   int32 [ceil(rows/512), cols], dg_quantize_fp8_cols's layout */
+dg_status dg_requantize_fp8_cols(const void* q, const int32_t* sf, const int32_t* m_indices,
+                                 void* q_cols, int32_t* sf_cols, int64_t rows, int64_t cols,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gated feed-forward product                                                */
+/* ------------------------------------------------------------------------ */
+
+/* Backward pass of h = act(g) * u from the 8-bit checkpoint of [g | u]:
+ *   dg = dh u act'(g),  du = dh act(g)
+ * as the operands of the three gradient products:
+ *   dh        BF16 [m, f], row stride lddh (lddh >= f, lddh % 4 == 0), 8-byte aligned
+ *   gu        E4M3 [m, 2f] (contiguous), the checkpoint's codes, g first
+ *   gu_sf     packed row-group scales, int32 [ceil(2f/512), align(m, 4)]
+ *   m_indices int32 [m] on the device or NULL: rows with a negative entry
+ *             count as zero, whatever dh and the checkpoint hold there
+ *   q, sf           [dg | du] with 1 x 128 groups: E4M3 [m, 2f], layout of gu_sf
+ *   q_cols, sf_cols [dg | du] with one scale per 128 rows of each column:
+ *                   E4M3 [align(m, 128), 2f], int32 [ceil(m/512), 2f]
+ *   h_cols, h_sf_cols  h = act(g) u in the same form: E4M3 [align(m, 128), f],
+ *                   int32 [ceil(m/512), f]
+ * f % 128 == 0; any m (rows past m are zero in the column forms). */
+dg_status dg_fp8_gated_backward(const void* dh, int64_t lddh, const void* gu, const int32_t* gu_sf,
+                                const int32_t* m_indices, void* q, int32_t* sf, void* q_cols,
+                                int32_t* sf_cols, void* h_cols, int32_t* h_sf_cols, int64_t m,
+                                int64_t f, int32_t activation, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Layer norm                                                                */
+/* ------------------------------------------------------------------------ */
+
+/* y = (x - mean) rstd w + b over the last axis, mean and rstd =
+ * 1 / sqrt(var + eps) of each row (FP32; the variance divides by cols).
+ *   x       [rows, cols] of `dtype`, row stride ldx >= cols
+ *   weight  [cols], bias [cols] or NULL, of w_dtype: DG_DTYPE_FP32 or `dtype`
+ *   y, sf   sf == NULL: y [rows, cols] of `dtype` (contiguous);
+ *           else y is E4M3 [rows, cols] and sf its packed 1 x 128 row-group
+ *           scales, int32 [ceil(cols/512), align(rows, 4)] (quantised from
+ *           FP32): cols % 128 == 0, cols <= 16384 (FP32 x) or 32768, x and y
+ *           16-byte aligned and ldx a multiple of 16 bytes
+ *   mean, rstd  float [rows], kept for the backward pass
+ * cols >= 1; rows == 0 is a no-op. */
+dg_status dg_layer_norm(const void* x, int32_t dtype, const void* weight, const void* bias,
+                        int32_t w_dtype, void* y, int32_t* sf, float* mean, float* rstd,
+                        int64_t rows, int64_t cols, int64_t ldx, float eps, void* stream);
+
+/* With xh = (x - mean) rstd and t = w dy:
+ *   dx = rstd (t - mean(t) - xh mean(t xh)),
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *   dy   [rows, cols] of `dtype`, row stride lddy;  dx the same, contiguous
+ *   dweight, dbias  float [cols], every element written (0 when rows == 0)
+ *   workspace  dg_layer_norm_backward_workspace_size bytes, 4-byte aligned;
+ *              needs no initialisation.  Calls that can overlap on the device
+ *              need separate ones.
+ * Sums are added in a fixed order: results are reproducible bit for bit on
+ * the same SM count. */
+dg_status dg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, const void* weight,
+                                 int32_t w_dtype, const float* mean, const float* rstd, void* dx,
+                                 float* dweight, float* dbias, void* workspace,
+                                 uint64_t workspace_bytes, int64_t rows, int64_t cols, int64_t lddy,
+                                 int64_t ldx, void* stream);
+/* Bytes of workspace dg_layer_norm_backward needs for `cols` columns on
+ * num_sms SMs (the device's count, or the dg_set_num_sms limit). */
+dg_status dg_layer_norm_backward_workspace_size(int64_t cols, int32_t num_sms, uint64_t* bytes);
 
 /* ------------------------------------------------------------------------ */
 /* Utilities (same page, section "Utilitários e variáveis de ambiente")      */

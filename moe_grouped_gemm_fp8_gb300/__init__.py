@@ -37,5 +37,14 @@ from .api import (  # noqa: F401
     sf_packed_shape,
     transform_sf_into_required_layout,
 )
+from .feedforward import (  # noqa: F401
+    GatedGradients,
+    LayerNormOutput,
+    dequantize_fp8,
+    fp8_gated_backward,
+    layer_norm,
+    layer_norm_backward,
+    requantize_fp8_cols,
+)
 
 __version__ = "0.1.0"

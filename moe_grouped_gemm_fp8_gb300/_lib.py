@@ -24,6 +24,8 @@ STATUS_NAMES = {
 }
 DG_SF_FP32 = 0
 DG_SF_UE8M0_PACKED = 1
+DG_DTYPE_FP32, DG_DTYPE_BF16, DG_DTYPE_FP16 = 0, 1, 2
+DG_ACT_SILU, DG_ACT_GELU_TANH = 0, 1
 
 _p = C.c_void_p
 _i64 = C.c_int64
@@ -47,6 +49,14 @@ SIGNATURES = {
     "dg_quantize_fp8": (_st, [_p, _p, _p, _i64, _i64, _i64, _i32, _i32, _p]),
     "dg_quantize_fp8_cols": (_st, [_p, _p, _p, _i64, _i64, _i32, _p]),
     "dg_transform_sf": (_st, [_p, _p, _i64, _i64, _i64, _i32, _p]),
+    "dg_quantize_fp8_bf16": (_st, [_p, _p, _p, _i64, _i64, _i64, _p]),
+    "dg_dequantize_fp8": (_st, [_p, _p, _p, _i32, _i64, _i64, _i64, _p]),
+    "dg_requantize_fp8_cols": (_st, [_p, _p, _p, _p, _p, _i64, _i64, _p]),
+    "dg_fp8_gated_backward": (_st, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i32, _p]),
+    "dg_layer_norm": (_st, [_p, _i32, _p, _p, _i32, _p, _p, _p, _p, _i64, _i64, _i64, C.c_float, _p]),
+    "dg_layer_norm_backward": (_st, [_p, _p, _i32, _p, _i32, _p, _p, _p, _p, _p, _p, C.c_uint64, _i64, _i64,
+                                     _i64, _i64, _p]),
+    "dg_layer_norm_backward_workspace_size": (_st, [_i64, _i32, C.POINTER(C.c_uint64)]),
     "dg_get_tma_aligned_size": (_i64, [_i64, _i32]),
     "dg_get_mk_alignment_for_contiguous_layout": (_i32, []),
     "dg_set_mk_alignment_for_contiguous_layout": (_st, [_i32]),

@@ -195,15 +195,18 @@ def sf_packed_shape(mn: int, k: int, groups: Optional[int] = None):
 
 
 def quantize_fp8(x: torch.Tensor, block_rows: int, packed: bool = True, out=None, stream=None):
-    """FP32 [rows, cols] or [G, rows, cols] -> (E4M3 codes, scales).
+    """FP32 or BF16 [rows, cols] or [G, rows, cols] -> (E4M3 codes, scales).
 
     block_rows=1: 1x128 row groups (activations); 128: 128x128 blocks
     (weights).  packed=True gives the int32 UE8M0 layout the GEMMs take;
     packed=False FP32 scales [G?, ceil(rows/block_rows), cols/128].
-    out=(q, sf) writes into preallocated tensors of those shapes."""
+    BF16 input (saving an activation in 8 bits) takes block_rows=1 and
+    packed=True.  out=(q, sf) writes into preallocated tensors of those shapes."""
     if x.dim() not in (2, 3):
         raise ValueError("x must be [rows, cols] or [groups, rows, cols]")
-    _need(x, "x", (torch.float32,), x.dim())
+    _need(x, "x", (torch.float32, torch.bfloat16), x.dim())
+    if x.dtype == torch.bfloat16 and (block_rows != 1 or not packed):
+        raise ValueError("BF16 input is quantised over 1x128 groups (block_rows=1) with packed scales")
     x = x.contiguous()
     grouped = x.dim() == 3
     groups = x.shape[0] if grouped else 1
@@ -225,6 +228,10 @@ def quantize_fp8(x: torch.Tensor, block_rows: int, packed: bool = True, out=None
                 not q.is_contiguous() or not sf.is_contiguous():
             raise ValueError("out tensors must be contiguous %s / %s" % (tuple(x.shape), sf_shape))
     _on_current_device(stream, x, q, sf)
+    if x.dtype == torch.bfloat16:
+        _check(_lib.lib().dg_quantize_fp8_bf16(_ptr(x), _ptr(q), _ptr(sf), groups, rows, cols, _stream(stream)),
+               "dg_quantize_fp8_bf16")
+        return q, sf
     st = _lib.lib().dg_quantize_fp8(_ptr(x), _ptr(q), _ptr(sf), groups, rows, cols, int(block_rows),
                                     _lib.DG_SF_UE8M0_PACKED if packed else _lib.DG_SF_FP32,
                                     _stream(stream))

@@ -232,4 +232,30 @@ cudaError_t transform_sf_launch(const float* sf, int32_t* packed, int64_t groups
                                 int64_t k, int block_rows, bool pdl, cudaStream_t stream);
 cudaError_t quant_fetch_error(unsigned long long* word);  // reads and clears
 
+
+// checkpoint.cu
+cudaError_t save_rows_launch(const void* x, void* q, void* sf, int64_t groups, int64_t rows,
+                             int64_t cols, bool pdl, cudaStream_t stream);
+cudaError_t restore_rows_launch(const void* q, const void* sf, void* x, int dtype, int64_t groups,
+                                int64_t rows, int64_t cols, bool pdl, cudaStream_t stream);
+cudaError_t use_cols_launch(const void* q, const void* sf, const int32_t* m_indices, void* qc,
+                            void* sfc, int64_t rows, int64_t cols, bool pdl, cudaStream_t stream);
+
+// gated_backward.cu
+cudaError_t gated_backward_launch(const void* dh, int64_t lddh, const void* gu, const void* gu_sf,
+                                  const int32_t* m_indices, void* q, void* sf, void* qc, void* sfc,
+                                  void* hc, void* hsfc, int64_t m, int64_t f, int activation, bool pdl,
+                                  cudaStream_t stream);
+
+// layer_norm.cu
+cudaError_t layer_norm_launch(const void* x, int dtype, const void* weight, const void* bias,
+                              bool w_fp32, void* y, void* sf, float* mean, float* rstd, int64_t rows,
+                              int64_t cols, int64_t ldx, float eps, bool pdl, cudaStream_t stream);
+int layer_norm_backward_parts(int sms);  // partial sums a column needs room for, at most
+cudaError_t layer_norm_backward_launch(const void* dy, const void* x, int dtype, const void* weight,
+                                       bool w_fp32, const float* mean, const float* rstd, void* dx,
+                                       float* dw, float* db, float* part, int parts, int64_t rows,
+                                       int64_t cols, int64_t lddy, int64_t ldx, bool pdl,
+                                       cudaStream_t stream);
+
 }  // namespace dg

@@ -1343,6 +1343,150 @@ dg_status dg_transform_sf(const float* sf, int32_t* packed, int64_t groups, int6
                                        static_cast<cudaStream_t>(stream)));
 }
 
+dg_status dg_quantize_fp8_bf16(const void* x, void* q, int32_t* sf, int64_t groups, int64_t rows,
+                               int64_t cols, void* stream) {
+  if (groups < 0 || rows < 0 || cols < 0) return DG_ERR_INVALID_ARG;
+  if (cols % kBlockK != 0) return DG_ERR_ALIGNMENT;
+  if (groups == 0 || rows == 0 || cols == 0) return DG_OK;
+  if (!x || !q || !sf) return DG_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(sf)) return DG_ERR_ALIGNMENT;
+  if (rows >= kMaxCoord || cols >= kMaxCoord || groups >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  if ((double)groups * (double)align4(rows) * (double)((cols + 511) / 512) >= 8.0 * (kMaxCoord - 1))
+    return DG_ERR_TOO_LARGE;
+  int sms = 0;
+  dg_status s = current_device(&sms);
+  if (s != DG_OK) return s;
+  return from_cuda(save_rows_launch(x, q, sf, groups, rows, cols, g_pdl.load() != 0,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_dequantize_fp8(const void* q, const int32_t* sf, void* x, int32_t out_dtype,
+                            int64_t groups, int64_t rows, int64_t cols, void* stream) {
+  if (groups < 0 || rows < 0 || cols < 0) return DG_ERR_INVALID_ARG;
+  if (out_dtype != DG_DTYPE_FP32 && out_dtype != DG_DTYPE_BF16) return DG_ERR_INVALID_ARG;
+  if (cols % kBlockK != 0) return DG_ERR_ALIGNMENT;
+  if (groups == 0 || rows == 0 || cols == 0) return DG_OK;
+  if (!x || !q || !sf) return DG_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(sf)) return DG_ERR_ALIGNMENT;
+  if (rows >= kMaxCoord || cols >= kMaxCoord || groups >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  if ((double)groups * (double)align4(rows) * (double)((cols + 511) / 512) >= 8.0 * (kMaxCoord - 1))
+    return DG_ERR_TOO_LARGE;
+  int sms = 0;
+  dg_status s = current_device(&sms);
+  if (s != DG_OK) return s;
+  return from_cuda(restore_rows_launch(q, sf, x, out_dtype, groups, rows, cols, g_pdl.load() != 0,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_requantize_fp8_cols(const void* q, const int32_t* sf, const int32_t* m_indices,
+                                 void* q_cols, int32_t* sf_cols, int64_t rows, int64_t cols,
+                                 void* stream) {
+  if (rows < 0 || cols < 0) return DG_ERR_INVALID_ARG;
+  if (cols % kBlockK != 0) return DG_ERR_ALIGNMENT;
+  if (rows == 0 || cols == 0) return DG_OK;
+  if (!q || !sf || !q_cols || !sf_cols) return DG_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(sf) || !aligned16(q_cols) || !aligned16(sf_cols) ||
+      (reinterpret_cast<uintptr_t>(m_indices) & 3u))
+    return DG_ERR_ALIGNMENT;
+  if (rows >= kMaxCoord - kBlockM || cols >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  if ((rows + kBlockM - 1) / kBlockM * (cols / kBlockK) >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  int sms = 0;
+  dg_status s = current_device(&sms);
+  if (s != DG_OK) return s;
+  return from_cuda(use_cols_launch(q, sf, m_indices, q_cols, sf_cols, rows, cols, g_pdl.load() != 0,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_fp8_gated_backward(const void* dh, int64_t lddh, const void* gu, const int32_t* gu_sf,
+                                const int32_t* m_indices, void* q, int32_t* sf, void* q_cols,
+                                int32_t* sf_cols, void* h_cols, int32_t* h_sf_cols, int64_t m,
+                                int64_t f, int32_t activation, void* stream) {
+  if (m < 0 || f < 0 || lddh < f) return DG_ERR_INVALID_ARG;
+  if (activation != DG_ACT_SILU && activation != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
+  if (f % kBlockK != 0 || lddh % 4 != 0) return DG_ERR_ALIGNMENT;
+  if (m == 0 || f == 0) return DG_OK;
+  if (!dh || !gu || !gu_sf || !q || !sf || !q_cols || !sf_cols || !h_cols || !h_sf_cols)
+    return DG_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(dh) & 7u) || (reinterpret_cast<uintptr_t>(m_indices) & 3u) ||
+      !aligned16(gu) || !aligned16(gu_sf) || !aligned16(q) || !aligned16(sf) || !aligned16(q_cols) ||
+      !aligned16(sf_cols) || !aligned16(h_cols) || !aligned16(h_sf_cols))
+    return DG_ERR_ALIGNMENT;
+  if (m >= kMaxCoord - kBlockM || f >= kMaxCoord / 2) return DG_ERR_TOO_LARGE;
+  if ((m + kBlockM - 1) / kBlockM * (f / kBlockK) >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  int sms = 0;
+  dg_status s = current_device(&sms);
+  if (s != DG_OK) return s;
+  return from_cuda(gated_backward_launch(dh, lddh, gu, gu_sf, m_indices, q, sf, q_cols, sf_cols, h_cols,
+                                         h_sf_cols, m, f, activation, g_pdl.load() != 0,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+static dg_status check_norm(int32_t dtype, int32_t w_dtype, int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1) return DG_ERR_INVALID_ARG;
+  if (dtype != DG_DTYPE_FP32 && dtype != DG_DTYPE_BF16 && dtype != DG_DTYPE_FP16) return DG_ERR_INVALID_ARG;
+  if (w_dtype != DG_DTYPE_FP32 && w_dtype != dtype) return DG_ERR_INVALID_ARG;
+  if (rows >= kMaxCoord - 4 || cols >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  return DG_OK;
+}
+
+dg_status dg_layer_norm(const void* x, int32_t dtype, const void* weight, const void* bias,
+                        int32_t w_dtype, void* y, int32_t* sf, float* mean, float* rstd,
+                        int64_t rows, int64_t cols, int64_t ldx, float eps, void* stream) {
+  dg_status s = check_norm(dtype, w_dtype, rows, cols);
+  if (s != DG_OK) return s;
+  if (ldx < cols || !(eps >= 0.0f)) return DG_ERR_INVALID_ARG;
+  if (sf && cols % kBlockK != 0) return DG_ERR_ALIGNMENT;
+  if (rows == 0) return DG_OK;
+  if (!x || !weight || !y || !mean || !rstd) return DG_ERR_INVALID_ARG;
+  const uintptr_t esz = dtype == DG_DTYPE_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % esz || reinterpret_cast<uintptr_t>(weight) % (w_dtype == DG_DTYPE_FP32 ? 4 : 2) ||
+      reinterpret_cast<uintptr_t>(bias) % (w_dtype == DG_DTYPE_FP32 ? 4 : 2) ||
+      (!sf && reinterpret_cast<uintptr_t>(y) % esz) || ((reinterpret_cast<uintptr_t>(mean) | reinterpret_cast<uintptr_t>(rstd)) & 3u))
+    return DG_ERR_ALIGNMENT;
+  if (sf) {
+    if (!aligned16(x) || !aligned16(y) || !aligned16(sf) || (ldx * (int64_t)esz) % 16 != 0) return DG_ERR_ALIGNMENT;
+    if (cols > (dtype == DG_DTYPE_FP32 ? 16384 : 32768)) return DG_ERR_TOO_LARGE;
+  }
+  int sms = 0;
+  if ((s = current_device(&sms)) != DG_OK) return s;
+  return from_cuda(layer_norm_launch(x, dtype, weight, bias, w_dtype == DG_DTYPE_FP32, y, sf, mean, rstd, rows,
+                                     cols, ldx, eps, g_pdl.load() != 0, static_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_layer_norm_backward_workspace_size(int64_t cols, int32_t num_sms, uint64_t* bytes) {
+  if (!bytes || cols < 1 || num_sms < 1) return DG_ERR_INVALID_ARG;
+  if (cols >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  *bytes = (uint64_t)2 * layer_norm_backward_parts(num_sms) * cols * sizeof(float);
+  return DG_OK;
+}
+
+dg_status dg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, const void* weight,
+                                 int32_t w_dtype, const float* mean, const float* rstd, void* dx,
+                                 float* dweight, float* dbias, void* workspace,
+                                 uint64_t workspace_bytes, int64_t rows, int64_t cols, int64_t lddy,
+                                 int64_t ldx, void* stream) {
+  dg_status s = check_norm(dtype, w_dtype, rows, cols);
+  if (s != DG_OK) return s;
+  if (ldx < cols || lddy < cols) return DG_ERR_INVALID_ARG;
+  if (!weight || !dweight || !dbias || !workspace) return DG_ERR_INVALID_ARG;
+  if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return DG_ERR_INVALID_ARG;
+  const uintptr_t esz = dtype == DG_DTYPE_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(dx)) % esz ||
+      reinterpret_cast<uintptr_t>(weight) % (w_dtype == DG_DTYPE_FP32 ? 4 : 2) ||
+      ((reinterpret_cast<uintptr_t>(mean) | reinterpret_cast<uintptr_t>(rstd) | reinterpret_cast<uintptr_t>(dweight) |
+        reinterpret_cast<uintptr_t>(dbias) | reinterpret_cast<uintptr_t>(workspace)) & 3u))
+    return DG_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((s = current_device(&sms)) != DG_OK) return s;
+  uint64_t need = 0;
+  if ((s = dg_layer_norm_backward_workspace_size(cols, sms, &need)) != DG_OK) return s;
+  if (workspace_bytes < need) return DG_ERR_INVALID_ARG;
+  return from_cuda(layer_norm_backward_launch(dy, x, dtype, weight, w_dtype == DG_DTYPE_FP32, mean, rstd, dx,
+                                              dweight, dbias, static_cast<float*>(workspace),
+                                              layer_norm_backward_parts(sms), rows, cols, lddy, ldx,
+                                              g_pdl.load() != 0, static_cast<cudaStream_t>(stream)));
+}
+
 int64_t dg_get_tma_aligned_size(int64_t x, int32_t element_size) {
   if (x < 0 || element_size <= 0 || 16 % element_size != 0) return -1;
   const int64_t unit = 16 / element_size;

@@ -1,0 +1,255 @@
+"""Torch-facing wrappers of the operators around a feed-forward block's GEMMs:
+8-bit activation checkpoints, the gated product's backward pass and layer norm.
+
+Argument marshalling only, as in ``api``: every step of the computation runs
+in libdg.so's kernels; there is no fallback.
+"""
+import ctypes as C
+from typing import NamedTuple, Optional, Tuple
+
+import torch
+
+from . import _lib
+from .api import FP8_DTYPES, _check, _need, _on_current_device, _ptr, _stream, get_num_sms, sf_packed_shape
+
+ACTIVATIONS = {"silu": _lib.DG_ACT_SILU, "gelu_tanh": _lib.DG_ACT_GELU_TANH}
+_DTYPES = {torch.float32: _lib.DG_DTYPE_FP32, torch.bfloat16: _lib.DG_DTYPE_BF16,
+           torch.float16: _lib.DG_DTYPE_FP16}
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError("activation %r not in %s" % (name, sorted(ACTIVATIONS)))
+    return ACTIVATIONS[name]
+
+
+def _contiguous(**tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+def _used_on(stream, *tensors) -> None:
+    """Temporary tensors used on an explicit stream: their memory is not
+    handed out again before that stream is past this call."""
+    if stream is None:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in tensors:
+        t.record_stream(stream)
+
+
+def _row_index(m_indices: Optional[torch.Tensor], rows: int) -> None:
+    if m_indices is not None:
+        _need(m_indices, "m_indices", (torch.int32,), 1)
+        if m_indices.numel() != rows or not m_indices.is_contiguous():
+            raise ValueError("m_indices must be contiguous [%d]" % rows)
+
+
+# ---------------------------------------------------------------- 8-bit checkpoints
+
+
+def dequantize_fp8(q: torch.Tensor, sf: torch.Tensor, dtype: torch.dtype = torch.bfloat16, out=None,
+                   stream=None) -> torch.Tensor:
+    """E4M3 codes [rows, cols] or [G, rows, cols] with packed 1x128 row-group
+    scales -> the values they stand for, in BF16 or FP32."""
+    if q.dim() not in (2, 3):
+        raise ValueError("q must be [rows, cols] or [groups, rows, cols]")
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("dtype %s is not float32 or bfloat16" % dtype)
+    _need(q, "q", FP8_DTYPES, q.dim())
+    _need(sf, "sf", (torch.int32,), q.dim())
+    groups = q.shape[0] if q.dim() == 3 else 1
+    rows, cols = q.shape[-2:]
+    want = sf_packed_shape(rows, cols, groups if q.dim() == 3 else None)
+    if tuple(sf.shape) != want:
+        raise ValueError("scale shape %s, expected %s" % (tuple(sf.shape), want))
+    _contiguous(q=q, sf=sf)
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=q.device)
+    _need(out, "out", (dtype,), q.dim())
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous %s" % (tuple(q.shape),))
+    _on_current_device(stream, q, sf, out)
+    _check(_lib.lib().dg_dequantize_fp8(_ptr(q), _ptr(sf), _ptr(out), _DTYPES[dtype], groups, rows, cols,
+                                        _stream(stream)), "dg_dequantize_fp8")
+    return out
+
+
+def requantize_fp8_cols(q: torch.Tensor, sf: torch.Tensor, m_indices: Optional[torch.Tensor] = None,
+                        out=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows saved in 8 bits as an operand of a weight gradient: E4M3 [rows,
+    cols] with packed 1x128 row-group scales -> (E4M3 [align(rows, 128), cols],
+    packed scales [ceil(rows/512), cols]) with one scale per 128 rows of each
+    column, the layout of k_grouped_fp8_gemm_tn_contiguous's operands.
+
+    m_indices: int32 [rows]; rows with a negative entry (padding of the
+    contiguous layout) and rows past `rows` are zero in the result."""
+    _need(q, "q", FP8_DTYPES, 2)
+    _need(sf, "sf", (torch.int32,), 2)
+    rows, cols = q.shape
+    if tuple(sf.shape) != sf_packed_shape(rows, cols):
+        raise ValueError("scale shape %s, expected %s" % (tuple(sf.shape), sf_packed_shape(rows, cols)))
+    _contiguous(q=q, sf=sf)
+    _row_index(m_indices, rows)
+    rows128 = (rows + 127) // 128 * 128
+    qc, sfc = _cols_out(out, rows128, cols, q.device, "out")
+    _on_current_device(stream, q, sf, m_indices, qc, sfc)
+    _check(_lib.lib().dg_requantize_fp8_cols(_ptr(q), _ptr(sf), _ptr(m_indices), _ptr(qc), _ptr(sfc), rows, cols,
+                                             _stream(stream)), "dg_requantize_fp8_cols")
+    return qc, sfc
+
+
+def _codes_out(out, shape, sf_shape, device, name):
+    """(codes, packed scales) to write: the caller's, checked, or new ones."""
+    if out is None:
+        return (torch.empty(shape, dtype=torch.float8_e4m3fn, device=device),
+                torch.empty(sf_shape, dtype=torch.int32, device=device))
+    q, sf = out
+    _need(q, name + " codes", FP8_DTYPES, len(shape))
+    _need(sf, name + " scales", (torch.int32,), len(sf_shape))
+    if tuple(q.shape) != tuple(shape) or tuple(sf.shape) != tuple(sf_shape) or \
+            not q.is_contiguous() or not sf.is_contiguous():
+        raise ValueError("%s must be contiguous %s / %s" % (name, tuple(shape), tuple(sf_shape)))
+    return q, sf
+
+
+def _cols_out(out, rows128, cols, device, name):
+    return _codes_out(out, (rows128, cols), sf_packed_shape(cols, rows128), device, name)
+
+
+# ---------------------------------------------------------------- gated product
+
+
+class GatedGradients(NamedTuple):
+    """fp8_gated_backward's results, E4M3 codes and packed scales each."""
+    q: torch.Tensor          # [dg | du] [M, 2F], 1x128 row groups: dX = q @ W (fp8_gemm_nn)
+    sf: torch.Tensor
+    q_cols: torch.Tensor     # [dg | du] [align(M, 128), 2F], 128 rows of a column: dW = q_cols^T X
+    sf_cols: torch.Tensor
+    h_cols: torch.Tensor     # act(g) u [align(M, 128), F], the same grouping: dW_down = dY^T h_cols
+    h_sf_cols: torch.Tensor
+
+
+def fp8_gated_backward(dh: torch.Tensor, gu: torch.Tensor, gu_sf: torch.Tensor,
+                       m_indices: Optional[torch.Tensor] = None, activation: str = "silu",
+                       stream=None) -> GatedGradients:
+    """Backward pass of h = act(g) * u from the 8-bit checkpoint of [g | u]:
+    dg = dh u act'(g) and du = dh act(g), with h recomputed, as the E4M3
+    operands of the gradient products.
+
+    dh BF16 [M, F] (unit column stride); gu E4M3 [M, 2F] with packed 1x128
+    row-group scales gu_sf (what the gated product keeps with
+    checkpoint=True); F % 128 == 0.  m_indices: int32 [M]; rows with a
+    negative entry count as zero, whatever dh and gu hold there."""
+    _need(dh, "dh", (torch.bfloat16,), 2)
+    _need(gu, "gu", FP8_DTYPES, 2)
+    _need(gu_sf, "gu_sf", (torch.int32,), 2)
+    act = _activation(activation)
+    m, f = dh.shape
+    if tuple(gu.shape) != (m, 2 * f):
+        raise ValueError("gu %s, expected %s" % (tuple(gu.shape), (m, 2 * f)))
+    if tuple(gu_sf.shape) != sf_packed_shape(m, 2 * f):
+        raise ValueError("scale shape %s, expected %s" % (tuple(gu_sf.shape), sf_packed_shape(m, 2 * f)))
+    if dh.stride(1) != 1:
+        raise ValueError("dh needs unit column stride")
+    _contiguous(gu=gu, gu_sf=gu_sf)
+    _row_index(m_indices, m)
+    m128 = (m + 127) // 128 * 128
+    q, sf = _codes_out(None, (m, 2 * f), sf_packed_shape(m, 2 * f), dh.device, "q")
+    qc, sfc = _cols_out(None, m128, 2 * f, dh.device, "q_cols")
+    hc, hsfc = _cols_out(None, m128, f, dh.device, "h_cols")
+    _on_current_device(stream, dh, gu, gu_sf, m_indices)
+    _check(_lib.lib().dg_fp8_gated_backward(_ptr(dh), dh.stride(0) if m > 1 else f, _ptr(gu), _ptr(gu_sf),
+                                            _ptr(m_indices), _ptr(q), _ptr(sf), _ptr(qc), _ptr(sfc), _ptr(hc),
+                                            _ptr(hsfc), m, f, act, _stream(stream)), "dg_fp8_gated_backward")
+    return GatedGradients(q, sf, qc, sfc, hc, hsfc)
+
+
+# ---------------------------------------------------------------- layer norm
+
+
+class LayerNormOutput(NamedTuple):
+    y: torch.Tensor                # x's type, or E4M3 codes
+    sf: Optional[torch.Tensor]     # packed 1x128 row-group scales of the codes, else None
+    mean: torch.Tensor             # FP32 [rows], for the backward pass
+    rstd: torch.Tensor
+
+
+def _norm_args(x, weight, bias):
+    _need(x, "x", tuple(_DTYPES), 2)
+    cols = x.shape[1]
+    if cols < 1:
+        raise ValueError("x needs at least one column")
+    if x.stride(1) != 1 and cols > 1:
+        raise ValueError("x needs unit column stride")
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, name, (torch.float32, x.dtype), 1)
+            if t.numel() != cols or not t.is_contiguous():
+                raise ValueError("%s must be contiguous [%d]" % (name, cols))
+    if bias is not None and bias.dtype != weight.dtype:
+        raise TypeError("weight and bias must have one dtype")
+
+
+def _row_stride(x: torch.Tensor) -> int:
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               out_format: str = "same", stream=None) -> LayerNormOutput:
+    """y = (x - mean) * rstd * weight + bias over the last axis of [rows, cols].
+
+    x FP32, BF16 or FP16 (unit column stride), weight and bias FP32 or x's
+    type.  out_format "same": y in x's type; "fp8": y as E4M3 codes with
+    packed 1x128 row-group scales (cols % 128 == 0), the operand of the FP8
+    GEMMs and at the same time the 8-bit checkpoint of the normed activation."""
+    _norm_args(x, weight, bias)
+    if out_format not in ("same", "fp8"):
+        raise ValueError("out_format %r not in ('same', 'fp8')" % (out_format,))
+    rows, cols = x.shape
+    sf = None
+    if out_format == "same":
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    else:
+        if cols % 128:
+            raise ValueError("out_format 'fp8' needs cols %% 128 == 0, got %d" % cols)
+        y, sf = _codes_out(None, (rows, cols), sf_packed_shape(rows, cols), x.device, "y")
+    mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _on_current_device(stream, x, weight, bias)
+    _check(_lib.lib().dg_layer_norm(_ptr(x), _DTYPES[x.dtype], _ptr(weight), _ptr(bias), _DTYPES[weight.dtype],
+                                    _ptr(y), _ptr(sf), _ptr(mean), _ptr(rstd), rows, cols, _row_stride(x),
+                                    float(eps), _stream(stream)), "dg_layer_norm")
+    return LayerNormOutput(y, sf, mean, rstd)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
+                        rstd: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dx, dweight, dbias) of layer_norm: dx in x's type, the parameters'
+    gradients in FP32 (summed in a fixed order)."""
+    _norm_args(x, weight, None)
+    _need(dy, "dy", (x.dtype,), 2)
+    _need(mean, "mean", (torch.float32,), 1)
+    _need(rstd, "rstd", (torch.float32,), 1)
+    rows, cols = x.shape
+    if dy.shape != x.shape or (dy.stride(1) != 1 and cols > 1):
+        raise ValueError("dy must be %s with unit column stride" % (tuple(x.shape),))
+    if mean.numel() != rows or rstd.numel() != rows:
+        raise ValueError("mean and rstd must be [%d]" % rows)
+    _contiguous(mean=mean, rstd=rstd)
+    dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    dw = torch.empty(cols, dtype=torch.float32, device=x.device)
+    db = torch.empty_like(dw)
+    need = C.c_uint64(0)
+    _check(_lib.lib().dg_layer_norm_backward_workspace_size(cols, get_num_sms(), C.byref(need)),
+           "dg_layer_norm_backward_workspace_size")
+    ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+    _used_on(stream, ws)
+    _on_current_device(stream, dy, x, weight, mean, rstd)
+    _check(_lib.lib().dg_layer_norm_backward(_ptr(dy), _ptr(x), _DTYPES[x.dtype], _ptr(weight),
+                                             _DTYPES[weight.dtype], _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dw),
+                                             _ptr(db), _ptr(ws), need.value, rows, cols, _row_stride(dy),
+                                             _row_stride(x), _stream(stream)), "dg_layer_norm_backward")
+    return dx, dw, db
