@@ -369,6 +369,46 @@ dg_status dg_requantize_fp8_cols(const void* q, const int32_t* sf, const int32_t
 /* Gated feed-forward product                                                */
 /* ------------------------------------------------------------------------ */
 
+/* Both projections, the activation and the product in one kernel:
+ *   g = A Wg^T,  u = A Wu^T,  h = act(g) * u      (B = [Wg; Wu], dequantised)
+ *   a, sfa    E4M3 [m, k] (row stride lda) and its scales, as dg_fp8_gemm_nt's
+ *   b, sfb    E4M3 [2f, k] (row stride ldb), Wg's f rows first, then Wu's, and
+ *             the packed scales of its 2f rows
+ *   h, h_sf   h_sf == NULL: h BF16 [m, f], row stride ldh (f % 8 == 0,
+ *             ldh % 8 == 0); else h E4M3 [m, f] (contiguous, ldh == f) and its
+ *             packed 1 x 128 row-group scales int32 [ceil(f/512), align(m, 4)]
+ *             (quantised from FP32 by dg_quantize_fp8's rule): f % 128 == 0
+ *   gu, gu_sf NULL, or the 8-bit checkpoint of [g | u]: E4M3 [m, 2f]
+ *             (contiguous) and its packed 1 x 128 row-group scales
+ *             int32 [ceil(2f/512), align(m, 4)]: f % 128 == 0
+ * Other checks as dg_fp8_gemm_nt; m == 0 or f == 0 is a no-op. */
+dg_status dg_fp8_gated_gemm_nt(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+                               void* h, int32_t* h_sf, void* gu, int32_t* gu_sf, int64_t m, int64_t f,
+                               int64_t k, int64_t lda, int64_t ldb, int64_t ldh, int32_t activation,
+                               void* stream);
+
+/* The same for the experts of the contiguous layout: a [m_sum, k],
+ * b [num_groups, 2f, k], m_indices as dg_m_grouped_fp8_gemm_nt_contiguous
+ * takes them (same rules and errors); all tensors contiguous.  Rows whose
+ * entry is negative keep what h, gu and their scale words held. */
+dg_status dg_m_grouped_fp8_gated_gemm_nt_contiguous(const void* a, const int32_t* sfa, const void* b,
+                                                    const int32_t* sfb, void* h, int32_t* h_sf,
+                                                    void* gu, int32_t* gu_sf, const int32_t* m_indices,
+                                                    int64_t m_sum, int64_t f, int64_t k,
+                                                    int32_t num_groups, int32_t activation,
+                                                    void* stream);
+
+/* The same for the masked layout: a [num_groups, max_m, k], b [num_groups,
+ * 2f, k], h [num_groups, max_m, f] (h_sf [num_groups, ceil(f/512),
+ * align(max_m, 4)]), masked_m and expected_m as
+ * dg_m_grouped_fp8_gemm_nt_masked takes them.  Rows past masked_m[g] keep
+ * what h and its scale words held. */
+dg_status dg_m_grouped_fp8_gated_gemm_nt_masked(const void* a, const int32_t* sfa, const void* b,
+                                                const int32_t* sfb, void* h, int32_t* h_sf,
+                                                const int32_t* masked_m, int32_t num_groups,
+                                                int64_t max_m, int64_t f, int64_t k,
+                                                int64_t expected_m, int32_t activation, void* stream);
+
 /* Backward pass of h = act(g) * u from the 8-bit checkpoint of [g | u]:
  *   dg = dh u act'(g),  du = dh act(g)
  * as the operands of the three gradient products:

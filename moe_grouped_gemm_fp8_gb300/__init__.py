@@ -39,11 +39,15 @@ from .api import (  # noqa: F401
 )
 from .feedforward import (  # noqa: F401
     GatedGradients,
+    GatedOutput,
     LayerNormOutput,
     dequantize_fp8,
     fp8_gated_backward,
+    fp8_gated_gemm_nt,
     layer_norm,
     layer_norm_backward,
+    m_grouped_fp8_gated_gemm_nt_contiguous,
+    m_grouped_fp8_gated_gemm_nt_masked,
     requantize_fp8_cols,
 )
 

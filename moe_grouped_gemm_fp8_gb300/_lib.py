@@ -52,6 +52,11 @@ SIGNATURES = {
     "dg_quantize_fp8_bf16": (_st, [_p, _p, _p, _i64, _i64, _i64, _p]),
     "dg_dequantize_fp8": (_st, [_p, _p, _p, _i32, _i64, _i64, _i64, _p]),
     "dg_requantize_fp8_cols": (_st, [_p, _p, _p, _p, _p, _i64, _i64, _p]),
+    "dg_fp8_gated_gemm_nt": (_st, [_p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64, _i32, _p]),
+    "dg_m_grouped_fp8_gated_gemm_nt_contiguous": (_st, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i32,
+                                                        _i32, _p]),
+    "dg_m_grouped_fp8_gated_gemm_nt_masked": (_st, [_p, _p, _p, _p, _p, _p, _p, _i32, _i64, _i64, _i64, _i64, _i32,
+                                                    _p]),
     "dg_fp8_gated_backward": (_st, [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i32, _p]),
     "dg_layer_norm": (_st, [_p, _i32, _p, _p, _i32, _p, _p, _p, _p, _i64, _i64, _i64, C.c_float, _p]),
     "dg_layer_norm_backward": (_st, [_p, _p, _i32, _p, _i32, _p, _p, _p, _p, _p, _p, C.c_uint64, _i64, _i64,

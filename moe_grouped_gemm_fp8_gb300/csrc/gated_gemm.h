@@ -1,0 +1,25 @@
+// Arguments and launches of the gated feed-forward product's kernels.
+#pragma once
+
+#include "dg_internal.h"
+
+namespace dg {
+
+struct GatedArgs {
+  GemmArgs base;           // m, k, groups, blocks (n_blocks: of 128 columns of h), timeouts
+  __nv_bfloat16* h;        // BF16 result [.., m, f], row stride ldh; or:
+  uint8_t* hq;             // E4M3 result [.., m, f] and its packed scales
+  uint32_t* hsf;
+  uint8_t* cq;             // nullable: E4M3 [.., m, 2f] of [g | u] and its packed scales
+  uint32_t* csf;
+  int64_t ldh;
+  int32_t f;
+  int32_t m_pad;           // align(m, 4): rows of a scale word's line
+  int32_t activation;      // dg_activation
+};
+
+// gated_gemm.cu; mode kDense, kContiguous or kMasked
+cudaError_t gated_gemm_launch(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& sfa,
+                              const CUtensorMap& sfb, GatedArgs args, int grid, cudaStream_t stream);
+
+}  // namespace dg

@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "dg_internal.h"
+#include "gated_gemm.h"
 
 namespace dg {
 namespace {
@@ -1395,6 +1396,97 @@ dg_status dg_requantize_fp8_cols(const void* q, const int32_t* sf, const int32_t
   if (s != DG_OK) return s;
   return from_cuda(use_cols_launch(q, sf, m_indices, q_cols, sf_cols, rows, cols, g_pdl.load() != 0,
                                    static_cast<cudaStream_t>(stream)));
+}
+
+// The three forms of the gated product (mode kDense, kContiguous, kMasked).
+static dg_status gated_gemm(int mode, const char* name, const void* a, const int32_t* sfa, const void* b,
+                            const int32_t* sfb, void* h, int32_t* h_sf, void* gu, int32_t* gu_sf,
+                            const int32_t* rows, int64_t m, int64_t f, int64_t k, int64_t lda, int64_t ldb,
+                            int64_t ldh, int32_t groups, int32_t activation, void* stream) {
+  if (m < 0 || groups < 0) return DG_ERR_INVALID_ARG;
+  if (activation != DG_ACT_SILU && activation != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
+  dg_status s = check_common_k_n(f, k);
+  if (s != DG_OK) return s;
+  if ((h_sf || gu) && f % kBlockK != 0) return DG_ERR_ALIGNMENT;
+  if (m == 0 || f == 0 || groups == 0) return DG_OK;
+  if (!a || !sfa || !b || !sfb || !h || (gu != nullptr) != (gu_sf != nullptr)) return DG_ERR_INVALID_ARG;
+  if (mode != kDense && !rows) return DG_ERR_INVALID_ARG;
+  if (lda < k || ldb < k || ldh < f || (h_sf && ldh != f)) return DG_ERR_INVALID_ARG;
+  if (lda % 16 || ldb % 16 || ldh % 8) return DG_ERR_ALIGNMENT;
+  if (mode == kContiguous && m % kBlockM != 0) return DG_ERR_ALIGNMENT;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(sfa) || !aligned16(sfb) || !aligned16(h) || !aligned16(h_sf) ||
+      !aligned16(gu) || !aligned16(gu_sf) || (reinterpret_cast<uintptr_t>(rows) & 3u))
+    return DG_ERR_ALIGNMENT;
+  if (mode == kMasked && groups > kMaxMaskedGroups) return DG_ERR_TOO_LARGE;
+  if (m >= kMaxCoord - kBlockM || f >= kMaxCoord / 4 || (int64_t)groups * 2 * f >= kMaxCoord ||
+      (mode == kMasked && (int64_t)groups * m >= kMaxCoord))
+    return DG_ERR_TOO_LARGE;
+  int sms = 0;
+  if ((s = current_device(&sms)) != DG_OK) return s;
+  if ((s = get_encoder()) != DG_OK) return s;
+
+  GatedArgs args = {};
+  args.base.m_blocks = (int32_t)((m + kBlockM - 1) / kBlockM);
+  args.base.n_blocks = (int32_t)((f + 127) / 128);
+  args.base.k_blocks = (int32_t)(k / kBlockK);
+  const int64_t tiles = (int64_t)args.base.m_blocks * args.base.n_blocks;
+  if (tiles * (mode == kMasked ? groups : 1) >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  Operands o;
+  if ((s = mode == kMasked ? encode_a_3d(o, a, sfa, groups, m, k) : encode_a_2d(o, a, sfa, m, k, lda)) != DG_OK)
+    return s;
+  // Wg's and Wu's 128 rows of a tile are two boxes of one map
+  if ((s = encode_b_side(o, b, sfb, groups, 2 * f, k, ldb, 128, 128)) != DG_OK) return s;
+  args.base.m = (int32_t)m;
+  args.base.n = (int32_t)f;
+  args.base.k = (int32_t)k;
+  args.base.num_groups = groups;
+  args.base.m_indices = mode == kContiguous ? rows : nullptr;
+  args.base.masked_m = mode == kMasked ? rows : nullptr;
+  args.base.band = raster_band(args.base.m_blocks, kBlockM, k);
+  args.base.timeout_ns = g_timeout_ns.load();
+  args.base.pdl = g_pdl.load();
+  args.base.debug_drop_load = mode == kDense ? g_debug_drop_load.load() : 0;
+  args.h = h_sf ? nullptr : static_cast<__nv_bfloat16*>(h);
+  args.hq = h_sf ? static_cast<uint8_t*>(h) : nullptr;
+  args.hsf = reinterpret_cast<uint32_t*>(h_sf);
+  args.cq = static_cast<uint8_t*>(gu);
+  args.csf = reinterpret_cast<uint32_t*>(gu_sf);
+  args.ldh = ldh;
+  args.f = (int32_t)f;
+  args.m_pad = (int32_t)align4(m);
+  args.activation = activation;
+  const int64_t most = mode == kMasked ? tiles * groups : tiles;
+  const int grid = (int)(most < sms ? most : sms);
+  print_config(name, m, f, k, groups, kBlockM, 128, 4, grid, args.base.band);
+  return from_cuda(gated_gemm_launch(mode, o.a, o.b, o.sfa, o.sfb, args, grid, static_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_fp8_gated_gemm_nt(const void* a, const int32_t* sfa, const void* b, const int32_t* sfb,
+                               void* h, int32_t* h_sf, void* gu, int32_t* gu_sf, int64_t m, int64_t f,
+                               int64_t k, int64_t lda, int64_t ldb, int64_t ldh, int32_t activation,
+                               void* stream) {
+  return gated_gemm(kDense, "fp8_gated_gemm_nt", a, sfa, b, sfb, h, h_sf, gu, gu_sf, nullptr, m, f, k, lda, ldb,
+                    ldh, 1, activation, stream);
+}
+
+dg_status dg_m_grouped_fp8_gated_gemm_nt_contiguous(const void* a, const int32_t* sfa, const void* b,
+                                                    const int32_t* sfb, void* h, int32_t* h_sf,
+                                                    void* gu, int32_t* gu_sf, const int32_t* m_indices,
+                                                    int64_t m_sum, int64_t f, int64_t k,
+                                                    int32_t num_groups, int32_t activation,
+                                                    void* stream) {
+  return gated_gemm(kContiguous, "m_grouped_fp8_gated_gemm_nt_contiguous", a, sfa, b, sfb, h, h_sf, gu, gu_sf,
+                    m_indices, m_sum, f, k, k, k, f, num_groups, activation, stream);
+}
+
+dg_status dg_m_grouped_fp8_gated_gemm_nt_masked(const void* a, const int32_t* sfa, const void* b,
+                                                const int32_t* sfb, void* h, int32_t* h_sf,
+                                                const int32_t* masked_m, int32_t num_groups,
+                                                int64_t max_m, int64_t f, int64_t k,
+                                                int64_t expected_m, int32_t activation, void* stream) {
+  if (expected_m < 0) return DG_ERR_INVALID_ARG;
+  return gated_gemm(kMasked, "m_grouped_fp8_gated_gemm_nt_masked", a, sfa, b, sfb, h, h_sf, nullptr, nullptr,
+                    masked_m, max_m, f, k, k, k, f, num_groups, activation, stream);
 }
 
 dg_status dg_fp8_gated_backward(const void* dh, int64_t lddh, const void* gu, const int32_t* gu_sf,

@@ -122,6 +122,128 @@ def _cols_out(out, rows128, cols, device, name):
 # ---------------------------------------------------------------- gated product
 
 
+class GatedOutput(NamedTuple):
+    """Results of the gated products."""
+    h: torch.Tensor                         # BF16, or E4M3 codes
+    h_sf: Optional[torch.Tensor]            # packed 1x128 row-group scales of the codes, else None
+    checkpoint: Optional[torch.Tensor]      # E4M3 codes of [g | u] with checkpoint=True, else None
+    checkpoint_sf: Optional[torch.Tensor]   # their packed scales
+
+
+def _gated_out(d, checkpoint, out_format, lead, f, device):
+    """The tensors a gated product writes: rows `lead` + (m,), the caller's or new ones."""
+    m = lead[-1]
+    groups = lead[0] if len(lead) == 2 else None
+    if out_format == "fp8":
+        h, h_sf = _codes_out(d, lead + (f,), sf_packed_shape(m, f, groups), device, "d")
+    elif out_format == "bf16":
+        h, h_sf = d, None
+        if h is None:
+            h = torch.empty(lead + (f,), dtype=torch.bfloat16, device=device)
+        _need(h, "d", (torch.bfloat16,), len(lead) + 1)
+        if tuple(h.shape) != lead + (f,) or h.stride(-1) != 1:
+            raise ValueError("d must be %s with unit column stride" % (lead + (f,),))
+    else:
+        raise ValueError("out_format %r not in ('bf16', 'fp8')" % (out_format,))
+    if (h_sf is not None or checkpoint) and f % 128:
+        raise ValueError("8-bit results need F %% 128 == 0, got %d" % f)
+    gu = gu_sf = None
+    if checkpoint:
+        gu, gu_sf = _codes_out(None if checkpoint is True else checkpoint, lead + (2 * f,),
+                               sf_packed_shape(m, 2 * f, groups), device, "checkpoint")
+    return h, h_sf, gu, gu_sf
+
+
+def _gated_operands(a, sfa, b, sfb, lead_dims):
+    _need(a, "a", FP8_DTYPES, lead_dims + 1)
+    _need(sfa, "sfa", (torch.int32,), lead_dims + 1)
+    k = a.shape[-1]
+    n = b.shape[-2]
+    if b.shape[-1] != k or n % 2:
+        raise ValueError("b must be [.., 2F, %d], got %s" % (k, tuple(b.shape)))
+    ga = a.shape[0] if lead_dims == 2 else None
+    gb = b.shape[0] if b.dim() == 3 else None
+    if tuple(sfa.shape) != sf_packed_shape(a.shape[-2], k, ga) or tuple(sfb.shape) != sf_packed_shape(n, k, gb):
+        raise ValueError("scale shapes %s / %s, expected %s / %s" % (
+            tuple(sfa.shape), tuple(sfb.shape), sf_packed_shape(a.shape[-2], k, ga), sf_packed_shape(n, k, gb)))
+    _contiguous(sfa=sfa, sfb=sfb)
+    return n // 2, k
+
+
+def fp8_gated_gemm_nt(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor, d=None,
+                      activation: str = "silu", out_format: str = "bf16", checkpoint=False,
+                      stream=None) -> GatedOutput:
+    """h = act(A Wg^T) * (A Wu^T) in one kernel: A [M, K] and B = [Wg; Wu]
+    [2F, K] E4M3 with packed UE8M0 scales (as fp8_gemm_nt's).
+
+    activation "silu" or "gelu_tanh".  out_format "bf16": h BF16 [M, F]
+    (F % 8 == 0); "fp8": h as E4M3 codes with packed 1x128 row-group scales,
+    the next GEMM's operand (F % 128 == 0).  checkpoint=True also keeps
+    [g | u] in 8 bits for fp8_gated_backward (F % 128 == 0).  d, checkpoint:
+    preallocated results (a BF16 tensor, or (codes, scales))."""
+    act = _activation(activation)
+    _need(b, "b", FP8_DTYPES, 2)
+    _need(sfb, "sfb", (torch.int32,), 2)
+    f, k = _gated_operands(a, sfa, b, sfb, 1)
+    m = a.shape[0]
+    if a.stride(1) != 1 or b.stride(1) != 1:
+        raise ValueError("a and b need unit stride along K")
+    h, h_sf, gu, gu_sf = _gated_out(d, checkpoint, out_format, (m,), f, a.device)
+    _on_current_device(stream, a, sfa, b, sfb, h, h_sf, gu, gu_sf)
+    _check(_lib.lib().dg_fp8_gated_gemm_nt(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(h), _ptr(h_sf), _ptr(gu),
+                                           _ptr(gu_sf), m, f, k, a.stride(0) if m > 1 else k, b.stride(0),
+                                           h.stride(0) if m > 1 else f, act, _stream(stream)),
+           "dg_fp8_gated_gemm_nt")
+    return GatedOutput(h, h_sf, gu, gu_sf)
+
+
+def m_grouped_fp8_gated_gemm_nt_contiguous(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor,
+                                           m_indices: torch.Tensor, d=None, activation: str = "silu",
+                                           out_format: str = "bf16", checkpoint=False,
+                                           stream=None) -> GatedOutput:
+    """fp8_gated_gemm_nt for the experts of the contiguous layout: rows of A
+    [m_sum, K] routed to B [G, 2F, K] by m_indices (-1 = padding: those rows
+    of the results are left as they are)."""
+    act = _activation(activation)
+    _need(b, "b", FP8_DTYPES, 3)
+    _need(sfb, "sfb", (torch.int32,), 3)
+    f, k = _gated_operands(a, sfa, b, sfb, 1)
+    _need(m_indices, "m_indices", (torch.int32,), 1)
+    _row_index(m_indices, a.shape[0])
+    _contiguous(a=a, b=b)
+    h, h_sf, gu, gu_sf = _gated_out(d, checkpoint, out_format, (a.shape[0],), f, a.device)
+    _contiguous(d=h)
+    _on_current_device(stream, a, sfa, b, sfb, m_indices, h, h_sf, gu, gu_sf)
+    _check(_lib.lib().dg_m_grouped_fp8_gated_gemm_nt_contiguous(
+        _ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(h), _ptr(h_sf), _ptr(gu), _ptr(gu_sf), _ptr(m_indices),
+        a.shape[0], f, k, b.shape[0], act, _stream(stream)), "dg_m_grouped_fp8_gated_gemm_nt_contiguous")
+    return GatedOutput(h, h_sf, gu, gu_sf)
+
+
+def m_grouped_fp8_gated_gemm_nt_masked(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor,
+                                       masked_m: torch.Tensor, expected_m: int = 0, d=None,
+                                       activation: str = "silu", out_format: str = "bf16",
+                                       stream=None) -> GatedOutput:
+    """fp8_gated_gemm_nt for the masked layout: A [G, max_m, K] x B [G, 2F, K];
+    rows at or past masked_m[g] (read on the device) are left as they are."""
+    act = _activation(activation)
+    _need(b, "b", FP8_DTYPES, 3)
+    _need(sfb, "sfb", (torch.int32,), 3)
+    f, k = _gated_operands(a, sfa, b, sfb, 2)
+    _need(masked_m, "masked_m", (torch.int32,), 1)
+    g, max_m = a.shape[:2]
+    if b.shape[0] != g or masked_m.numel() != g:
+        raise ValueError("shape mismatch")
+    _contiguous(a=a, b=b, masked_m=masked_m)
+    h, h_sf, _, _ = _gated_out(d, False, out_format, (g, max_m), f, a.device)
+    _contiguous(d=h)
+    _on_current_device(stream, a, sfa, b, sfb, masked_m, h, h_sf)
+    _check(_lib.lib().dg_m_grouped_fp8_gated_gemm_nt_masked(
+        _ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(h), _ptr(h_sf), _ptr(masked_m), g, max_m, f, k,
+        int(expected_m), act, _stream(stream)), "dg_m_grouped_fp8_gated_gemm_nt_masked")
+    return GatedOutput(h, h_sf, None, None)
+
+
 class GatedGradients(NamedTuple):
     """fp8_gated_backward's results, E4M3 codes and packed scales each."""
     q: torch.Tensor          # [dg | du] [M, 2F], 1x128 row groups: dX = q @ W (fp8_gemm_nn)
