@@ -13,6 +13,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "dg_device.cuh"
 #include "dg_ops.cuh"
 
@@ -46,11 +48,11 @@ __global__ void __launch_bounds__(256) save_rows_kernel(const __nv_bfloat16* __r
     for (int t = 0; t < 4; ++t) {
       if (4 * j + t >= kblocks) break;
       const float a = bf16_lo(v[t].x), b = bf16_hi(v[t].x), c = bf16_lo(v[t].y), d = bf16_hi(v[t].y);
-      const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits_max4(a, b, c, d));
-      const int e = scale_exponent(__uint_as_float(m));
-      const float inv = pow2f(-e);
+      const float m = abs_max2(abs_max2(0.0f, make_float2(a, b)), make_float2(c, d));
+      const uint32_t e = scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
+      const float inv = inverse_of_byte(e);
       *reinterpret_cast<uint32_t*>(q + at + t * 128) = e4m3x4(a * inv, b * inv, c * inv, d * inv);
-      word |= (uint32_t)(e + 127) << (8 * t);
+      word |= e << (8 * t);
     }
   }
   if (lane == 0) sf[(g * kpacks + j) * rows_pad + r] = word;
@@ -88,61 +90,138 @@ __global__ void __launch_bounds__(256) restore_rows_kernel(const uint8_t* __rest
   }
 }
 
-// One CTA per 128 x 128 tile, 512 threads: warp w holds rows 8w .. 8w+7, lane
-// l columns 4l .. 4l+3.  Column maxima go through shared memory once.
-__global__ void __launch_bounds__(512) use_cols_kernel(const uint8_t* __restrict__ q,
-                                                       const uint32_t* __restrict__ sf,
-                                                       const int32_t* __restrict__ m_indices,
-                                                       uint8_t* __restrict__ qc,
-                                                       uint32_t* __restrict__ sfc, int64_t rows,
-                                                       int64_t rows_pad, int64_t cols, int rblocks) {
-  __shared__ uint4 cmax[16][32];
-  __shared__ float4 cinv[32];
+// Persistent CTAs of 4 warps, kUseCtas a SM, over 128 x 128 tiles.  Warp w
+// holds rows 32w .. 32w+31: lane l columns 16 (l % 8) .. +15 (one 16-byte
+// access) of rows 4i + l / 8.  The next tiles are on their way into shared
+// memory while one is worked on (rows that count as zero are filled with zeros
+// instead of being read).  The codes are read from there and decoded twice, for
+// the columns' maxima and to encode them.
+constexpr int kUseRing = 3;
+constexpr int kUseCtas = 4;
+
+struct UseShared {
+  uint4 codes[kUseRing][8][128];
+  uint32_t words[kUseRing][128];  // the rows' scale words
+  float cmax[4][128];
+  float cinv[128];
+};
+
+__global__ void __launch_bounds__(128, kUseCtas) use_cols_kernel(const uint8_t* __restrict__ q,
+                                                          const uint32_t* __restrict__ sf,
+                                                          const int32_t* __restrict__ m_indices,
+                                                          uint8_t* __restrict__ qc,
+                                                          uint32_t* __restrict__ sfc, int64_t rows,
+                                                          int64_t rows_pad, int64_t cols, int kblocks,
+                                                          int rblocks) {
+  extern __shared__ uint4 smem[];
+  UseShared& sh = *reinterpret_cast<UseShared*>(smem);
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int kblocks = (int)(cols / 128);
-  const int rb = blockIdx.x / kblocks, kb = blockIdx.x % kblocks;
-  const int64_t row0 = (int64_t)rb * 128 + warp * 8;
-  const int64_t col = (int64_t)kb * 128 + lane * 4;
-  float v[8][4];
-  uint4 m = make_uint4(0, 0, 0, 0);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tiles = kblocks * rblocks;
+  // Which of the warp's 32 rows hold data, bit l for row 32 warp + l.
+  auto fetch = [&](int t, int s, uint32_t& live) {
+    live = 0;
+    if (t < tiles) {
+      const int rb = t / kblocks, kb = t % kblocks;
+      const int64_t row = (int64_t)rb * 128 + warp * 32 + lane;
+      const bool in = row < rows && (!m_indices || __ldg(m_indices + row) >= 0);
+      live = __ballot_sync(0xffffffffu, in);
+      cp_async4_or_zero(&sh.words[s][tid], in ? sf + (int64_t)(kb >> 2) * rows_pad + row : sf, in);
+      const uint8_t* src = q + ((int64_t)rb * 128 + warp * 32 + lane / 8) * cols + (int64_t)kb * 128 + (lane % 8) * 16;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = row0 + i;
-    const bool live = r < rows && (!m_indices || __ldg(m_indices + r) >= 0);
-    uint32_t codes = 0;
-    float s = 0.0f;
-    if (live) {
-      codes = __ldg(reinterpret_cast<const uint32_t*>(q + r * cols + col));
-      s = scale_of_byte((__ldg(sf + (int64_t)(kb >> 2) * rows_pad + r) >> (8 * (kb & 3))) & 0xFFu);
+      for (int i = 0; i < 8; ++i) {
+        const bool on = live >> (4 * i + lane / 8) & 1;
+        cp_async16_or_zero(&sh.codes[s][i][tid], on ? src : q, on);
+        src += 4 * cols;
+      }
     }
-    e4m3x4_to_float(codes, v[i]);
+    cp_async_commit();
+  };
+  uint32_t live[kUseRing];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[i][c] *= s;
-    m.x = max(m.x, abs_bits(v[i][0]));
-    m.y = max(m.y, abs_bits(v[i][1]));
-    m.z = max(m.z, abs_bits(v[i][2]));
-    m.w = max(m.w, abs_bits(v[i][3]));
+  for (int s = 0; s < kUseRing - 1; ++s) fetch(blockIdx.x + s * gridDim.x, s, live[s]);
+  int at = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int rb = t / kblocks, kb = t % kblocks;
+    fetch(t + (kUseRing - 1) * gridDim.x, at == 0 ? kUseRing - 1 : at - 1, live[kUseRing - 1]);
+    cp_async_wait<kUseRing - 1>();
+    __syncwarp();  // a warp's scale words are copied by its own lanes
+    auto row_scale = [&](int i) {
+      const uint32_t w = sh.words[at][warp * 32 + 4 * i + lane / 8];
+      return (live[0] >> (4 * i + lane / 8) & 1) ? scale_of_byte((w >> (8 * (kb & 3))) & 0xFFu) : 0.0f;
+    };
+    float m[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) m[c] = 0.0f;
+#pragma unroll 2
+    for (int i = 0; i < 8; i += 2) {
+      const uint4 c0 = sh.codes[at][i][tid], c1 = sh.codes[at][i + 1][tid];
+      const float s0 = row_scale(i), s1 = row_scale(i + 1);
+      const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float f0[4], f1[4];
+        e4m3x4_to_float(w0[c], f0);
+        e4m3x4_to_float(w1[c], f1);
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const float2 a = mul2(make_float2(f0[k], f0[k + 1]), s0);
+          const float2 b = mul2(make_float2(f1[k], f1[k + 1]), s1);
+          m[4 * c + k] = fmaxf(fmaxf(m[4 * c + k], fabsf(a.x)), fabsf(b.x));
+          m[4 * c + k + 1] = fmaxf(fmaxf(m[4 * c + k + 1], fabsf(a.y)), fabsf(b.y));
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], 8));
+      m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], 16));
+    }
+    if (lane < 8) {
+#pragma unroll
+      for (int c = 0; c < 16; c += 4)
+        *reinterpret_cast<float4*>(&sh.cmax[warp][lane * 16 + c]) = make_float4(m[c], m[c + 1], m[c + 2], m[c + 3]);
+    }
+    __syncthreads();
+    {
+      const float a = fmaxf(fmaxf(sh.cmax[0][tid], sh.cmax[1][tid]), fmaxf(sh.cmax[2][tid], sh.cmax[3][tid]));
+      const uint32_t b = scale_byte(a);
+      sh.cinv[tid] = inverse_of_byte(b);
+      store_scale_byte(sfc + (int64_t)(rb >> 2) * cols + (int64_t)kb * 128 + tid, rb, rb == rblocks - 1, b);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 16; c += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&sh.cinv[(lane % 8) * 16 + c]);
+      m[c] = x.x;
+      m[c + 1] = x.y;
+      m[c + 2] = x.z;
+      m[c + 3] = x.w;
+    }
+    uint8_t* dst = qc + ((int64_t)rb * 128 + warp * 32 + lane / 8) * cols + (int64_t)kb * 128 + (lane % 8) * 16;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const uint4 ci = sh.codes[at][i][tid];
+      const float si = row_scale(i);
+      uint32_t w[4] = {ci.x, ci.y, ci.z, ci.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float f[4];
+        e4m3x4_to_float(w[c], f);
+        const float2 a = mul2(mul2(make_float2(f[0], f[1]), si), make_float2(m[4 * c], m[4 * c + 1]));
+        const float2 b = mul2(mul2(make_float2(f[2], f[3]), si), make_float2(m[4 * c + 2], m[4 * c + 3]));
+        w[c] = e4m3x4(a, b);
+      }
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      dst += 4 * cols;
+    }
+    __syncwarp();  // every lane has read its words before the slot is filled again
+    if (++at == kUseRing) at = 0;
+#pragma unroll
+    for (int k = 0; k < kUseRing - 1; ++k) live[k] = live[k + 1];
   }
-  cmax[warp][lane] = m;
-  __syncthreads();
-  if (threadIdx.x < 128) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(&cmax[0][0]) + threadIdx.x;
-    uint32_t a = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) a = max(a, p[w * 128]);
-    const int e = scale_exponent(__uint_as_float(a));
-    reinterpret_cast<float*>(cinv)[threadIdx.x] = pow2f(-e);
-    store_scale_byte(sfc + (int64_t)(rb >> 2) * cols + (int64_t)kb * 128 + threadIdx.x, rb, rb == rblocks - 1,
-                     (uint32_t)(e + 127));
-  }
-  __syncthreads();
-  const float4 inv = cinv[lane];
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    *reinterpret_cast<uint32_t*>(qc + (row0 + i) * cols + col) =
-        e4m3x4(v[i][0] * inv.x, v[i][1] * inv.y, v[i][2] * inv.z, v[i][3] * inv.w);
+  cp_async_wait<0>();
 }
 
 }  // namespace
@@ -170,11 +249,16 @@ cudaError_t restore_rows_launch(const void* q, const void* sf, void* x, int dtyp
 }
 
 cudaError_t use_cols_launch(const void* q, const void* sf, const int32_t* m_indices, void* qc,
-                            void* sfc, int64_t rows, int64_t cols, bool pdl, cudaStream_t stream) {
-  const int rblocks = (int)((rows + 127) / 128);
-  return launch_op(use_cols_kernel, dim3((unsigned)(cols / 128 * rblocks)), 512, 0, pdl, stream,
-                   (const uint8_t*)q, (const uint32_t*)sf, m_indices, (uint8_t*)qc, (uint32_t*)sfc, rows,
-                   (rows + 3) / 4 * 4, cols, rblocks);
+                            void* sfc, int64_t rows, int64_t cols, int sms, bool pdl,
+                            cudaStream_t stream) {
+  const int rblocks = (int)((rows + 127) / 128), kblocks = (int)(cols / 128);
+  const int64_t tiles = (int64_t)rblocks * kblocks;
+  const dim3 grid((unsigned)std::min<int64_t>(tiles, (int64_t)kUseCtas * sms));
+  cudaError_t e = set_smem(use_cols_kernel, sizeof(UseShared));
+  if (e != cudaSuccess) return e;
+  return launch_op(use_cols_kernel, grid, 128, sizeof(UseShared), pdl, stream, (const uint8_t*)q,
+                   (const uint32_t*)sf, m_indices, (uint8_t*)qc, (uint32_t*)sfc, rows, (rows + 3) / 4 * 4, cols,
+                   kblocks, rblocks);
 }
 
 }  // namespace dg

@@ -239,13 +239,14 @@ cudaError_t save_rows_launch(const void* x, void* q, void* sf, int64_t groups, i
 cudaError_t restore_rows_launch(const void* q, const void* sf, void* x, int dtype, int64_t groups,
                                 int64_t rows, int64_t cols, bool pdl, cudaStream_t stream);
 cudaError_t use_cols_launch(const void* q, const void* sf, const int32_t* m_indices, void* qc,
-                            void* sfc, int64_t rows, int64_t cols, bool pdl, cudaStream_t stream);
+                            void* sfc, int64_t rows, int64_t cols, int sms, bool pdl,
+                            cudaStream_t stream);
 
 // gated_backward.cu
 cudaError_t gated_backward_launch(const void* dh, int64_t lddh, const void* gu, const void* gu_sf,
                                   const int32_t* m_indices, void* q, void* sf, void* qc, void* sfc,
-                                  void* hc, void* hsfc, int64_t m, int64_t f, int activation, bool pdl,
-                                  cudaStream_t stream);
+                                  void* hc, void* hsfc, int64_t m, int64_t f, int activation, int sms,
+                                  bool pdl, cudaStream_t stream);
 
 // layer_norm.cu
 cudaError_t layer_norm_launch(const void* x, int dtype, const void* weight, const void* bias,

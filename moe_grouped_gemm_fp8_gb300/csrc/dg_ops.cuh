@@ -19,6 +19,38 @@ __device__ __forceinline__ uint2 ld_stream_u2(const void* p) {
   return v;
 }
 
+__device__ __forceinline__ uint4 ld_stream_u4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Asynchronous 16-byte copy into shared memory, past L1, in groups.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// The same with zeros in the place of the source where `live` is false (the
+// source is not read).
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async8_or_zero(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4_or_zero(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
@@ -53,6 +85,34 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t codes, float (&f)[4]) {
   f[3] = b.y;
 }
 
+// scale_exponent(amax) + 127 for a finite amax, without branches: adding
+// 0x1FFFFF carries into the exponent exactly when the fraction is above 1.75.
+__device__ __forceinline__ uint32_t scale_byte(float amax) {
+  const int t = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 8;
+  return amax > 0.0f ? (uint32_t)max(t, 0) : 127u;
+}
+// 2^(127 - byte), the factor that brings a group into E4M3's range (byte <= 253).
+__device__ __forceinline__ float inverse_of_byte(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Pairs of FP32 (one instruction for two).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float b) { return __fmul2_rn(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float abs_max2(float m, float2 a) { return fmaxf(fmaxf(m, fabsf(a.x)), fabsf(a.y)); }
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+  return (uint32_t)cvt_e4m3x2(a.x, a.y) | ((uint32_t)cvt_e4m3x2(b.x, b.y) << 16);
+}
+// Two FP32 sums over the warp in one butterfly: lanes 0-15 end with a's, lanes
+// 16-31 with b's.
+__device__ __forceinline__ float warp_sum2(float a, float b) {
+  const bool hi = (threadIdx.x & 16) != 0;
+  float v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // UE8M0 byte -> its scale 2^(b - 127) (b = 0: 2^-127, a subnormal).
 __device__ __forceinline__ float scale_of_byte(uint32_t b) { return pow2f((int)b - 127); }
 
@@ -66,11 +126,23 @@ __device__ __forceinline__ void store_scale_byte(uint32_t* word, int block, bool
     for (int i = t + 1; i < 4; ++i) p[i] = 0;
 }
 
+// The hardware's base-2 exponential and reciprocal (about 2^-22 relative each).
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // act(g) and act'(g).  The logistic function uses the fast exponential and
 // reciprocal: together about 2^-21 relative, well below the 2^-9 (BF16) or
 // 2^-4 (E4M3) at which every result of these kernels is rounded.  For large
 // negative g exp(-g) is inf and s is 0, so silu and its derivative are 0.
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+__device__ __forceinline__ float logistic(float z) { return rcp_approx(1.0f + exp2_approx(z * -1.4426950408889634f)); }
 
 // silu(g) = g s with s = logistic(g); its derivative s + g s (1 - s).
 // gelu in its tanh form, g (1 + tanh t) / 2 with t = c (g + 0.044715 g^3),
@@ -96,6 +168,36 @@ __device__ __forceinline__ void gate_act_grad(float g, float& a, float& da) {
     constexpr float c2 = 1.5957691216057308f;
     da = s + a * (1.0f - s) * (c2 + (3.0f * c2 * 0.044715f) * g * g);
   }
+}
+
+// The same for a pair: a and act'.
+template <int ACT>
+__device__ __forceinline__ void gate_act_grad2(float2 g, float2& a, float2& da) {
+  float2 z = g;  // logistic's argument times -log2(e)
+  float2 dz = make_float2(1.0f, 1.0f);
+  constexpr float kLog2e = 1.4426950408889634f;
+  if constexpr (ACT == DG_ACT_SILU) {
+    z = mul2(g, -kLog2e);
+  } else {
+    constexpr float c2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    const float2 gg = mul2(g, g);
+    z = mul2(mul2(g, -kLog2e), fma2(gg, make_float2(c2 * 0.044715f, c2 * 0.044715f), make_float2(c2, c2)));
+    dz = fma2(gg, make_float2(3.0f * c2 * 0.044715f, 3.0f * c2 * 0.044715f), make_float2(c2, c2));
+  }
+  const float2 q = add2(make_float2(exp2_approx(z.x), exp2_approx(z.y)), make_float2(1.0f, 1.0f));
+  const float2 s = make_float2(rcp_approx(q.x), rcp_approx(q.y));
+  a = mul2(g, s);
+  float2 t = fma2(s, make_float2(-1.0f, -1.0f), make_float2(1.0f, 1.0f));
+  if constexpr (ACT != DG_ACT_SILU) t = mul2(t, dz);
+  da = fma2(a, t, s);
+}
+
+// Raises a kernel's dynamic shared-memory limit where it needs more than 48 KB.
+// Set on every such launch: the call only writes a field of the function's state.
+template <class Kern>
+static cudaError_t set_smem(Kern kern, size_t smem) {
+  if (smem <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
 // Launches with programmatic stream serialisation when pdl is set.

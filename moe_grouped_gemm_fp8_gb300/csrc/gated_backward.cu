@@ -33,108 +33,205 @@ struct GatedBackwardArgs {
   int fblocks, rblocks;
 };
 
-// One CTA of 16 warps per 128 x 128 tile of h: warp w holds rows 8w .. 8w+7,
-// lane l columns 4l .. 4l+3, so a row group's maximum is one warp reduction
-// and a column's maximum is 8 values in registers and one exchange through
-// shared memory.
+// Persistent CTAs of 16 warps, one a SM, over 128 x 128 tiles of h.  Warp w
+// holds rows 8w .. 8w+7, lane l columns 4l .. 4l+3: a row group's maximum is
+// one warp reduction, a column's 8 values in registers and one exchange
+// through shared memory, and dg, du and h (96 values a thread) stay in
+// registers from the arithmetic to the five stores.  The tile after next is on
+// its way into shared memory meanwhile; each thread copies and reads only its
+// own pieces, so no barrier guards them, and rows that count as zero are
+// filled with zeros instead of being read.
+//
+// Bound by HBM (4 bytes in and 5 out an element of h) as long as an element
+// costs no more than about 50 instructions, so arithmetic goes in pairs, and a
+// warp's 16 row scales are worked out by 16 lanes at once.
+constexpr int kBackRing = 3;
+constexpr int kBackThreads = 512;
+
+struct BackStage {
+  uint2 dh[8][kBackThreads];
+  uint32_t g[8][kBackThreads];
+  uint32_t u[8][kBackThreads];
+};
+struct BackShared {
+  BackStage stage[kBackRing];
+  float4 cmax[3][16][32];
+  float4 cinv[3][32];
+};
+
 template <int ACT>
-__global__ void __launch_bounds__(512) gated_backward_kernel(const GatedBackwardArgs p) {
-  __shared__ uint4 cmax[3][16][32];
-  __shared__ float4 cinv[3][32];
+__global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const GatedBackwardArgs p) {
+  extern __shared__ uint4 smem[];
+  BackShared& sh = *reinterpret_cast<BackShared*>(smem);
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int rb = blockIdx.x / p.fblocks, fb = blockIdx.x % p.fblocks;
-  const int64_t row0 = (int64_t)rb * 128 + warp * 8;
-  const int64_t col = (int64_t)fb * 128 + lane * 4;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int64_t m_pad = (p.m + 3) / 4 * 4;
-  const int kg = fb, ku = p.fblocks + fb;  // column blocks of g and u in [g | u]
-  float dg[8][4], du[8][4], h[8][4];
-  uint32_t mg[4] = {}, mu[4] = {}, mh[4] = {};
+  const int tiles = p.fblocks * p.rblocks;
+  const int64_t f2 = 2 * p.f;
+
+  // Rows of the warp that hold data, bit i for row 8 warp + i.
+  auto live_rows = [&](int64_t row0) {
+    const int64_t r = row0 + lane;
+    const bool in = lane < 8 && r < p.m && (!p.m_indices || __ldg(p.m_indices + r) >= 0);
+    return __ballot_sync(0xffffffffu, in);
+  };
+  // Lanes 0-7 / 8-15: the scale of g / u in the warp's row (lane % 8), 0 where it counts as zero.
+  auto row_scale = [&](int64_t row0, int fb, uint32_t live) {
+    float s = 0.0f;
+    if (lane < 16 && (live >> (lane & 7) & 1)) {
+      const int k = lane < 8 ? fb : p.fblocks + fb;
+      const uint32_t w = __ldg(p.gu_sf + (int64_t)(k >> 2) * m_pad + row0 + (lane & 7));
+      s = scale_of_byte((w >> (8 * (k & 3))) & 0xFFu);
+    }
+    return s;
+  };
+  auto fetch = [&](int t, int s, uint32_t& live, float& scale) {
+    live = 0;
+    scale = 0.0f;
+    if (t < tiles) {
+      const int rb = t / p.fblocks, fb = t % p.fblocks;
+      const int64_t row0 = (int64_t)rb * 128 + warp * 8;
+      live = live_rows(row0);
+      scale = row_scale(row0, fb, live);
+      const int64_t col = (int64_t)fb * 128 + lane * 4;
+      const __nv_bfloat16* d = p.dh + row0 * p.lddh + col;
+      const uint8_t* c = p.gu + row0 * f2 + col;
+      BackStage& st = sh.stage[s];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = row0 + i;
-    uint2 dhv = make_uint2(0u, 0u);
-    uint32_t gc = 0u, uc = 0u;
-    float sg = 0.0f, su = 0.0f;
-    if (r < p.m && (!p.m_indices || __ldg(p.m_indices + r) >= 0)) {
-      dhv = ld_stream_u2(p.dh + r * p.lddh + col);
-      gc = __ldg(reinterpret_cast<const uint32_t*>(p.gu + r * 2 * p.f + col));
-      uc = __ldg(reinterpret_cast<const uint32_t*>(p.gu + r * 2 * p.f + p.f + col));
-      sg = scale_of_byte((__ldg(p.gu_sf + (int64_t)(kg >> 2) * m_pad + r) >> (8 * (kg & 3))) & 0xFFu);
-      su = scale_of_byte((__ldg(p.gu_sf + (int64_t)(ku >> 2) * m_pad + r) >> (8 * (ku & 3))) & 0xFFu);
+      for (int i = 0; i < 8; ++i) {
+        const bool in = live >> i & 1;
+        cp_async8_or_zero(&st.dh[i][tid], in ? d : p.dh, in);
+        cp_async4_or_zero(&st.g[i][tid], in ? c : p.gu, in);
+        cp_async4_or_zero(&st.u[i][tid], in ? c + p.f : p.gu, in);
+        d += p.lddh;
+        c += f2;
+      }
     }
-    const float d[4] = {bf16_lo(dhv.x), bf16_hi(dhv.x), bf16_lo(dhv.y), bf16_hi(dhv.y)};
-    float g[4], u[4];
-    e4m3x4_to_float(gc, g);
-    e4m3x4_to_float(uc, u);
-    uint32_t rg = 0, ru = 0;
+    cp_async_commit();
+  };
+
+  // live rows and scales of the tiles in flight, oldest first
+  uint32_t live[kBackRing];
+  float scale[kBackRing];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float a, da;
-      gate_act_grad<ACT>(g[c] * sg, a, da);
-      const float uu = u[c] * su;
-      dg[i][c] = d[c] * uu * da;
-      du[i][c] = d[c] * a;
-      h[i][c] = a * uu;
-      const uint32_t bg = abs_bits(dg[i][c]), bu = abs_bits(du[i][c]);
-      rg = max(rg, bg);
-      ru = max(ru, bu);
-      mg[c] = max(mg[c], bg);
-      mu[c] = max(mu[c], bu);
-      mh[c] = max(mh[c], abs_bits(h[i][c]));
+  for (int s = 0; s < kBackRing - 1; ++s) fetch(blockIdx.x + s * gridDim.x, s, live[s], scale[s]);
+  int at = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    fetch(t + (kBackRing - 1) * gridDim.x, at == 0 ? kBackRing - 1 : at - 1, live[kBackRing - 1],
+          scale[kBackRing - 1]);
+    cp_async_wait<kBackRing - 1>();
+    const int rb = t / p.fblocks, fb = t % p.fblocks;
+    const int64_t row0 = (int64_t)rb * 128 + warp * 8;
+    const int64_t col = (int64_t)fb * 128 + lane * 4;
+    const BackStage& st = sh.stage[at];
+    if (++at == kBackRing) at = 0;
+
+    float2 dg[8][2], du[8][2], h[8][2];
+    float mg[4] = {}, mu[4] = {}, mh[4] = {};
+    float rowmax = 0.0f;  // lanes 0-7: of dg in the row (lane % 8); lanes 8-15: of du
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float sg = __shfl_sync(0xffffffffu, scale[0], i), su = __shfl_sync(0xffffffffu, scale[0], 8 + i);
+      const uint2 dv = st.dh[i][tid];
+      float g[4], u[4];
+      e4m3x4_to_float(st.g[i][tid], g);
+      e4m3x4_to_float(st.u[i][tid], u);
+      const float2 d[2] = {make_float2(bf16_lo(dv.x), bf16_hi(dv.x)), make_float2(bf16_lo(dv.y), bf16_hi(dv.y))};
+      float rg = 0.0f, ru = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float2 a, da;
+        gate_act_grad2<ACT>(mul2(make_float2(g[2 * c], g[2 * c + 1]), sg), a, da);
+        const float2 uu = mul2(make_float2(u[2 * c], u[2 * c + 1]), su);
+        dg[i][c] = mul2(mul2(d[c], uu), da);
+        du[i][c] = mul2(d[c], a);
+        h[i][c] = mul2(a, uu);
+        rg = abs_max2(rg, dg[i][c]);
+        ru = abs_max2(ru, du[i][c]);
+      }
+      rg = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rg)));
+      ru = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(ru)));
+      if (lane == i) rowmax = rg;
+      if (lane == 8 + i) rowmax = ru;
     }
-    const int eg = scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, rg)));
-    const int eu = scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, ru)));
-    if (r < p.m) {
-      const float ig = pow2f(-eg), iu = pow2f(-eu);
-      uint8_t* qr = p.q + r * 2 * p.f + col;
-      *reinterpret_cast<uint32_t*>(qr) = e4m3x4(dg[i][0] * ig, dg[i][1] * ig, dg[i][2] * ig, dg[i][3] * ig);
-      *reinterpret_cast<uint32_t*>(qr + p.f) = e4m3x4(du[i][0] * iu, du[i][1] * iu, du[i][2] * iu, du[i][3] * iu);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mg[2 * c] = fmaxf(fmaxf(mg[2 * c], fabsf(dg[i][c].x)), fabsf(dg[i + 1][c].x));
+        mg[2 * c + 1] = fmaxf(fmaxf(mg[2 * c + 1], fabsf(dg[i][c].y)), fabsf(dg[i + 1][c].y));
+        mu[2 * c] = fmaxf(fmaxf(mu[2 * c], fabsf(du[i][c].x)), fabsf(du[i + 1][c].x));
+        mu[2 * c + 1] = fmaxf(fmaxf(mu[2 * c + 1], fabsf(du[i][c].y)), fabsf(du[i + 1][c].y));
+        mh[2 * c] = fmaxf(fmaxf(mh[2 * c], fabsf(h[i][c].x)), fabsf(h[i + 1][c].x));
+        mh[2 * c + 1] = fmaxf(fmaxf(mh[2 * c + 1], fabsf(h[i][c].y)), fabsf(h[i + 1][c].y));
+      }
+    sh.cmax[0][warp][lane] = make_float4(mg[0], mg[1], mg[2], mg[3]);
+    sh.cmax[1][warp][lane] = make_float4(mu[0], mu[1], mu[2], mu[3]);
+    sh.cmax[2][warp][lane] = make_float4(mh[0], mh[1], mh[2], mh[3]);
+
+    // the rows' scales and codes
+    const uint32_t byte = scale_byte(rowmax);
+    const float inv = inverse_of_byte(byte);
+    if (lane < 16 && row0 + (lane & 7) < m_pad) {
+      const int64_t r = row0 + (lane & 7);
+      const int k = lane < 8 ? fb : p.fblocks + fb;
+      store_scale_byte(p.sf + (int64_t)(k >> 2) * m_pad + r, k, k == 2 * p.fblocks - 1, r < p.m ? byte : 0u);
     }
-    if (lane == 0 && r < m_pad) {
-      const bool in = r < p.m;
-      store_scale_byte(p.sf + (int64_t)(kg >> 2) * m_pad + r, kg, false, in ? (uint32_t)(eg + 127) : 0u);
-      store_scale_byte(p.sf + (int64_t)(ku >> 2) * m_pad + r, ku, ku == 2 * p.fblocks - 1,
-                       in ? (uint32_t)(eu + 127) : 0u);
+    uint8_t* qr = p.q + row0 * f2 + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float ig = __shfl_sync(0xffffffffu, inv, i), iu = __shfl_sync(0xffffffffu, inv, 8 + i);
+      if (row0 + i < p.m) {
+        *reinterpret_cast<uint32_t*>(qr) = e4m3x4(mul2(dg[i][0], ig), mul2(dg[i][1], ig));
+        *reinterpret_cast<uint32_t*>(qr + p.f) = e4m3x4(mul2(du[i][0], iu), mul2(du[i][1], iu));
+      }
+      qr += f2;
+    }
+    __syncthreads();
+    if (tid < 384) {
+      const int k = tid / 128, c = tid % 128;
+      const float* s = reinterpret_cast<const float*>(&sh.cmax[k][0][0]) + c;
+      float a = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 16; ++w) a = fmaxf(a, s[w * 128]);
+      const uint32_t b = scale_byte(a);
+      reinterpret_cast<float*>(sh.cinv[k])[c] = inverse_of_byte(b);
+      const int64_t cc = (int64_t)fb * 128 + c;
+      uint32_t* w = k == 2 ? p.hsfc + (int64_t)(rb >> 2) * p.f + cc
+                           : p.sfc + (int64_t)(rb >> 2) * f2 + (k ? p.f : 0) + cc;
+      store_scale_byte(w, rb, rb == p.rblocks - 1, b);
+    }
+    __syncthreads();
+    const float4 ig = sh.cinv[0][lane], iu = sh.cinv[1][lane], ih = sh.cinv[2][lane];
+    const float2 ig0 = make_float2(ig.x, ig.y), ig1 = make_float2(ig.z, ig.w);
+    const float2 iu0 = make_float2(iu.x, iu.y), iu1 = make_float2(iu.z, iu.w);
+    const float2 ih0 = make_float2(ih.x, ih.y), ih1 = make_float2(ih.z, ih.w);
+    uint8_t* qc = p.qc + row0 * f2 + col;
+    uint8_t* hc = p.hc + row0 * p.f + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      *reinterpret_cast<uint32_t*>(qc) = e4m3x4(mul2(dg[i][0], ig0), mul2(dg[i][1], ig1));
+      *reinterpret_cast<uint32_t*>(qc + p.f) = e4m3x4(mul2(du[i][0], iu0), mul2(du[i][1], iu1));
+      *reinterpret_cast<uint32_t*>(hc) = e4m3x4(mul2(h[i][0], ih0), mul2(h[i][1], ih1));
+      qc += f2;
+      hc += p.f;
+    }
+#pragma unroll
+    for (int s = 0; s < kBackRing - 1; ++s) {
+      live[s] = live[s + 1];
+      scale[s] = scale[s + 1];
     }
   }
-  cmax[0][warp][lane] = make_uint4(mg[0], mg[1], mg[2], mg[3]);
-  cmax[1][warp][lane] = make_uint4(mu[0], mu[1], mu[2], mu[3]);
-  cmax[2][warp][lane] = make_uint4(mh[0], mh[1], mh[2], mh[3]);
-  __syncthreads();
-  if (threadIdx.x < 384) {
-    const int k = threadIdx.x / 128, c = threadIdx.x % 128;
-    const uint32_t* s = reinterpret_cast<const uint32_t*>(&cmax[k][0][0]) + c;
-    uint32_t a = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) a = max(a, s[w * 128]);
-    const int e = scale_exponent(__uint_as_float(a));
-    reinterpret_cast<float*>(cinv[k])[c] = pow2f(-e);
-    const int64_t cc = (int64_t)fb * 128 + c;
-    uint32_t* w = k == 2 ? p.hsfc + (int64_t)(rb >> 2) * p.f + cc
-                         : p.sfc + (int64_t)(rb >> 2) * 2 * p.f + (k ? p.f : 0) + cc;
-    store_scale_byte(w, rb, rb == p.rblocks - 1, (uint32_t)(e + 127));
-  }
-  __syncthreads();
-  const float4 ig = cinv[0][lane], iu = cinv[1][lane], ih = cinv[2][lane];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = row0 + i;
-    uint8_t* qr = p.qc + r * 2 * p.f + col;
-    *reinterpret_cast<uint32_t*>(qr) = e4m3x4(dg[i][0] * ig.x, dg[i][1] * ig.y, dg[i][2] * ig.z, dg[i][3] * ig.w);
-    *reinterpret_cast<uint32_t*>(qr + p.f) = e4m3x4(du[i][0] * iu.x, du[i][1] * iu.y, du[i][2] * iu.z, du[i][3] * iu.w);
-    *reinterpret_cast<uint32_t*>(p.hc + r * p.f + col) =
-        e4m3x4(h[i][0] * ih.x, h[i][1] * ih.y, h[i][2] * ih.z, h[i][3] * ih.w);
-  }
+  cp_async_wait<0>();
 }
 
 }  // namespace
 
 cudaError_t gated_backward_launch(const void* dh, int64_t lddh, const void* gu, const void* gu_sf,
                                   const int32_t* m_indices, void* q, void* sf, void* qc, void* sfc,
-                                  void* hc, void* hsfc, int64_t m, int64_t f, int activation, bool pdl,
-                                  cudaStream_t stream) {
+                                  void* hc, void* hsfc, int64_t m, int64_t f, int activation, int sms,
+                                  bool pdl, cudaStream_t stream) {
   GatedBackwardArgs p;
   p.dh = (const __nv_bfloat16*)dh;
   p.gu = (const uint8_t*)gu;
@@ -151,10 +248,12 @@ cudaError_t gated_backward_launch(const void* dh, int64_t lddh, const void* gu, 
   p.lddh = lddh;
   p.fblocks = (int)(f / 128);
   p.rblocks = (int)((m + 127) / 128);
-  const dim3 grid((unsigned)(p.fblocks * p.rblocks));
-  if (activation == DG_ACT_SILU)
-    return launch_op(gated_backward_kernel<DG_ACT_SILU>, grid, 512, 0, pdl, stream, p);
-  return launch_op(gated_backward_kernel<DG_ACT_GELU_TANH>, grid, 512, 0, pdl, stream, p);
+  const int tiles = p.fblocks * p.rblocks;
+  const dim3 grid((unsigned)(tiles < sms ? tiles : sms));
+  auto kern = activation == DG_ACT_SILU ? gated_backward_kernel<DG_ACT_SILU> : gated_backward_kernel<DG_ACT_GELU_TANH>;
+  cudaError_t e = set_smem(kern, sizeof(BackShared));
+  if (e != cudaSuccess) return e;
+  return launch_op(kern, grid, kBackThreads, sizeof(BackShared), pdl, stream, p);
 }
 
 }  // namespace dg

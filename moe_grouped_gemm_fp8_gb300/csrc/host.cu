@@ -1390,11 +1390,11 @@ dg_status dg_requantize_fp8_cols(const void* q, const int32_t* sf, const int32_t
       (reinterpret_cast<uintptr_t>(m_indices) & 3u))
     return DG_ERR_ALIGNMENT;
   if (rows >= kMaxCoord - kBlockM || cols >= kMaxCoord) return DG_ERR_TOO_LARGE;
-  if ((rows + kBlockM - 1) / kBlockM * (cols / kBlockK) >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  if ((rows + kBlockM - 1) / kBlockM * (cols / kBlockK) >= kMaxCoord / 2) return DG_ERR_TOO_LARGE;
   int sms = 0;
   dg_status s = current_device(&sms);
   if (s != DG_OK) return s;
-  return from_cuda(use_cols_launch(q, sf, m_indices, q_cols, sf_cols, rows, cols, g_pdl.load() != 0,
+  return from_cuda(use_cols_launch(q, sf, m_indices, q_cols, sf_cols, rows, cols, sms, g_pdl.load() != 0,
                                    static_cast<cudaStream_t>(stream)));
 }
 
@@ -1504,12 +1504,12 @@ dg_status dg_fp8_gated_backward(const void* dh, int64_t lddh, const void* gu, co
       !aligned16(sf_cols) || !aligned16(h_cols) || !aligned16(h_sf_cols))
     return DG_ERR_ALIGNMENT;
   if (m >= kMaxCoord - kBlockM || f >= kMaxCoord / 2) return DG_ERR_TOO_LARGE;
-  if ((m + kBlockM - 1) / kBlockM * (f / kBlockK) >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  if ((m + kBlockM - 1) / kBlockM * (f / kBlockK) >= kMaxCoord / 2) return DG_ERR_TOO_LARGE;
   int sms = 0;
   dg_status s = current_device(&sms);
   if (s != DG_OK) return s;
   return from_cuda(gated_backward_launch(dh, lddh, gu, gu_sf, m_indices, q, sf, q_cols, sf_cols, h_cols,
-                                         h_sf_cols, m, f, activation, g_pdl.load() != 0,
+                                         h_sf_cols, m, f, activation, sms, g_pdl.load() != 0,
                                          static_cast<cudaStream_t>(stream)));
 }
 
