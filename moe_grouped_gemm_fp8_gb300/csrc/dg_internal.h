@@ -251,7 +251,7 @@ cudaError_t gated_backward_launch(const void* dh, int64_t lddh, const void* gu, 
 // layer_norm.cu
 cudaError_t layer_norm_launch(const void* x, int dtype, const void* weight, const void* bias,
                               bool w_fp32, void* y, void* sf, float* mean, float* rstd, int64_t rows,
-                              int64_t cols, int64_t ldx, float eps, bool pdl, cudaStream_t stream);
+                              int64_t cols, int64_t ldx, float eps, int sms, bool pdl, cudaStream_t stream);
 int layer_norm_backward_parts(int sms);  // partial sums a column needs room for, at most
 cudaError_t layer_norm_backward_launch(const void* dy, const void* x, int dtype, const void* weight,
                                        bool w_fp32, const float* mean, const float* rstd, void* dx,

@@ -70,34 +70,41 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
   const int tiles = p.fblocks * p.rblocks;
   const int64_t f2 = 2 * p.f;
 
-  // Rows of the warp that hold data, bit i for row 8 warp + i.
-  auto live_rows = [&](int64_t row0) {
-    const int64_t r = row0 + lane;
-    const bool in = lane < 8 && r < p.m && (!p.m_indices || __ldg(p.m_indices + r) >= 0);
-    return __ballot_sync(0xffffffffu, in);
-  };
-  // Lanes 0-7 / 8-15: the scale of g / u in the warp's row (lane % 8), 0 where it counts as zero.
-  auto row_scale = [&](int64_t row0, int fb, uint32_t live) {
-    float s = 0.0f;
-    if (lane < 16 && (live >> (lane & 7) & 1)) {
-      const int k = lane < 8 ? fb : p.fblocks + fb;
-      const uint32_t w = __ldg(p.gu_sf + (int64_t)(k >> 2) * m_pad + row0 + (lane & 7));
-      s = scale_of_byte((w >> (8 * (k & 3))) & 0xFFu);
+  // What a fetch needs to know of its rows is loaded a round before it, and the
+  // scale words it loads are decoded when their tile is worked on, so that no
+  // load is waited for where it is issued.
+  // Lanes 0-7: m_indices of the warp's row `lane` of tile t, negative where it counts as zero.
+  auto row_index = [&](int t) {
+    int index = -1;
+    if (t < tiles && lane < 8) {
+      const int64_t r = (int64_t)(t / p.fblocks) * 128 + warp * 8 + lane;
+      if (r < p.m) index = p.m_indices ? __ldg(p.m_indices + r) : 0;
     }
-    return s;
+    return index;
   };
-  auto fetch = [&](int t, int s, uint32_t& live, float& scale) {
-    live = 0;
-    scale = 0.0f;
+  // word: in lanes 0-7 / 8-15 the scale word of g / u in the warp's row (lane % 8), 0 where it counts as zero.
+  auto fetch = [&](int t, int s, int index, uint32_t& live, uint32_t& word) {
+    live = __ballot_sync(0xffffffffu, index >= 0);
+    word = 0;
     if (t < tiles) {
       const int rb = t / p.fblocks, fb = t % p.fblocks;
       const int64_t row0 = (int64_t)rb * 128 + warp * 8;
-      live = live_rows(row0);
-      scale = row_scale(row0, fb, live);
+      if (lane < 16 && (live >> (lane & 7) & 1))
+        word = __ldg(p.gu_sf + (int64_t)((lane < 8 ? fb : p.fblocks + fb) >> 2) * m_pad + row0 + (lane & 7));
       const int64_t col = (int64_t)fb * 128 + lane * 4;
       const __nv_bfloat16* d = p.dh + row0 * p.lddh + col;
       const uint8_t* c = p.gu + row0 * f2 + col;
       BackStage& st = sh.stage[s];
+      if ((live & 0xFFu) == 0xFFu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          cp_async8(&st.dh[i][tid], d);
+          cp_async4(&st.g[i][tid], c);
+          cp_async4(&st.u[i][tid], c + p.f);
+          d += p.lddh;
+          c += f2;
+        }
+      } else
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool in = live >> i & 1;
@@ -111,17 +118,23 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
     cp_async_commit();
   };
 
-  // live rows and scales of the tiles in flight, oldest first
-  uint32_t live[kBackRing];
-  float scale[kBackRing];
+  // live rows and scale words of the tiles in flight, oldest first
+  uint32_t live[kBackRing], word[kBackRing];
 #pragma unroll
-  for (int s = 0; s < kBackRing - 1; ++s) fetch(blockIdx.x + s * gridDim.x, s, live[s], scale[s]);
+  for (int s = 0; s < kBackRing - 1; ++s) {
+    const int t = blockIdx.x + s * gridDim.x;
+    fetch(t, s, row_index(t), live[s], word[s]);
+  }
+  int index = row_index(blockIdx.x + (kBackRing - 1) * gridDim.x);
   int at = 0;
   for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    fetch(t + (kBackRing - 1) * gridDim.x, at == 0 ? kBackRing - 1 : at - 1, live[kBackRing - 1],
-          scale[kBackRing - 1]);
+    fetch(t + (kBackRing - 1) * gridDim.x, at == 0 ? kBackRing - 1 : at - 1, index, live[kBackRing - 1],
+          word[kBackRing - 1]);
+    index = row_index(t + kBackRing * gridDim.x);
     cp_async_wait<kBackRing - 1>();
     const int rb = t / p.fblocks, fb = t % p.fblocks;
+    const int kmine = lane < 8 ? fb : p.fblocks + fb;
+    const float scale = (live[0] >> (lane & 7) & 1) ? scale_of_byte((word[0] >> (8 * (kmine & 3))) & 0xFFu) : 0.0f;
     const int64_t row0 = (int64_t)rb * 128 + warp * 8;
     const int64_t col = (int64_t)fb * 128 + lane * 4;
     const BackStage& st = sh.stage[at];
@@ -132,7 +145,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
     float rowmax = 0.0f;  // lanes 0-7: of dg in the row (lane % 8); lanes 8-15: of du
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float sg = __shfl_sync(0xffffffffu, scale[0], i), su = __shfl_sync(0xffffffffu, scale[0], 8 + i);
+      const float sg = __shfl_sync(0xffffffffu, scale, i), su = __shfl_sync(0xffffffffu, scale, 8 + i);
       const uint2 dv = st.dh[i][tid];
       float g[4], u[4];
       e4m3x4_to_float(st.g[i][tid], g);
@@ -175,14 +188,14 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
     const float inv = inverse_of_byte(byte);
     if (lane < 16 && row0 + (lane & 7) < m_pad) {
       const int64_t r = row0 + (lane & 7);
-      const int k = lane < 8 ? fb : p.fblocks + fb;
-      store_scale_byte(p.sf + (int64_t)(k >> 2) * m_pad + r, k, k == 2 * p.fblocks - 1, r < p.m ? byte : 0u);
+      store_scale_byte(p.sf + (int64_t)(kmine >> 2) * m_pad + r, kmine, kmine == 2 * p.fblocks - 1, r < p.m ? byte : 0u);
     }
     uint8_t* qr = p.q + row0 * f2 + col;
+    const int here = (int)min((int64_t)8, p.m - row0);  // rows of the warp inside m
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float ig = __shfl_sync(0xffffffffu, inv, i), iu = __shfl_sync(0xffffffffu, inv, 8 + i);
-      if (row0 + i < p.m) {
+      if (i < here) {
         *reinterpret_cast<uint32_t*>(qr) = e4m3x4(mul2(dg[i][0], ig), mul2(dg[i][1], ig));
         *reinterpret_cast<uint32_t*>(qr + p.f) = e4m3x4(mul2(du[i][0], iu), mul2(du[i][1], iu));
       }
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
 #pragma unroll
     for (int s = 0; s < kBackRing - 1; ++s) {
       live[s] = live[s + 1];
-      scale[s] = scale[s + 1];
+      word[s] = word[s + 1];
     }
   }
   cp_async_wait<0>();

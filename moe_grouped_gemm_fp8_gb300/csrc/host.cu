@@ -1542,7 +1542,7 @@ dg_status dg_layer_norm(const void* x, int32_t dtype, const void* weight, const 
   int sms = 0;
   if ((s = current_device(&sms)) != DG_OK) return s;
   return from_cuda(layer_norm_launch(x, dtype, weight, bias, w_dtype == DG_DTYPE_FP32, y, sf, mean, rstd, rows,
-                                     cols, ldx, eps, g_pdl.load() != 0, static_cast<cudaStream_t>(stream)));
+                                     cols, ldx, eps, sms, g_pdl.load() != 0, static_cast<cudaStream_t>(stream)));
 }
 
 dg_status dg_layer_norm_backward_workspace_size(int64_t cols, int32_t num_sms, uint64_t* bytes) {
