@@ -121,20 +121,20 @@ __global__ void __launch_bounds__(128, kUseCtas) use_cols_kernel(const uint8_t* 
   const int tiles = kblocks * rblocks;
   // m_indices of the lane's row of tile t, negative where it counts as zero;
   // loaded a round before the fetch that needs it.
-  auto row_index = [&](int t) {
+  auto row_index = [&](const TileWalk& w) {
     int index = -1;
-    if (t < tiles) {
-      const int64_t row = (int64_t)(t / kblocks) * 128 + warp * 32 + lane;
+    if (w.t < tiles) {
+      const int64_t row = (int64_t)w.rb * 128 + warp * 32 + lane;
       if (row < rows) index = m_indices ? __ldg(m_indices + row) : 0;
     }
     return index;
   };
   // live: which of the warp's 32 rows hold data, bit l for row 32 warp + l.
-  auto fetch = [&](int t, int s, int index, uint32_t& live) {
+  auto fetch = [&](const TileWalk& w, int s, int index, uint32_t& live) {
     const bool in = index >= 0;
     live = __ballot_sync(0xffffffffu, in);
-    if (t < tiles) {
-      const int rb = t / kblocks, kb = t % kblocks;
+    if (w.t < tiles) {
+      const int rb = w.rb, kb = w.cb;
       const int64_t row = (int64_t)rb * 128 + warp * 32 + lane;
       cp_async4_or_zero(&sh.words[s][tid], in ? sf + (int64_t)(kb >> 2) * rows_pad + row : sf, in);
       const uint8_t* src = q + ((int64_t)rb * 128 + warp * 32 + lane / 8) * cols + (int64_t)kb * 128 + (lane % 8) * 16;
@@ -148,17 +148,22 @@ __global__ void __launch_bounds__(128, kUseCtas) use_cols_kernel(const uint8_t* 
     cp_async_commit();
   };
   uint32_t live[kUseRing];
+  const int drb = gridDim.x / kblocks, dcb = gridDim.x % kblocks;
+  TileWalk now, ahead;  // the tile worked on; the tile whose rows are looked up next
+  now.init(blockIdx.x, kblocks);
+  ahead = now;
 #pragma unroll
   for (int s = 0; s < kUseRing - 1; ++s) {
-    const int t = blockIdx.x + s * gridDim.x;
-    fetch(t, s, row_index(t), live[s]);
+    fetch(ahead, s, row_index(ahead), live[s]);
+    ahead.next(kblocks, drb, dcb);
   }
-  int index = row_index(blockIdx.x + (kUseRing - 1) * gridDim.x);
+  int index = row_index(ahead);
   int at = 0;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int rb = t / kblocks, kb = t % kblocks;
-    fetch(t + (kUseRing - 1) * gridDim.x, at == 0 ? kUseRing - 1 : at - 1, index, live[kUseRing - 1]);
-    index = row_index(t + kUseRing * gridDim.x);
+  for (; now.t < tiles; now.next(kblocks, drb, dcb)) {
+    const int rb = now.rb, kb = now.cb;
+    fetch(ahead, at == 0 ? kUseRing - 1 : at - 1, index, live[kUseRing - 1]);
+    ahead.next(kblocks, drb, dcb);
+    index = row_index(ahead);
     cp_async_wait<kUseRing - 1>();
     __syncwarp();  // a warp's scale words are copied by its own lanes
     auto row_scale = [&](int i) {

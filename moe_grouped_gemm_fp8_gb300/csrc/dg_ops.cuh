@@ -132,15 +132,16 @@ __device__ __forceinline__ void store_scale_byte(uint32_t* word, int block, bool
     for (int i = t + 1; i < 4; ++i) p[i] = 0;
 }
 
-// The hardware's base-2 exponential and reciprocal (about 2^-22 relative each).
+// The hardware's base-2 exponential and reciprocal (about 2^-22 relative each;
+// results below 2^-126 become 0, which the logistic function does not notice).
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -205,6 +206,26 @@ static cudaError_t set_smem(Kern kern, size_t smem) {
   if (smem <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
+
+// The (row block, column block) of tiles t, t + grid, ...: one division per CTA.
+struct TileWalk {
+  int t, rb, cb;
+  __device__ __forceinline__ void init(int first, int blocks) {
+    t = first;
+    rb = first / blocks;
+    cb = first - rb * blocks;
+  }
+  // drb = grid / blocks, dcb = grid % blocks
+  __device__ __forceinline__ void next(int blocks, int drb, int dcb) {
+    t += gridDim.x;
+    rb += drb;
+    cb += dcb;
+    if (cb >= blocks) {
+      cb -= blocks;
+      ++rb;
+    }
+  }
+};
 
 // Launches with programmatic stream serialisation when pdl is set.
 template <class Kern, class... Args>

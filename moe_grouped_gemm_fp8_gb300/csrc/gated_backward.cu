@@ -74,20 +74,20 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
   // scale words it loads are decoded when their tile is worked on, so that no
   // load is waited for where it is issued.
   // Lanes 0-7: m_indices of the warp's row `lane` of tile t, negative where it counts as zero.
-  auto row_index = [&](int t) {
+  auto row_index = [&](const TileWalk& w) {
     int index = -1;
-    if (t < tiles && lane < 8) {
-      const int64_t r = (int64_t)(t / p.fblocks) * 128 + warp * 8 + lane;
+    if (w.t < tiles && lane < 8) {
+      const int64_t r = (int64_t)w.rb * 128 + warp * 8 + lane;
       if (r < p.m) index = p.m_indices ? __ldg(p.m_indices + r) : 0;
     }
     return index;
   };
   // word: in lanes 0-7 / 8-15 the scale word of g / u in the warp's row (lane % 8), 0 where it counts as zero.
-  auto fetch = [&](int t, int s, int index, uint32_t& live, uint32_t& word) {
+  auto fetch = [&](const TileWalk& w, int s, int index, uint32_t& live, uint32_t& word) {
     live = __ballot_sync(0xffffffffu, index >= 0);
     word = 0;
-    if (t < tiles) {
-      const int rb = t / p.fblocks, fb = t % p.fblocks;
+    if (w.t < tiles) {
+      const int rb = w.rb, fb = w.cb;
       const int64_t row0 = (int64_t)rb * 128 + warp * 8;
       if (lane < 16 && (live >> (lane & 7) & 1))
         word = __ldg(p.gu_sf + (int64_t)((lane < 8 ? fb : p.fblocks + fb) >> 2) * m_pad + row0 + (lane & 7));
@@ -120,19 +120,23 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
 
   // live rows and scale words of the tiles in flight, oldest first
   uint32_t live[kBackRing], word[kBackRing];
+  const int drb = gridDim.x / p.fblocks, dcb = gridDim.x % p.fblocks;
+  TileWalk now, ahead;  // the tile worked on; the tile whose rows are looked up next
+  now.init(blockIdx.x, p.fblocks);
+  ahead = now;
 #pragma unroll
   for (int s = 0; s < kBackRing - 1; ++s) {
-    const int t = blockIdx.x + s * gridDim.x;
-    fetch(t, s, row_index(t), live[s], word[s]);
+    fetch(ahead, s, row_index(ahead), live[s], word[s]);
+    ahead.next(p.fblocks, drb, dcb);
   }
-  int index = row_index(blockIdx.x + (kBackRing - 1) * gridDim.x);
+  int index = row_index(ahead);
   int at = 0;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    fetch(t + (kBackRing - 1) * gridDim.x, at == 0 ? kBackRing - 1 : at - 1, index, live[kBackRing - 1],
-          word[kBackRing - 1]);
-    index = row_index(t + kBackRing * gridDim.x);
+  for (; now.t < tiles; now.next(p.fblocks, drb, dcb)) {
+    fetch(ahead, at == 0 ? kBackRing - 1 : at - 1, index, live[kBackRing - 1], word[kBackRing - 1]);
+    ahead.next(p.fblocks, drb, dcb);
+    index = row_index(ahead);
     cp_async_wait<kBackRing - 1>();
-    const int rb = t / p.fblocks, fb = t % p.fblocks;
+    const int rb = now.rb, fb = now.cb;
     const int kmine = lane < 8 ? fb : p.fblocks + fb;
     const float scale = (live[0] >> (lane & 7) & 1) ? scale_of_byte((word[0] >> (8 * (kmine & 3))) & 0xFFu) : 0.0f;
     const int64_t row0 = (int64_t)rb * 128 + warp * 8;
