@@ -202,6 +202,15 @@ def quantize_fp8(x: torch.Tensor, block_rows: int, packed: bool = True, out=None
     packed=False FP32 scales [G?, ceil(rows/block_rows), cols/128].
     BF16 input (saving an activation in 8 bits) takes block_rows=1 and
     packed=True.  out=(q, sf) writes into preallocated tensors of those shapes."""
+    if x.dtype is torch.bfloat16 and out is None and stream is None and block_rows == 1 and packed and \
+            x.dim() == 2 and x.get_device() == torch.cuda.current_device() and x.is_contiguous():
+        rows, cols = x.shape  # the usual form of saving an activation, where a call's own time counts
+        q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
+        sf = torch.empty(sf_packed_shape(rows, cols), dtype=torch.int32, device=x.device)
+        rc = _lib.lib().dg_quantize_fp8_bf16(x.data_ptr(), q.data_ptr(), sf.data_ptr(), 1, rows, cols, _stream(None))
+        if rc:
+            _check(rc, "dg_quantize_fp8_bf16")
+        return q, sf
     if x.dim() not in (2, 3):
         raise ValueError("x must be [rows, cols] or [groups, rows, cols]")
     _need(x, "x", (torch.float32, torch.bfloat16), x.dim())

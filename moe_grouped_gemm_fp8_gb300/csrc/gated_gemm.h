@@ -22,4 +22,14 @@ struct GatedArgs {
 cudaError_t gated_gemm_launch(int mode, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& sfa,
                               const CUtensorMap& sfb, GatedArgs args, int grid, cudaStream_t stream);
 
+
+// gated_decode.cu; tn = tokens per CTA (32 or 64), split = CTAs per cluster (1,
+// 2, 4 or 8); each CTA's K range spans at most gated_decode_max_packs() scale
+// words of 4 K blocks
+cudaError_t gated_decode_launch(int tn, int split, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& sfa,
+                                const CUtensorMap& sfb, GatedArgs args, int strips, int token_blocks,
+                                cudaStream_t stream);
+int gated_decode_max_packs();
+int gated_decode_max_clusters(int tn, int split);  // that run at once on the current device
+
 }  // namespace dg

@@ -1398,6 +1398,24 @@ dg_status dg_requantize_fp8_cols(const void* q, const int32_t* sf, const int32_t
                                    static_cast<cudaStream_t>(stream)));
 }
 
+// Cluster size of the gated product's kernel for a few tokens: the largest
+// whose clusters all run at once and whose K ranges span few enough scale
+// words; 0 when none does.  DG_SPLIT_K = 1, 2, 4 or 8 forces a size where it
+// applies.
+static int gated_decode_split(int64_t clusters, int64_t kb, int tn, int sms) {
+  const int forced = env().split_k;
+  int best = 0;
+  for (int s : {1, 2, 4, 8}) {
+    if (s > kb || clusters * s > sms || (s > 1 && clusters > gated_decode_max_clusters(tn, s))) break;
+    if (forced != 0 && forced != s) continue;
+    bool fits = true;
+    for (int r = 0; r < s && fits; ++r)
+      fits = ((kb * (r + 1) / s - 1) >> 2) - ((kb * r / s) >> 2) + 1 <= gated_decode_max_packs();
+    if (fits) best = s;
+  }
+  return best;
+}
+
 // The three forms of the gated product (mode kDense, kContiguous, kMasked).
 static dg_status gated_gemm(int mode, const char* name, const void* a, const int32_t* sfa, const void* b,
                             const int32_t* sfb, void* h, int32_t* h_sf, void* gu, int32_t* gu_sf,
@@ -1431,11 +1449,31 @@ static dg_status gated_gemm(int mode, const char* name, const void* a, const int
   args.base.k_blocks = (int32_t)(k / kBlockK);
   const int64_t tiles = (int64_t)args.base.m_blocks * args.base.n_blocks;
   if (tiles * (mode == kMasked ? groups : 1) >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  // a few tokens: the kernel with swapped operand roles, whose clusters split K
+  const bool few = mode == kDense && m <= kBlockM && env().decode != 0;
+  const int tn = m <= 32 ? 32 : 64;
+  const int token_blocks = (int)((m + tn - 1) / tn);
+  const int split = few ? gated_decode_split((int64_t)args.base.n_blocks * token_blocks, args.base.k_blocks, tn, sms) : 0;
   Operands o;
-  if ((s = mode == kMasked ? encode_a_3d(o, a, sfa, groups, m, k) : encode_a_2d(o, a, sfa, m, k, lda)) != DG_OK)
+  if (split > 0) {
+    const uint64_t kp = (uint64_t)((k / kBlockK + 3) / 4);
+    const uint32_t packs = (uint32_t)gated_decode_max_packs();
+    auto map = [&](CUtensorMap* to, CUtensorMapDataType type, const void* base, uint64_t x, uint64_t y,
+                   uint64_t stride, uint32_t bx, uint32_t by, CUtensorMapSwizzle swizzle) {
+      const uint64_t dims[2] = {x, y}, strides[1] = {stride};
+      const uint32_t box[2] = {bx, by};
+      return encode(to, type, 2, base, dims, strides, box, swizzle);
+    };
+    const uint64_t m4 = (uint64_t)align4(m), n4 = (uint64_t)align4(2 * f);
+    if ((s = map(&o.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, k, m, lda, kBlockK, tn, CU_TENSOR_MAP_SWIZZLE_128B)) != DG_OK ||
+        (s = map(&o.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, b, k, 2 * f, ldb, kBlockK, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != DG_OK ||
+        (s = map(&o.sfa, CU_TENSOR_MAP_DATA_TYPE_INT32, sfa, m4, kp, m4 * 4, tn, packs, CU_TENSOR_MAP_SWIZZLE_NONE)) != DG_OK ||
+        (s = map(&o.sfb, CU_TENSOR_MAP_DATA_TYPE_INT32, sfb, n4, kp, n4 * 4, 128, packs, CU_TENSOR_MAP_SWIZZLE_NONE)) != DG_OK)
+      return s;
+  } else if ((s = mode == kMasked ? encode_a_3d(o, a, sfa, groups, m, k) : encode_a_2d(o, a, sfa, m, k, lda)) != DG_OK)
     return s;
   // Wg's and Wu's 128 rows of a tile are two boxes of one map
-  if ((s = encode_b_side(o, b, sfb, groups, 2 * f, k, ldb, 128, 128)) != DG_OK) return s;
+  if (split == 0 && (s = encode_b_side(o, b, sfb, groups, 2 * f, k, ldb, 128, 128)) != DG_OK) return s;
   args.base.m = (int32_t)m;
   args.base.n = (int32_t)f;
   args.base.k = (int32_t)k;
@@ -1455,6 +1493,12 @@ static dg_status gated_gemm(int mode, const char* name, const void* a, const int
   args.f = (int32_t)f;
   args.m_pad = (int32_t)align4(m);
   args.activation = activation;
+  if (split > 0) {
+    print_config("fp8_gated_gemm_nt (few tokens, swapped operands)", m, f, k, 1, tn, 128, split,
+                 args.base.n_blocks * split * token_blocks, 0);
+    return from_cuda(gated_decode_launch(tn, split, o.a, o.b, o.sfa, o.sfb, args, args.base.n_blocks, token_blocks,
+                                         static_cast<cudaStream_t>(stream)));
+  }
   const int64_t most = mode == kMasked ? tiles * groups : tiles;
   const int grid = (int)(most < sms ? most : sms);
   print_config(name, m, f, k, groups, kBlockM, 128, 4, grid, args.base.band);

@@ -285,3 +285,34 @@ def test_refusals():
         dg.m_grouped_fp8_gated_gemm_nt_contiguous(q3, s3, qw3, sw3, torch.zeros(100, dtype=torch.int32, device="cuda"))
     with pytest.raises(ValueError):
         dg.m_grouped_fp8_gated_gemm_nt_contiguous(q3, s3, qw3, sw3, torch.zeros(99, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("out_format,checkpoint", [("bf16", False), ("fp8", True)])
+@pytest.mark.parametrize("m,f,k", [(1, 128, 128), (3, 128, 7168), (17, 256, 4224), (32, 2048, 512), (33, 128, 1408),
+                                   (64, 384, 2048), (65, 256, 896), (100, 1024, 640), (128, 128, 256)])
+def test_few_tokens_agree_with_the_tiled_kernel(m, f, k, out_format, checkpoint, monkeypatch):
+    """The kernel for a few tokens (K split over clusters) and the tiled one,
+    each against FP64; K ranges that do and do not divide among the CTAs."""
+    q, sf, qw, sw = _operands(m, f, k, m + f + k + 2)
+    x, w = R.row_values(_np(q), _np(sf)), _weights(qw, sw)
+    for decode in ("1", "0"):
+        monkeypatch.setenv("DG_DECODE", decode)
+        _check(dg.fp8_gated_gemm_nt(q, sf, qw, sw, out_format=out_format, checkpoint=checkpoint), x, w, "silu")
+        assert dg.get_device_error()[0] == 0
+
+
+def test_few_tokens_with_a_load_that_never_lands():
+    q, sf, qw, sw = _operands(5, 256, 2048, 9)
+    want = dg.fp8_gated_gemm_nt(q, sf, qw, sw, out_format="fp8", checkpoint=True)
+    torch.cuda.synchronize()
+    dg.set_wait_timeout_ns(20_000_000)
+    dg.debug_set_drop_load(1)
+    try:
+        dg.fp8_gated_gemm_nt(q, sf, qw, sw, out_format="fp8", checkpoint=True)
+        assert dg.get_device_error()[0] == 5
+    finally:
+        dg.debug_set_drop_load(0)
+        dg.set_wait_timeout_ns(2_000_000_000)
+    again = dg.fp8_gated_gemm_nt(q, sf, qw, sw, out_format="fp8", checkpoint=True)
+    assert dg.get_device_error()[0] == 0
+    assert all(np.array_equal(_np(x), _np(y)) for x, y in zip(again, want))
