@@ -83,39 +83,33 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
     return index;
   };
   // word: in lanes 0-7 / 8-15 the scale word of g / u in the warp's row (lane % 8), 0 where it counts as zero.
-  auto fetch = [&](const TileWalk& w, int s, int index, uint32_t& live, uint32_t& word) {
+  auto look = [&](const TileWalk& w, int index, uint32_t& live, uint32_t& word) {
     live = __ballot_sync(0xffffffffu, index >= 0);
     word = 0;
-    if (w.t < tiles) {
-      const int rb = w.rb, fb = w.cb;
-      const int64_t row0 = (int64_t)rb * 128 + warp * 8;
-      if (lane < 16 && (live >> (lane & 7) & 1))
-        word = __ldg(p.gu_sf + (int64_t)((lane < 8 ? fb : p.fblocks + fb) >> 2) * m_pad + row0 + (lane & 7));
-      const int64_t col = (int64_t)fb * 128 + lane * 4;
-      const __nv_bfloat16* d = p.dh + row0 * p.lddh + col;
-      const uint8_t* c = p.gu + row0 * f2 + col;
-      BackStage& st = sh.stage[s];
-      if ((live & 0xFFu) == 0xFFu) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cp_async8(&st.dh[i][tid], d);
-          cp_async4(&st.g[i][tid], c);
-          cp_async4(&st.u[i][tid], c + p.f);
-          d += p.lddh;
-          c += f2;
-        }
-      } else
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in = live >> i & 1;
-        cp_async8_or_zero(&st.dh[i][tid], in ? d : p.dh, in);
-        cp_async4_or_zero(&st.g[i][tid], in ? c : p.gu, in);
-        cp_async4_or_zero(&st.u[i][tid], in ? c + p.f : p.gu, in);
-        d += p.lddh;
-        c += f2;
-      }
-    }
-    cp_async_commit();
+    if (lane < 16 && (live >> (lane & 7) & 1))
+      word = __ldg(p.gu_sf + (int64_t)((lane < 8 ? w.cb : p.fblocks + w.cb) >> 2) * m_pad + (int64_t)w.rb * 128 +
+                   warp * 8 + (lane & 7));
+  };
+  // Row i of the warp (dh and the checkpoint at d, c) into stage s; zeros where
+  // it is not live.  The pointers stay inside the tensors all the same: they
+  // walk over the warp's rows before m, and stop on the last one.
+  auto fetch_row = [&](int i, int s, bool in, const __nv_bfloat16* d, const uint8_t* c) {
+    BackStage& st = sh.stage[s];
+    cp_async8_or_zero(&st.dh[i][tid], d, in);
+    cp_async4_or_zero(&st.g[i][tid], c, in);
+    cp_async4_or_zero(&st.u[i][tid], c + p.f, in);
+  };
+  struct Source {
+    const __nv_bfloat16* d;
+    const uint8_t* c;
+    int left;  // rows of the warp before m
+  };
+  auto source = [&](const TileWalk& w) {
+    const int64_t row0 = (int64_t)w.rb * 128 + warp * 8;
+    const bool some = w.t < tiles && row0 < p.m;
+    const int64_t r = some ? row0 : 0;
+    const int64_t c = (some ? (int64_t)w.cb * 128 : 0) + lane * 4;
+    return Source{p.dh + r * p.lddh + c, p.gu + r * f2 + c, some ? (int)min((int64_t)8, p.m - row0) : 0};
   };
 
   // live rows and scale words of the tiles in flight, oldest first
@@ -126,16 +120,27 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
   ahead = now;
 #pragma unroll
   for (int s = 0; s < kBackRing - 1; ++s) {
-    fetch(ahead, s, row_index(ahead), live[s], word[s]);
+    look(ahead, row_index(ahead), live[s], word[s]);
+    Source src = source(ahead);
+    for (int i = 0; i < 8; ++i) {
+      fetch_row(i, s, live[s] >> i & 1, src.d, src.c);
+      if (i + 1 < src.left) {
+        src.d += p.lddh;
+        src.c += f2;
+      }
+    }
+    cp_async_commit();
     ahead.next(p.fblocks, drb, dcb);
   }
   int index = row_index(ahead);
   int at = 0;
   for (; now.t < tiles; now.next(p.fblocks, drb, dcb)) {
-    fetch(ahead, at == 0 ? kBackRing - 1 : at - 1, index, live[kBackRing - 1], word[kBackRing - 1]);
+    look(ahead, index, live[kBackRing - 1], word[kBackRing - 1]);
+    Source src = source(ahead);
+    const int free_at = at == 0 ? kBackRing - 1 : at - 1;
     ahead.next(p.fblocks, drb, dcb);
     index = row_index(ahead);
-    cp_async_wait<kBackRing - 1>();
+    cp_async_wait<kBackRing - 2>();
     const int rb = now.rb, fb = now.cb;
     const int kmine = lane < 8 ? fb : p.fblocks + fb;
     const float scale = (live[0] >> (lane & 7) & 1) ? scale_of_byte((word[0] >> (8 * (kmine & 3))) & 0xFFu) : 0.0f;
@@ -149,6 +154,12 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
     float rowmax = 0.0f;  // lanes 0-7: of dg in the row (lane % 8); lanes 8-15: of du
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      // a row of the tile after next, copied row by row between the arithmetic
+      fetch_row(i, free_at, live[kBackRing - 1] >> i & 1, src.d, src.c);
+      if (i + 1 < src.left) {
+        src.d += p.lddh;
+        src.c += f2;
+      }
       const float sg = __shfl_sync(0xffffffffu, scale, i), su = __shfl_sync(0xffffffffu, scale, 8 + i);
       const uint2 dv = st.dh[i][tid];
       float g[4], u[4];
@@ -172,6 +183,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
       if (lane == i) rowmax = rg;
       if (lane == 8 + i) rowmax = ru;
     }
+    cp_async_commit();
 #pragma unroll
     for (int i = 0; i < 8; i += 2)
 #pragma unroll
