@@ -316,3 +316,4 @@ def test_few_tokens_with_a_load_that_never_lands():
     again = dg.fp8_gated_gemm_nt(q, sf, qw, sw, out_format="fp8", checkpoint=True)
     assert dg.get_device_error()[0] == 0
     assert all(np.array_equal(_np(x), _np(y)) for x, y in zip(again, want))
+
