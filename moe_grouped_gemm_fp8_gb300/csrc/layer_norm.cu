@@ -124,7 +124,8 @@ struct LayerNormArgs {
   float* rstd;
   float* part;       // backward: [2][parts][cols] partial sums
   int64_t rows, cols, ldx, lddy, rows_pad;
-  int tpr;           // threads a row
+  int64_t ring_bytes;  // of one ring of rows
+  int tpr;             // threads a row
   float eps;
   bool w_fp32;       // weight and bias are FP32, else x's type
   bool w_wide;       // weight and bias are 16-byte aligned
@@ -301,30 +302,41 @@ __global__ void __launch_bounds__(512) layer_norm_kernel(const LayerNormArgs p) 
   }
 }
 
-// Rows on their way into shared memory.  A warp's share of a row is 32 NV pieces
-// of 16 bytes, copied by its lanes side by side and read back as each lane's
-// own NV neighbouring pieces (with two, stored crosswise so that 8 lanes meet
-// no bank twice).  Pieces past the row are never copied and stay zero, rows
-// past the last leave what was there; only the warp itself reads its pieces,
-// so __syncwarp is all that guards them.
-constexpr int kNormRing = 4;
+// ---------------------------------------------------------------- rows in a ring
+// Rows on their way into shared memory, Row::kRing of them, while others are
+// worked on.  Every warp copies and reads only its own columns, so __syncwarp
+// is all that guards them.  Two forms with one interface: a thread's P pairs of
+// values of a row (zeros past it), the same of weight or bias, and storing them.
 
-template <class T, int NV>
-struct RowRing {
+// Rows of whole, 16-byte aligned pieces.  A warp's share is 32 NV pieces, copied
+// by its lanes side by side and read back as each lane's own NV neighbouring
+// pieces (with two, stored crosswise so that 8 lanes meet no bank twice).
+// Pieces past the row are never copied and stay zero; rows past the last leave
+// what was there.
+template <class T_, int NV_>
+struct AlignedRow {
+  using T = T_;
+  static constexpr int NV = NV_;
   static constexpr int V = 16 / (int)sizeof(T);
   static constexpr int E = NV * V;  // neighbouring columns of a lane
-  uint4* mine;                      // [kNormRing][blockDim / 32][32 NV] at this warp's part
+  static constexpr int P = E / 2;
+  static constexpr int kRing = 4;
+  static constexpr bool kWide = NV == 2;  // CTAs of up to 448 or 512 threads instead of 256
+  static size_t bytes(int64_t threads) { return (size_t)kRing * NV * threads * 16; }
+  static constexpr size_t store_bytes(int64_t) { return 0; }
+  uint4* mine;                      // [kRing][blockDim / 32][32 NV] at this warp's part
   int stage;                        // distance between stages
   const T* src;                     // this lane's first piece of the next row to copy
   int64_t step;                     // elements between the rows this thread meets
   int64_t row, rows, row_step;      // the next row to copy
-  uint32_t on;                      // bit j: piece lane + 32 j lies in the row
+  uint32_t copy, on;                // bit j: piece lane + 32 j / the lane's own piece j lies in the row
+  int c;                            // the lane's first column
 
   __device__ __forceinline__ static int place(int p) { return NV == 2 ? p ^ ((p >> 3) & 1) : p; }
-  __device__ __forceinline__ void init(uint4* ring, const void* x, int64_t ld, int64_t first, int64_t every,
+  __device__ __forceinline__ void init(void* ring, const void* x, int64_t ld, int64_t first, int64_t every,
                                        int64_t last, int tid, int cols) {
     const int lane = threadIdx.x & 31;
-    mine = ring + (threadIdx.x >> 5) * 32 * NV;
+    mine = static_cast<uint4*>(ring) + (threadIdx.x >> 5) * 32 * NV;
     stage = blockDim.x * NV;
     const int c0 = (tid >> 5) * 32 * E;
     src = static_cast<const T*>(x) + first * ld + c0 + lane * V;
@@ -332,12 +344,14 @@ struct RowRing {
     row = first;
     rows = last;
     row_step = every;
-    on = 0;
+    c = tid * E;
+    copy = on = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (c0 + (lane + 32 * j) * V < cols) on |= 1u << j;
+      if (c + j * V < cols) on |= 1u << j;
+      if (c0 + (lane + 32 * j) * V < cols) copy |= 1u << j;
       else
-        for (int s = 0; s < kNormRing; ++s) mine[s * stage + place(lane + 32 * j)] = make_uint4(0, 0, 0, 0);
+        for (int s = 0; s < kRing; ++s) mine[s * stage + place(lane + 32 * j)] = make_uint4(0, 0, 0, 0);
     }
   }
   __device__ __forceinline__ void fetch(int s) {
@@ -345,72 +359,235 @@ struct RowRing {
       const int lane = threadIdx.x & 31;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (on >> j & 1) cp_async16(mine + s * stage + place(lane + 32 * j), src + 32 * j * V);
+        if (copy >> j & 1) cp_async16(mine + s * stage + place(lane + 32 * j), src + 32 * j * V);
     }
     src += step;
     row += row_step;
   }
-  __device__ __forceinline__ void read(int s, float2 (&v)[NV][V / 2]) const {
+  __device__ __forceinline__ void read(int s, float2 (&v)[P]) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint4 a = mine[s * stage + place(lane * NV + j)];
       const T* e = reinterpret_cast<const T*>(&a);
 #pragma unroll
-      for (int k = 0; k < V / 2; ++k) v[j][k] = make_float2(to_float(e[2 * k]), to_float(e[2 * k + 1]));
+      for (int k = 0; k < V / 2; ++k) v[j * V / 2 + k] = make_float2(to_float(e[2 * k]), to_float(e[2 * k + 1]));
+    }
+  }
+  __device__ __forceinline__ void params(const void* p, bool fp32, bool wide, float2 (&v)[P]) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float e[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) e[k] = 0.0f;
+      if (p && (on >> j & 1)) param_vec<T, V>(p, fp32, wide, c + j * V, e);
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) v[j * V / 2 + k] = make_float2(e[2 * k], e[2 * k + 1]);
+    }
+  }
+  // Adds m to the columns inside the row.
+  __device__ __forceinline__ void shift(float2 (&v)[P], float m) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const float a = (on >> j & 1) ? m : 0.0f;
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) v[j * V / 2 + k] = add2(v[j * V / 2 + k], make_float2(a, a));
+    }
+  }
+  // Into the row at y; `wide`: rows start on 32 bytes, so two pieces are one access.
+  __device__ __forceinline__ void store(T* y, bool wide, void*, const float2 (&v)[P]) const {
+    y += c;
+    uint32_t w[NV][4];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      T* e = reinterpret_cast<T*>(w[j]);
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        e[2 * k] = from_float<T>(v[j * V / 2 + k].x);
+        e[2 * k + 1] = from_float<T>(v[j * V / 2 + k].y);
+      }
+    }
+    if (NV == 2 && wide && on == 3u) {
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y), "r"(w[0][0]), "r"(w[0][1]),
+                   "r"(w[0][2]), "r"(w[0][3]), "r"(w[NV - 1][0]), "r"(w[NV - 1][1]), "r"(w[NV - 1][2]),
+                   "r"(w[NV - 1][3])
+                   : "memory");
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (on >> j & 1) *reinterpret_cast<uint4*>(y + j * V) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+  }
+  // A column sum per pair element.
+  __device__ __forceinline__ void store_sums(float* out, const float2 (&v)[P]) const {
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+      if (on >> (2 * k / V) & 1) {
+        out[c + 2 * k] = v[k].x;
+        out[c + 2 * k + 1] = v[k].y;
+      }
+  }
+};
+
+// Rows of any width and alignment.  A warp's share is 32 N columns; the
+// 16-byte granules that cover them are copied whole (from the granule's start,
+// which for the first column may lie before the row but not before the tensor,
+// up to the row's last byte) and the lanes read their elements at the row's own
+// offset: G neighbouring ones (2 where rows start on 4 bytes), 32 G columns
+// apart.  Results are collected the same way and leave as whole granules, with
+// single elements at both ends.
+template <class T_, int N_, int G_>
+struct RaggedRow {
+  using T = T_;
+  static constexpr int N = N_, G = G_, P = N / 2;
+  static constexpr bool kWide = N == 16;
+  static constexpr int kRing = kWide && sizeof(T) == 4 ? 2 : 4;  // what shared memory holds
+  static constexpr int kSize = (int)sizeof(T);
+  static constexpr int kGranules = 32 * N * kSize / 16 + 1;  // a warp's
+  static size_t bytes(int64_t threads) { return (size_t)kRing * kGranules * (threads / 32) * 16; }
+  static size_t store_bytes(int64_t threads) { return (size_t)kGranules * (threads / 32) * 16; }
+  uint4* mine;
+  int stage;
+  const uint8_t* src;           // this warp's first column in the next row to copy
+  const uint8_t* base;          // the tensor's first byte
+  int64_t step, row, rows, row_step;
+  uint32_t at, at_step;         // where in its granule the next row to read starts
+  int seg, live, cols;          // this warp's first column, its columns inside the row
+
+  __device__ __forceinline__ int col(int k, int e) const {  // element e of pair k
+    const int lane = threadIdx.x & 31;
+    return G == 2 ? seg + (k * 32 + lane) * 2 + e : seg + (2 * k + e) * 32 + lane;
+  }
+  __device__ __forceinline__ void init(void* ring, const void* x, int64_t ld, int64_t first, int64_t every,
+                                       int64_t last, int tid, int n) {
+    mine = static_cast<uint4*>(ring) + (threadIdx.x >> 5) * kGranules;
+    stage = (int)(blockDim.x >> 5) * kGranules;
+    seg = (tid >> 5) * 32 * N;
+    cols = n;
+    live = min(32 * N, n - seg);  // < 0: none
+    base = static_cast<const uint8_t*>(x);
+    src = base + (first * ld + seg) * kSize;
+    step = every * ld * kSize;
+    row = first;
+    rows = last;
+    row_step = every;
+    at = (uint32_t)(uintptr_t)src;
+    at_step = (uint32_t)step;
+  }
+  __device__ __forceinline__ void fetch(int s) {
+    if (row < rows && live > 0) {
+      const int lane = threadIdx.x & 31;
+      const int skip = (int)((uintptr_t)src & 15u);
+      const uint8_t* from = src - skip;
+      const int total = skip + live * kSize;
+#pragma unroll
+      for (int i = 0; i < (kGranules + 31) / 32; ++i) {
+        const int g = lane + 32 * i;
+        if (g * 16 < total) {
+          uint4* to = mine + s * stage + g;
+          if (from + g * 16 >= base) cp_async16_part(to, from + g * 16, min(16, total - g * 16));
+          else  // the tensor's first granule, where it starts inside one
+            for (int b = skip; b < min(16, total); b += kSize)
+              *reinterpret_cast<T*>(reinterpret_cast<uint8_t*>(to) + b) = *reinterpret_cast<const T*>(from + b);
+        }
+      }
+    }
+    src += step;
+    row += row_step;
+  }
+  __device__ __forceinline__ void read(int s, float2 (&v)[P]) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(mine + s * stage) + (at & 15u);
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if constexpr (G == 2) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(p + (k * 32 + lane) * 4);
+        const T* e = reinterpret_cast<const T*>(&w);
+        v[k] = make_float2(to_float(e[0]), to_float(e[1]));
+      } else {
+        v[k] = make_float2(to_float(*reinterpret_cast<const T*>(p + (2 * k * 32 + lane) * kSize)),
+                           to_float(*reinterpret_cast<const T*>(p + ((2 * k + 1) * 32 + lane) * kSize)));
+      }
+    }
+    at += at_step;
+    if (live < 32 * N) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        if (col(k, 0) >= cols) v[k].x = 0.0f;
+        if (col(k, 1) >= cols) v[k].y = 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void params(const void* p, bool fp32, bool, float2 (&v)[P]) const {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int a = col(k, 0), b = col(k, 1);
+      v[k] = make_float2(p && a < cols ? param<T>(p, fp32, a) : 0.0f, p && b < cols ? param<T>(p, fp32, b) : 0.0f);
+    }
+  }
+  __device__ __forceinline__ void shift(float2 (&v)[P], float m) const {
+    if (live == 32 * N) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) v[k] = add2(v[k], make_float2(m, m));
+    } else {
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        v[k] = add2(v[k], make_float2(col(k, 0) < cols ? m : 0.0f, col(k, 1) < cols ? m : 0.0f));
+    }
+  }
+  // Through `room` (store_bytes), which the caller's next __syncwarp frees again.
+  __device__ __forceinline__ void store(T* y, bool, void* room, const float2 (&v)[P]) const {
+    if (live <= 0) return;
+    const int lane = threadIdx.x & 31;
+    uint8_t* dst = reinterpret_cast<uint8_t*>(y + seg);
+    const int skip = (int)((uintptr_t)dst & 15u);
+    uint8_t* p = reinterpret_cast<uint8_t*>(static_cast<uint4*>(room) + (threadIdx.x >> 5) * kGranules);
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if constexpr (G == 2) {
+        uint32_t w;
+        T* e = reinterpret_cast<T*>(&w);
+        e[0] = from_float<T>(v[k].x);
+        e[1] = from_float<T>(v[k].y);
+        *reinterpret_cast<uint32_t*>(p + skip + (k * 32 + lane) * 4) = w;
+      } else {
+        *reinterpret_cast<T*>(p + skip + (2 * k * 32 + lane) * kSize) = from_float<T>(v[k].x);
+        *reinterpret_cast<T*>(p + skip + ((2 * k + 1) * 32 + lane) * kSize) = from_float<T>(v[k].y);
+      }
+    }
+    __syncwarp();
+    const int total = skip + live * kSize;
+#pragma unroll
+    for (int i = 0; i < (kGranules + 31) / 32; ++i) {
+      const int g = lane + 32 * i;
+      if (g * 16 >= skip && g * 16 + 16 <= total)
+        *reinterpret_cast<uint4*>(dst - skip + g * 16) = *reinterpret_cast<const uint4*>(p + g * 16);
+    }
+    // the ends: bytes before the first whole granule and after the last
+    const int head = min((skip + 15) / 16 * 16, total), rest = max(total / 16 * 16, head);
+    for (int b = skip + lane * kSize; b < head; b += 32 * kSize)
+      *reinterpret_cast<T*>(dst - skip + b) = *reinterpret_cast<const T*>(p + b);
+    for (int b = rest + lane * kSize; b < total; b += 32 * kSize)
+      *reinterpret_cast<T*>(dst - skip + b) = *reinterpret_cast<const T*>(p + b);
+  }
+  __device__ __forceinline__ void store_sums(float* out, const float2 (&v)[P]) const {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if (col(k, 0) < cols) out[col(k, 0)] = v[k].x;
+      if (col(k, 1) < cols) out[col(k, 1)] = v[k].y;
     }
   }
 };
 
-// A lane's NV neighbouring pieces of a row of y; `wide`: in one access of 32 bytes.
-template <class T, int NV>
-__device__ __forceinline__ void store_pieces(T* y, bool wide, uint32_t on, const float2 (&v)[NV][8 / (int)sizeof(T)]) {
-  constexpr int V = 16 / (int)sizeof(T);
-  uint32_t w[NV][4];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    T* e = reinterpret_cast<T*>(w[j]);
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) {
-      e[2 * k] = from_float<T>(v[j][k].x);
-      e[2 * k + 1] = from_float<T>(v[j][k].y);
-    }
-  }
-  if (NV == 2 && wide && on == 3u) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y), "r"(w[0][0]), "r"(w[0][1]),
-                 "r"(w[0][2]), "r"(w[0][3]), "r"(w[NV - 1][0]), "r"(w[NV - 1][1]), "r"(w[NV - 1][2]), "r"(w[NV - 1][3])
-                 : "memory");
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (on >> j & 1) *reinterpret_cast<uint4*>(y + j * V) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
-}
-
-// Weight or bias of a lane's columns, zeros past the row.
-template <class T, int NV>
-__device__ __forceinline__ void param_pieces(const void* p, bool fp32, bool wide, int c, uint32_t on,
-                                             float2 (&v)[NV][8 / (int)sizeof(T)]) {
-  constexpr int V = 16 / (int)sizeof(T);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    float e[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) e[k] = 0.0f;
-    if (p && (on >> j & 1)) param_vec<T, V>(p, fp32, wide, c + j * V, e);
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) v[j][k] = make_float2(e[2 * k], e[2 * k + 1]);
-  }
-}
-
-// The forward pass for rows of up to 896 pieces of 16 bytes: a CTA keeps its
-// columns' weight and bias in registers and walks over rows by the grid.
-// Reading weight and bias anew for every row would move four times the row's
-// own bytes through L1.
-template <class T, int NV, bool FP8>
-__global__ void __launch_bounds__(NV == 1 ? 256 : 448, NV == 1 ? 5 : 2) layer_norm_ring_kernel(const LayerNormArgs p) {
-  using R = RowRing<T, NV>;
-  constexpr int P = R::V / 2, E = R::E;
+// The forward pass for rows of up to about 7 KB of FP32 (448 threads of 16
+// values): a CTA keeps its columns' weight and bias in registers and walks over
+// rows by the grid.  Reading weight and bias anew for every row would move four
+// times the row's own bytes through L1.
+template <class Row, bool FP8>
+__global__ void __launch_bounds__(Row::kWide ? 448 : 256, Row::kWide ? 2 : 4)
+    layer_norm_ring_kernel(const LayerNormArgs p) {
+  using T = typename Row::T;
+  constexpr int P = Row::P, kRing = Row::kRing;
   extern __shared__ uint4 ring[];
   __shared__ float red[64];
   griddep_wait();
@@ -422,24 +599,14 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 448, NV == 1 ? 5 : 2) layer_no
   const int64_t rows = FP8 ? p.rows_pad : p.rows;
   const int64_t step = (int64_t)gridDim.x * rpc;
   int64_t row = (int64_t)blockIdx.x * rpc + threadIdx.x / tpr;
-  R src;
+  Row src;
   src.init(ring, p.x, p.ldx, row, step, p.rows, tid, cols);
-  const int c = tid * E;
-  uint32_t on = 0;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (c + j * R::V < cols) on |= 1u << j;
-  float2 w[NV][P], b[NV][P];
-  param_pieces<T, NV>(p.weight, p.w_fp32, p.w_wide, c, on, w);
-  param_pieces<T, NV>(p.bias, p.w_fp32, p.w_wide, c, on, b);
+  void* const room = reinterpret_cast<uint8_t*>(ring) + p.ring_bytes;
+  float2 w[P], b[P];
+  src.params(p.weight, p.w_fp32, p.w_wide, w);
+  src.params(p.bias, p.w_fp32, p.w_wide, b);
   const bool wide = ((p.cols * (int64_t)sizeof(T)) | (int64_t)(uintptr_t)p.y) % 32 == 0;
-  const int64_t y_step = step * p.cols;
-  T* y = static_cast<T*>(p.y) + row * p.cols + c;             // same-type results
-  uint8_t* q = static_cast<uint8_t*>(p.y) + row * p.cols + c;  // 8-bit results
-  uint32_t* sf = p.sf + (int64_t)(c / 512) * p.rows_pad + row;
-  const int kb = c / 128;
-  const bool sf_mine = FP8 && on && c % 128 == 0, sf_last = c + 128 == cols;
-  for (int s = 0; s < kNormRing - 1; ++s) {
+  for (int s = 0; s < kRing - 1; ++s) {
     src.fetch(s);
     cp_async_commit();
   }
@@ -449,66 +616,52 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 448, NV == 1 ? 5 : 2) layer_no
   for (int64_t base = (int64_t)blockIdx.x * rpc; base < rows; base += step) {
     const bool in = row < p.rows;
     __syncwarp();  // the warp has read the slot that is filled next
-    src.fetch(at == 0 ? kNormRing - 1 : at - 1);
+    src.fetch(at == 0 ? kRing - 1 : at - 1);
     cp_async_commit();
-    cp_async_wait<kNormRing - 1>();
+    cp_async_wait<kRing - 1>();
     __syncwarp();
-    float2 v[NV][P];
+    float2 v[P];
     src.read(at, v);
-    if (++at == kNormRing) at = 0;
+    if (++at == kRing) at = 0;
     float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < P; ++k) s = add2(s, v[j][k]);
+    for (int k = 0; k < P; ++k) s = add2(s, v[k]);
     const float mean = row_sum(s.x + s.y, red, warps, warp0, 0) * rn;
     float2 d2 = make_float2(0.0f, 0.0f);
+    src.shift(v, -mean);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const float m = (on >> j & 1) ? -mean : 0.0f;
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        v[j][k] = add2(v[j][k], make_float2(m, m));
-        d2 = fma2(v[j][k], v[j][k], d2);
-      }
-    }
+    for (int k = 0; k < P; ++k) d2 = fma2(v[k], v[k], d2);
     const float rstd = rsqrt_newton(row_sum(d2.x + d2.y, red, warps, warp0, 1) * rn + p.eps);
     if (in && tid == 0) {
       p.mean[row] = mean;
       p.rstd[row] = rstd;
     }
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int k = 0; k < P; ++k) v[j][k] = fma2(mul2(v[j][k], rstd), w[j][k], b[j][k]);
+    for (int k = 0; k < P; ++k) v[k] = fma2(mul2(v[k], rstd), w[k], b[k]);
     if constexpr (!FP8) {
-      if (in) store_pieces<T, NV>(y, wide, on, v);
+      if (in) src.store(static_cast<T*>(p.y) + row * p.cols, wide, room, v);
     } else {
+      constexpr int E = Row::E;  // neighbouring columns of a lane
       float m = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < P; ++k) m = abs_max2(m, v[j][k]);
+      for (int k = 0; k < P; ++k) m = abs_max2(m, v[k]);
 #pragma unroll
       for (int o = 64 / E; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       const uint32_t e = scale_byte(m);
-      if (in && on) {
+      const int c = src.c;
+      if (in && c < cols) {
         const float inv = inverse_of_byte(e);
         uint32_t o[E / 4];
 #pragma unroll
-        for (int k = 0; k < E / 4; ++k) {
-          const int j = 4 * k / R::V, i = (4 * k % R::V) / 2;
-          o[k] = e4m3x4(mul2(v[j][i], inv), mul2(v[j][i + 1], inv));
-        }
+        for (int k = 0; k < E / 4; ++k) o[k] = e4m3x4(mul2(v[2 * k], inv), mul2(v[2 * k + 1], inv));
+        uint8_t* q = static_cast<uint8_t*>(p.y) + row * p.cols + c;
         if constexpr (E == 16) *reinterpret_cast<uint4*>(q) = make_uint4(o[0], o[1], o[2], o[3]);
         else if constexpr (E == 8) *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
         else *reinterpret_cast<uint32_t*>(q) = o[0];
       }
-      if (sf_mine && row < rows) store_scale_byte(sf, kb, sf_last, in ? e : 0u);
-      sf += step;
+      if (c < cols && c % 128 == 0 && row < rows)
+        store_scale_byte(p.sf + (int64_t)(c / 512) * p.rows_pad + row, c / 128, c + 128 == cols, in ? e : 0u);
     }
-    y += y_step;
-    q += y_step;
     row += step;
   }
   cp_async_wait<0>();
@@ -566,68 +719,11 @@ __device__ __forceinline__ float2 row_sum_pair(float a, float b, float (&red)[2]
   return make_float2(__shfl_sync(0xffffffffu, t, 0), __shfl_sync(0xffffffffu, t, 16));
 }
 
-// One row's share: x becomes xh, dy becomes dx; the columns' sums grow.
-template <int NV, int P>
-__device__ __forceinline__ float2 backward_sums(float2 (&xv)[NV][P], float2 (&dv)[NV][P], const float2 (&w)[NV][P],
-                                                float2 (&aw)[NV][P], float2 (&ab)[NV][P], float mean, float rstd) {
-  const float2 nm = make_float2(-mean, -mean);
-  float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      xv[i][k] = mul2(add2(xv[i][k], nm), rstd);
-      aw[i][k] = fma2(dv[i][k], xv[i][k], aw[i][k]);
-      ab[i][k] = add2(ab[i][k], dv[i][k]);
-      dv[i][k] = mul2(dv[i][k], w[i][k]);
-      s1 = add2(s1, dv[i][k]);
-      s2 = fma2(dv[i][k], xv[i][k], s2);
-    }
-  return make_float2(s1.x + s1.y, s2.x + s2.y);
-}
-template <int NV, int P>
-__device__ __forceinline__ void backward_dx(const float2 (&xv)[NV][P], float2 (&dv)[NV][P], float2 c, float rn, float rstd) {
-  const float2 n1 = make_float2(-c.x * rn, -c.x * rn), n2 = make_float2(-c.y * rn, -c.y * rn);
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < P; ++k) dv[i][k] = mul2(fma2(xv[i][k], n2, add2(dv[i][k], n1)), rstd);
-}
-// Adds the CTA's row groups' sums up in their order; false in the threads of
-// all groups but the first, which ends with the whole.
-template <int NV, int P>
-__device__ __forceinline__ bool join_groups(float2* sums, int tpr, float2 (&aw)[NV][P], float2 (&ab)[NV][P]) {
-  const int rpc = blockDim.x / tpr;
-  if (rpc == 1) return true;
-  __syncthreads();
-  float2* mine = sums + (size_t)(threadIdx.x / tpr) * 2 * NV * P * tpr + threadIdx.x % tpr;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      mine[(i * P + k) * tpr] = aw[i][k];
-      mine[((NV + i) * P + k) * tpr] = ab[i][k];
-    }
-  __syncthreads();
-  if ((int)threadIdx.x >= tpr) return false;
-  for (int g = 1; g < rpc; ++g) {
-    mine += 2 * NV * P * tpr;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        aw[i][k] = add2(aw[i][k], mine[(i * P + k) * tpr]);
-        ab[i][k] = add2(ab[i][k], mine[((NV + i) * P + k) * tpr]);
-      }
-  }
-  return true;
-}
-
-template <class T, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : 1)
+template <class Row>
+__global__ void __launch_bounds__(Row::kWide ? 512 : 256, Row::kWide ? 1 : 3)
     layer_norm_backward_ring_kernel(const LayerNormArgs p) {
-  using R = RowRing<T, NV>;
-  constexpr int P = R::V / 2;
+  using T = typename Row::T;
+  constexpr int P = Row::P, kRing = Row::kRing;
   extern __shared__ uint4 ring[];  // x's rows, then dy's; at the end, the row groups' sums
   __shared__ float red[2][32];
   griddep_wait();
@@ -638,24 +734,17 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : 1)
   const int cols = (int)p.cols;
   const int64_t step = (int64_t)gridDim.x * rpc;
   int64_t row = (int64_t)blockIdx.x * rpc + threadIdx.x / tpr;
-  R xs, ds;
-  xs.init(ring, p.x, p.ldx, row, step, p.rows, tid, cols);
-  ds.init(ring + kNormRing * blockDim.x * NV, p.dy, p.lddy, row, step, p.rows, tid, cols);
-  const int c = tid * R::E;
-  uint32_t on = 0;
+  uint8_t* const shared = reinterpret_cast<uint8_t*>(ring);
+  Row xs, ds;
+  xs.init(shared, p.x, p.ldx, row, step, p.rows, tid, cols);
+  ds.init(shared + p.ring_bytes, p.dy, p.lddy, row, step, p.rows, tid, cols);
+  void* const room = shared + 2 * p.ring_bytes;
+  float2 w[P], aw[P], ab[P];
+  xs.params(p.weight, p.w_fp32, p.w_wide, w);
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (c + j * R::V < cols) on |= 1u << j;
-  float2 w[NV][P], aw[NV][P], ab[NV][P];
-  param_pieces<T, NV>(p.weight, p.w_fp32, p.w_wide, c, on, w);
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int k = 0; k < P; ++k) aw[j][k] = ab[j][k] = make_float2(0.0f, 0.0f);
+  for (int k = 0; k < P; ++k) aw[k] = ab[k] = make_float2(0.0f, 0.0f);
   const bool wide = ((p.cols * (int64_t)sizeof(T)) | (int64_t)(uintptr_t)p.y) % 32 == 0;
-  const int64_t y_step = step * p.cols;
-  T* y = static_cast<T*>(p.y) + row * p.cols + c;
-  for (int s = 0; s < kNormRing - 1; ++s) {
+  for (int s = 0; s < kRing - 1; ++s) {
     xs.fetch(s);
     ds.fetch(s);
     cp_async_commit();
@@ -667,104 +756,67 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : 1)
   for (int64_t base = (int64_t)blockIdx.x * rpc; base < p.rows; base += step) {
     const bool in = row < p.rows;
     __syncwarp();  // the warp has read the slot that is filled next
-    const int next = at == 0 ? kNormRing - 1 : at - 1;
+    const int next = at == 0 ? kRing - 1 : at - 1;
     xs.fetch(next);
     ds.fetch(next);
     cp_async_commit();
     const bool more = row + step < p.rows;
     const float mean1 = more ? __ldg(p.mean + row + step) : 0.0f, rstd1 = more ? __ldg(p.rstd + row + step) : 0.0f;
-    cp_async_wait<kNormRing - 1>();
+    cp_async_wait<kRing - 1>();
     __syncwarp();
-    float2 xv[NV][P], dv[NV][P];
+    float2 xv[P], dv[P];
     xs.read(at, xv);
     ds.read(at, dv);
-    if (++at == kNormRing) at = 0;
+    if (++at == kRing) at = 0;
     if (!in) {  // the last round of a row group that has no row in it: an old row adds nothing
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int k = 0; k < P; ++k) xv[j][k] = dv[j][k] = make_float2(0.0f, 0.0f);
+      for (int k = 0; k < P; ++k) xv[k] = dv[k] = make_float2(0.0f, 0.0f);
     }
-    const float2 mine = backward_sums<NV, P>(xv, dv, w, aw, ab, mean, rstd);
-    const float2 sums = row_sum_pair(mine.x, mine.y, red, turn, warps, warp0);
+    // past the row dy is 0, so whatever xh is there adds nothing
+    const float2 nm = make_float2(-mean, -mean);
+    float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      xv[k] = mul2(add2(xv[k], nm), rstd);
+      aw[k] = fma2(dv[k], xv[k], aw[k]);
+      ab[k] = add2(ab[k], dv[k]);
+      dv[k] = mul2(dv[k], w[k]);
+      s1 = add2(s1, dv[k]);
+      s2 = fma2(dv[k], xv[k], s2);
+    }
+    const float2 sums = row_sum_pair(s1.x + s1.y, s2.x + s2.y, red, turn, warps, warp0);
     turn ^= 1;
-    backward_dx<NV, P>(xv, dv, sums, rn, rstd);
-    if (in) store_pieces<T, NV>(y, wide, on, dv);
-    y += y_step;
+    const float2 n1 = make_float2(-sums.x * rn, -sums.x * rn), n2 = make_float2(-sums.y * rn, -sums.y * rn);
+#pragma unroll
+    for (int k = 0; k < P; ++k) dv[k] = mul2(fma2(xv[k], n2, add2(dv[k], n1)), rstd);
+    if (in) xs.store(static_cast<T*>(p.y) + row * p.cols, wide, room, dv);
     row += step;
     mean = mean1;
     rstd = rstd1;
   }
   cp_async_wait<0>();
-  if (!join_groups<NV, P>(reinterpret_cast<float2*>(ring), tpr, aw, ab)) return;
-  float* part = p.part + (int64_t)blockIdx.x * p.cols;
-  float* partb = part + (int64_t)gridDim.x * p.cols;
+  if (rpc > 1) {  // the row groups' sums, added up in their order by the first group
+    __syncthreads();
+    float2* mine = reinterpret_cast<float2*>(ring) + (size_t)(threadIdx.x / tpr) * 2 * P * tpr + tid;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (on >> j & 1) {
+    for (int k = 0; k < P; ++k) {
+      mine[k * tpr] = aw[k];
+      mine[(P + k) * tpr] = ab[k];
+    }
+    __syncthreads();
+    if ((int)threadIdx.x >= tpr) return;
+    for (int g = 1; g < rpc; ++g) {
+      mine += 2 * P * tpr;
 #pragma unroll
       for (int k = 0; k < P; ++k) {
-        const int cc = c + j * R::V + 2 * k;
-        part[cc] = aw[j][k].x;
-        part[cc + 1] = aw[j][k].y;
-        partb[cc] = ab[j][k].x;
-        partb[cc + 1] = ab[j][k].y;
+        aw[k] = add2(aw[k], mine[k * tpr]);
+        ab[k] = add2(ab[k], mine[(P + k) * tpr]);
       }
     }
-}
-
-// The same where rows are not 16-byte aligned: single elements, read directly.
-template <class T, int NV>
-__global__ void __launch_bounds__(512) layer_norm_backward_kernel(const LayerNormArgs p) {
-  extern __shared__ uint4 ring[];  // the row groups' sums
-  __shared__ float red[2][32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int tpr = p.tpr, rpc = blockDim.x / tpr;
-  const int tid = threadIdx.x % tpr;
-  const int warps = tpr / 32, warp0 = threadIdx.x / tpr * warps;
-  const int cols = (int)p.cols;
-  float2 w[NV][1], aw[NV][1], ab[NV][1];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    param_share<T, 1>(p.weight, p.w_fp32, p.w_wide, i, tid, tpr, cols, w[i]);
-    aw[i][0] = ab[i][0] = make_float2(0.0f, 0.0f);
   }
-  const float rn = 1.0f / (float)cols;
-  int turn = 0;
-  for (int64_t base = (int64_t)blockIdx.x * rpc; base < p.rows; base += (int64_t)gridDim.x * rpc) {
-    const int64_t row = base + threadIdx.x / tpr;
-    const bool in = row < p.rows;
-    const float mean = in ? __ldg(p.mean + row) : 0.0f, rstd = in ? __ldg(p.rstd + row) : 0.0f;
-    float2 xv[NV][1], dv[NV][1];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      load_share<T, 1>(static_cast<const T*>(p.x) + (in ? row : 0) * p.ldx, i, tid, tpr, in ? cols : 0, xv[i]);
-      load_share<T, 1>(static_cast<const T*>(p.dy) + (in ? row : 0) * p.lddy, i, tid, tpr, in ? cols : 0, dv[i]);
-    }
-    const float2 mine = backward_sums<NV, 1>(xv, dv, w, aw, ab, mean, rstd);  // past the row dy is 0
-    const float2 sums = row_sum_pair(mine.x, mine.y, red, turn, warps, warp0);
-    turn ^= 1;
-    backward_dx<NV, 1>(xv, dv, sums, rn, rstd);
-    if (in) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        store_share<T, 1>(static_cast<T*>(p.y) + row * p.cols, i, tid, tpr, cols, dv[i]);
-    }
-  }
-  if (!join_groups<NV, 1>(reinterpret_cast<float2*>(ring), tpr, aw, ab)) return;
   float* part = p.part + (int64_t)blockIdx.x * p.cols;
-  float* partb = part + (int64_t)gridDim.x * p.cols;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int c = Share<1>::col(i, k, tid, tpr);
-      if (c < cols) {
-        part[c] = k ? aw[i][0].y : aw[i][0].x;
-        partb[c] = k ? ab[i][0].y : ab[i][0].x;
-      }
-    }
+  xs.store_sums(part, aw);
+  xs.store_sums(part + (int64_t)gridDim.x * p.cols, ab);
 }
 
 // Rows too long for registers: dx one CTA a row ...
@@ -830,74 +882,112 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* __re
   if (lane == 0 && o < cols) (blockIdx.y ? db : dw)[o] = s;
 }
 
+// Threads of a row and of a CTA (at least 128, whole rows) for n values a thread.
+struct NormShape {
+  int64_t tpr, threads, rpc;
+  NormShape(int64_t cols, int n) {
+    tpr = ((cols + n - 1) / n + 31) / 32 * 32;
+    threads = tpr >= 128 ? tpr : 128 / tpr * tpr;
+    rpc = threads / tpr;
+  }
+};
+
+// Two neighbouring elements can be read at once where rows start on 4 bytes.
+template <class T>
+bool pairs_aligned(const LayerNormArgs& p, bool backward) {
+  if (sizeof(T) == 4) return false;
+  return ((p.ldx | p.cols | (backward ? p.lddy : 0)) & 1) == 0 &&
+         (((uintptr_t)p.x | (uintptr_t)p.y | (backward ? (uintptr_t)p.dy : 0)) & 3) == 0;
+}
+
 template <class T, bool FP8>
 cudaError_t forward(const LayerNormArgs& a, bool vec, int sms, bool pdl, cudaStream_t st) {
   LayerNormArgs p = a;
   constexpr int V = 16 / (int)sizeof(T);
-  // Rows of up to 896 vectors take the ring kernel: 1 or 2 vectors a thread,
-  // CTAs of 128 threads or one row.  Longer ones are read into 4 or 8 vectors
-  // a thread (or 8 or 32 single elements) of one CTA a row.
-  const int64_t units = vec ? p.cols / V : p.cols;
   const int64_t rows = FP8 ? p.rows_pad : p.rows;
-  auto shape = [&](int nv) {
-    const int64_t t = ((units + nv - 1) / nv + 31) / 32 * 32;
-    p.tpr = (int)t;
-    return t >= 128 ? t : 128 / t * t;
-  };
-  auto go = [&](auto kern, int nv) {
-    const int64_t threads = shape(nv), rpc = threads / p.tpr;
-    return launch_op(kern, dim3((unsigned)((rows + rpc - 1) / rpc)), (unsigned)threads, 0, pdl, st, p);
-  };
-  auto go_ring = [&](auto kern, int nv) {
-    const int64_t threads = shape(nv), rpc = threads / p.tpr;
-    const size_t smem = (size_t)kNormRing * nv * threads * 16;
+  // Rows of up to 448 threads of 16 values (8 of FP32 by pieces) take the ring
+  // kernel, as many CTAs an SM as its registers and shared memory hold.
+  // Longer ones are read into registers of one CTA a row, or in passes.
+  auto ring = [&](auto kern, auto row, int n) {
+    using Row = decltype(row);
+    const NormShape s(p.cols, n);
+    p.tpr = (int)s.tpr;
+    p.ring_bytes = (int64_t)Row::bytes(s.threads);
+    const size_t smem = Row::bytes(s.threads) + Row::store_bytes(s.threads);
     const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>((int64_t)(220 * 1024) / (int64_t)(smem + 2048),
-                                                                  (nv == 1 ? 1280 : 896) / threads));
+                                                                  (Row::kWide ? 896 : 1024) / s.threads));
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    return launch_op(kern, dim3((unsigned)std::min<int64_t>((rows + rpc - 1) / rpc, per_sm * sms)), (unsigned)threads,
-                     smem, pdl, st, p);
+    return launch_op(kern, dim3((unsigned)std::min<int64_t>((rows + s.rpc - 1) / s.rpc, per_sm * sms)),
+                     (unsigned)s.threads, smem, pdl, st, p);
   };
+  auto whole = [&](auto kern, int n) {
+    const NormShape s(p.cols, n);
+    p.tpr = (int)s.tpr;
+    return launch_op(kern, dim3((unsigned)((rows + s.rpc - 1) / s.rpc)), (unsigned)s.threads, 0, pdl, st, p);
+  };
+#define DG_NORM_RING(ROW, n) ring(layer_norm_ring_kernel<ROW, FP8>, ROW(), n)
   if (vec) {
-    if (units <= 256) return go_ring(layer_norm_ring_kernel<T, 1, FP8>, 1);
-    if (units <= 2 * 448) return go_ring(layer_norm_ring_kernel<T, 2, FP8>, 2);  // 2 x 448 threads of 72 registers
-    if (units <= 4 * 512) return go(layer_norm_kernel<T, V, 4, FP8>, 4);
-    if (units <= 8 * 512) return go(layer_norm_kernel<T, V, 8, FP8>, 8);
+    using One = AlignedRow<T, 1>;
+    using Two = AlignedRow<T, 2>;
+    if (p.cols <= 256 * V) return DG_NORM_RING(One, V);
+    if (p.cols <= 448 * 2 * V) return DG_NORM_RING(Two, 2 * V);
+    if (p.cols <= 512 * 4 * V) return whole(layer_norm_kernel<T, V, 4, FP8>, 4 * V);
+    if (p.cols <= 512 * 8 * V) return whole(layer_norm_kernel<T, V, 8, FP8>, 8 * V);
   }
   if constexpr (FP8) return cudaErrorInvalidValue;
   else {
-    if (!vec && units <= 8 * 512) return go(layer_norm_kernel<T, 1, 4, false>, 8);
-    if (!vec && units <= 32 * 512) return go(layer_norm_kernel<T, 1, 16, false>, 32);
+    if (!vec && p.cols <= 448 * 16) {
+      using Few1 = RaggedRow<T, 8, 1>;
+      using Many1 = RaggedRow<T, 16, 1>;
+      if constexpr (sizeof(T) == 2) {
+        using Few2 = RaggedRow<T, 8, 2>;
+        using Many2 = RaggedRow<T, 16, 2>;
+        if (pairs_aligned<T>(p, false)) return p.cols <= 256 * 8 ? DG_NORM_RING(Few2, 8) : DG_NORM_RING(Many2, 16);
+      }
+      return p.cols <= 256 * 8 ? DG_NORM_RING(Few1, 8) : DG_NORM_RING(Many1, 16);
+    }
+    if (!vec && p.cols <= 32 * 512) return whole(layer_norm_kernel<T, 1, 16, false>, 32);
     return launch_op(layer_norm_long_kernel<T>, dim3((unsigned)p.rows), 1024, 0, pdl, st, p);
   }
+#undef DG_NORM_RING
 }
 
 template <class T>
 cudaError_t backward(const LayerNormArgs& a, bool vec, int parts, int* used, bool pdl, cudaStream_t st) {
   LayerNormArgs p = a;
   constexpr int V = 16 / (int)sizeof(T);
-  const int64_t units = vec ? p.cols / V : p.cols;
-  // A row takes tpr threads of 1 or 2 pieces of 16 bytes (4 or 16 single
-  // elements); CTAs of 128 threads or one row, as many an SM as fit, at most
-  // kNormParts.
-  auto go = [&](auto kern, int nv, int most) {
-    const int64_t t = ((units + nv - 1) / nv + 31) / 32 * 32;
-    p.tpr = (int)t;
-    const int64_t threads = t >= 128 ? t : 128 / t * t;
-    const int64_t rpc = threads / t;
-    const size_t sums = rpc > 1 ? (size_t)threads * nv * (vec ? V : 1) * 2 * sizeof(float) : 0;
-    const size_t smem = std::max<size_t>(vec ? (size_t)kNormRing * 2 * nv * threads * 16 : 0, sums);
-    int64_t per_sm = std::min<int64_t>(kNormParts, most / threads);
+  auto ring = [&](auto kern, auto row, int n) {
+    using Row = decltype(row);
+    const NormShape s(p.cols, n);
+    p.tpr = (int)s.tpr;
+    p.ring_bytes = (int64_t)Row::bytes(s.threads);
+    const size_t sums = s.rpc > 1 ? (size_t)s.threads * 2 * Row::P * sizeof(float2) : 0;
+    const size_t smem = std::max<size_t>(2 * Row::bytes(s.threads) + Row::store_bytes(s.threads), sums);
+    int64_t per_sm = std::min<int64_t>(kNormParts, (Row::kWide ? 512 : 768) / s.threads);
     per_sm = std::max<int64_t>(1, std::min<int64_t>(per_sm, (int64_t)(220 * 1024) / (int64_t)(smem + 2048)));
-    *used = (int)std::min<int64_t>((p.rows + rpc - 1) / rpc, per_sm * (parts / kNormParts));
+    *used = (int)std::min<int64_t>((p.rows + s.rpc - 1) / s.rpc, per_sm * (parts / kNormParts));
     cudaError_t e = set_smem(kern, smem);
     if (e != cudaSuccess) return e;
-    return launch_op(kern, dim3((unsigned)*used), (unsigned)threads, smem, pdl, st, p);
+    return launch_op(kern, dim3((unsigned)*used), (unsigned)s.threads, smem, pdl, st, p);
   };
-  if (vec && units <= 256) return go(layer_norm_backward_ring_kernel<T, 1>, 1, 1024);
-  if (vec && units <= 2 * 512) return go(layer_norm_backward_ring_kernel<T, 2>, 2, 512);
-  if (!vec && units <= 4 * 256) return go(layer_norm_backward_kernel<T, 2>, 4, 1024);
-  if (!vec && units <= 16 * 512) return go(layer_norm_backward_kernel<T, 8>, 16, 512);
+#define DG_NORM_RING(ROW, n) ring(layer_norm_backward_ring_kernel<ROW>, ROW(), n)
+  if (vec) {
+    using One = AlignedRow<T, 1>;
+    using Two = AlignedRow<T, 2>;
+    if (p.cols <= 256 * V) return DG_NORM_RING(One, V);
+    if (p.cols <= 512 * 2 * V) return DG_NORM_RING(Two, 2 * V);
+  } else if (p.cols <= 512 * 16) {
+    using Few1 = RaggedRow<T, 8, 1>;
+    using Many1 = RaggedRow<T, 16, 1>;
+    if constexpr (sizeof(T) == 2) {
+      using Few2 = RaggedRow<T, 8, 2>;
+      using Many2 = RaggedRow<T, 16, 2>;
+      if (pairs_aligned<T>(p, true)) return p.cols <= 256 * 8 ? DG_NORM_RING(Few2, 8) : DG_NORM_RING(Many2, 16);
+    }
+    return p.cols <= 256 * 8 ? DG_NORM_RING(Few1, 8) : DG_NORM_RING(Many1, 16);
+  }
+#undef DG_NORM_RING
   cudaError_t e = launch_op(layer_norm_backward_long_kernel<T>, dim3((unsigned)p.rows), 1024, 0, pdl, st, p);
   if (e != cudaSuccess) return e;
   int64_t slices = p.rows < 32 ? p.rows : 32;

@@ -200,3 +200,21 @@ def test_refusals():
     odd = torch.zeros(4, 130, device="cuda", dtype=torch.bfloat16)[:, 1:129]
     with pytest.raises(dg.DGError):                # 8-bit results need 16-byte aligned rows
         dg.layer_norm(odd, torch.ones(128, device="cuda"), out_format="fp8")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,cols", [(40, 9), (700, 37), (513, 255), (300, 2047), (90, 2049), (60, 4414), (20, 7167)])
+@pytest.mark.parametrize("left,right", [(0, 0), (1, 0), (3, 2), (2, 4)])
+def test_rows_at_any_offset(rows, cols, dtype, left, right):
+    """Views whose rows start at every kind of byte offset, between NaNs that
+    must not be taken in; what lies around the results is not written."""
+    x, w, b, dy = _inputs(rows, cols, dtype, rows + cols + left)
+    def wide(t):
+        big = torch.full((rows * (left + cols + right) + left + right + 8,), float("nan"), dtype=dtype, device="cuda")
+        view = big[left:left + rows * (left + cols + right)].view(rows, -1)[:, :cols]
+        view.copy_(t)
+        return view
+    xv, dv = wide(x), wide(dy)
+    r = dg.layer_norm(xv, w.cuda(), b.cuda(), eps=EPS)
+    _check_forward(r, x, w, b)
+    _check_backward(dg.layer_norm_backward(dv, xv, w.cuda(), r.mean, r.rstd), x, w, dy, r)
