@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(256) restore_rows_kernel(const uint8_t* __rest
 // access) of rows 4i + l / 8.  The next tiles are on their way into shared
 // memory while one is worked on (rows that count as zero are filled with zeros
 // instead of being read).  The codes are read from there and decoded twice, for
-// the columns' maxima and to encode them.
+// the columns' maxima and to encode them; where the exponents allow it the
+// arithmetic is exact in pairs of halves, half as many instructions as in FP32.
 constexpr int kUseRing = 3;
 constexpr int kUseCtas = 4;
 
@@ -103,7 +104,7 @@ struct UseShared {
   uint4 codes[kUseRing][8][128];
   uint32_t words[kUseRing][128];  // the rows' scale words
   float cmax[4][128];
-  float cinv[128];
+  int cexp[128];                  // the columns' exponents
 };
 
 __global__ void __launch_bounds__(128, kUseCtas) use_cols_kernel(const uint8_t* __restrict__ q,
@@ -166,36 +167,64 @@ __global__ void __launch_bounds__(128, kUseCtas) use_cols_kernel(const uint8_t* 
     index = row_index(ahead);
     cp_async_wait<kUseRing - 1>();
     __syncwarp();  // a warp's scale words are copied by its own lanes
-    auto row_scale = [&](int i) {
-      const uint32_t w = sh.words[at][warp * 32 + 4 * i + lane / 8];
-      return (live[0] >> (4 * i + lane / 8) & 1) ? scale_of_byte((w >> (8 * (kb & 3))) & 0xFFu) : 0.0f;
-    };
+    // The warp's rows' exponents, one a lane, and their largest.
+    const uint32_t wd = sh.words[at][tid];
+    const bool on = live[0] >> lane & 1;
+    const int e_row = on ? (int)((wd >> (8 * (kb & 3))) & 0xFFu) - 127 : -1000;
+    const int e_max = __reduce_max_sync(0xffffffffu, e_row), e_min = __reduce_min_sync(0xffffffffu, on ? e_row : 1000);
+    const int e_ref = live[0] ? e_max : 0;
+    // Values relative to 2^e_ref are exact halves while the rows' exponents lie
+    // within 15 of one another: 4 significant bits from 2^-9 2^-15 to 448.
+    const bool halves = !live[0] || e_max - e_min <= 15;
     float m[16];
+    if (halves) {
+      __half2 mh[8];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) m[c] = 0.0f;
-#pragma unroll 2
-    for (int i = 0; i < 8; i += 2) {
-      const uint4 c0 = sh.codes[at][i][tid], c1 = sh.codes[at][i + 1][tid];
-      const float s0 = row_scale(i), s1 = row_scale(i + 1);
-      const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+      for (int c = 0; c < 8; ++c) mh[c] = __half2half2(__ushort_as_half(0));
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {
+        const uint4 ci = sh.codes[at][i][tid];
+        const __half2 f = half_pow2(__shfl_sync(0xffffffffu, e_row, 4 * i + lane / 8) - e_ref);
+        const uint32_t w[4] = {ci.x, ci.y, ci.z, ci.w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float f0[4], f1[4];
-        e4m3x4_to_float(w0[c], f0);
-        e4m3x4_to_float(w1[c], f1);
-#pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const float2 a = mul2(make_float2(f0[k], f0[k + 1]), s0);
-          const float2 b = mul2(make_float2(f1[k], f1[k + 1]), s1);
-          m[4 * c + k] = fmaxf(fmaxf(m[4 * c + k], fabsf(a.x)), fabsf(b.x));
-          m[4 * c + k + 1] = fmaxf(fmaxf(m[4 * c + k + 1], fabsf(a.y)), fabsf(b.y));
+        for (int c = 0; c < 4; ++c) {
+          __half2 lo, hi;
+          e4m3x4_to_half(w[c], lo, hi);
+          mh[2 * c] = __hmax2(mh[2 * c], __habs2(__hmul2(lo, f)));
+          mh[2 * c + 1] = __hmax2(mh[2 * c + 1], __habs2(__hmul2(hi, f)));
         }
       }
-    }
+      const float ref = pow2f(e_ref);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], 8));
-      m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], 16));
+      for (int c = 0; c < 8; ++c) {
+        mh[c] = __hmax2(mh[c], __shfl_xor_sync(0xffffffffu, mh[c], 8));
+        mh[c] = __hmax2(mh[c], __shfl_xor_sync(0xffffffffu, mh[c], 16));
+        const float2 v = __half22float2(mh[c]);
+        m[2 * c] = v.x * ref;
+        m[2 * c + 1] = v.y * ref;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) m[c] = 0.0f;
+#pragma unroll 2
+      for (int i = 0; i < 8; ++i) {
+        const uint4 ci = sh.codes[at][i][tid];
+        const int e = __shfl_sync(0xffffffffu, e_row, 4 * i + lane / 8);
+        const float s = e >= -127 ? pow2f(e) : 0.0f;
+        const uint32_t w[4] = {ci.x, ci.y, ci.z, ci.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float f[4];
+          e4m3x4_to_float(w[c], f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m[4 * c + k] = fmaxf(m[4 * c + k], fabsf(f[k] * s));
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], 8));
+        m[c] = fmaxf(m[c], __shfl_xor_sync(0xffffffffu, m[c], 16));
+      }
     }
     if (lane < 8) {
 #pragma unroll
@@ -206,34 +235,61 @@ __global__ void __launch_bounds__(128, kUseCtas) use_cols_kernel(const uint8_t* 
     {
       const float a = fmaxf(fmaxf(sh.cmax[0][tid], sh.cmax[1][tid]), fmaxf(sh.cmax[2][tid], sh.cmax[3][tid]));
       const uint32_t b = scale_byte(a);
-      sh.cinv[tid] = inverse_of_byte(b);
+      sh.cexp[tid] = (int)b - 127;
       store_scale_byte(sfc + (int64_t)(rb >> 2) * cols + (int64_t)kb * 128 + tid, rb, rb == rblocks - 1, b);
     }
     __syncthreads();
+    int e_col[16];
+    int least = 1000;
 #pragma unroll
     for (int c = 0; c < 16; c += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(&sh.cinv[(lane % 8) * 16 + c]);
-      m[c] = x.x;
-      m[c + 1] = x.y;
-      m[c + 2] = x.z;
-      m[c + 3] = x.w;
+      const int4 x = *reinterpret_cast<const int4*>(&sh.cexp[(lane % 8) * 16 + c]);
+      e_col[c] = x.x;
+      e_col[c + 1] = x.y;
+      e_col[c + 2] = x.z;
+      e_col[c + 3] = x.w;
+      least = min(min(least, min(x.x, x.y)), min(x.z, x.w));
     }
     uint8_t* dst = qc + ((int64_t)rb * 128 + warp * 32 + lane / 8) * cols + (int64_t)kb * 128 + (lane % 8) * 16;
-#pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-      const uint4 ci = sh.codes[at][i][tid];
-      const float si = row_scale(i);
-      uint32_t w[4] = {ci.x, ci.y, ci.z, ci.w};
+    // A column's factor 2^(e_ref - e_col) is a half up to 2^15.  Below 2^-24 it
+    // becomes 0, as its products, at most 448 2^-25, do in E4M3; and a product
+    // that still reaches a code (2^-10) has all its bits above 2^-24.
+    if (halves && __all_sync(0xffffffffu, e_ref - least <= 15)) {
+      __half2 f2[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float f[4];
-        e4m3x4_to_float(w[c], f);
-        const float2 a = mul2(mul2(make_float2(f[0], f[1]), si), make_float2(m[4 * c], m[4 * c + 1]));
-        const float2 b = mul2(mul2(make_float2(f[2], f[3]), si), make_float2(m[4 * c + 2], m[4 * c + 3]));
-        w[c] = e4m3x4(a, b);
+      for (int c = 0; c < 8; ++c)
+        f2[c] = __halves2half2(__low2half(half_pow2(e_ref - e_col[2 * c])), __low2half(half_pow2(e_ref - e_col[2 * c + 1])));
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {
+        const uint4 ci = sh.codes[at][i][tid];
+        const __half2 f = half_pow2(__shfl_sync(0xffffffffu, e_row, 4 * i + lane / 8) - e_ref);
+        uint32_t w[4] = {ci.x, ci.y, ci.z, ci.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          __half2 lo, hi;
+          e4m3x4_to_half(w[c], lo, hi);
+          w[c] = half_to_e4m3x4(__hmul2(__hmul2(lo, f), f2[2 * c]), __hmul2(__hmul2(hi, f), f2[2 * c + 1]));
+        }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        dst += 4 * cols;
       }
-      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-      dst += 4 * cols;
+    } else {
+#pragma unroll 2
+      for (int i = 0; i < 8; ++i) {
+        const uint4 ci = sh.codes[at][i][tid];
+        const int e = __shfl_sync(0xffffffffu, e_row, 4 * i + lane / 8);
+        const float s = e >= -127 ? pow2f(e) : 0.0f;
+        uint32_t w[4] = {ci.x, ci.y, ci.z, ci.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float f[4];
+          e4m3x4_to_float(w[c], f);
+          w[c] = e4m3x4(f[0] * s * pow2f(-e_col[4 * c]), f[1] * s * pow2f(-e_col[4 * c + 1]),
+                        f[2] * s * pow2f(-e_col[4 * c + 2]), f[3] * s * pow2f(-e_col[4 * c + 3]));
+        }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        dst += 4 * cols;
+      }
     }
     __syncwarp();  // every lane has read its words before the slot is filled again
     if (++at == kUseRing) at = 0;

@@ -78,8 +78,8 @@ __device__ __forceinline__ uint32_t abs_bits_max4(float a, float b, float c, flo
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return (uint32_t)cvt_e4m3x2(a, b) | ((uint32_t)cvt_e4m3x2(c, d) << 16);
 }
-// Four E4M3 codes -> FP32, exactly (every E4M3 value is a half).
-__device__ __forceinline__ void e4m3x4_to_float(uint32_t codes, float (&f)[4]) {
+// Four E4M3 codes -> halves and FP32, exactly (every E4M3 value is a half).
+__device__ __forceinline__ void e4m3x4_to_half(uint32_t codes, __half2& a, __half2& b) {
   uint32_t lo, hi;
   asm("{\n\t.reg .b16 l, h;\n\t"
       "mov.b32 {l, h}, %2;\n\t"
@@ -87,8 +87,31 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t codes, float (&f)[4]) {
       "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(codes));
-  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
+  a = *reinterpret_cast<__half2*>(&lo);
+  b = *reinterpret_cast<__half2*>(&hi);
+}
+// Four halves -> E4M3 codes, rounded to nearest even.
+__device__ __forceinline__ uint32_t half_to_e4m3x4(__half2 a, __half2 b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "r"(*reinterpret_cast<uint32_t*>(&a)), "r"(*reinterpret_cast<uint32_t*>(&b)));
+  return r;
+}
+// (2^k, 2^k) for k <= 15, 0 below 2^-24.
+__device__ __forceinline__ __half2 half_pow2(int k) {
+  const uint32_t h = k >= -14 ? (uint32_t)(k + 15) << 10 : (k >= -24 ? 1u << (k + 24) : 0u);
+  const uint32_t w = h * 0x10001u;
+  return *reinterpret_cast<const __half2*>(&w);
+}
+__device__ __forceinline__ void e4m3x4_to_float(uint32_t codes, float (&f)[4]) {
+  __half2 lo, hi;
+  e4m3x4_to_half(codes, lo, hi);
+  const float2 a = __half22float2(lo);
+  const float2 b = __half22float2(hi);
   f[0] = a.x;
   f[1] = a.y;
   f[2] = b.x;

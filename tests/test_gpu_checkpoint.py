@@ -171,3 +171,27 @@ def test_refusals():
         dg.dequantize_fp8(q, sf, dtype=torch.float16)
     with pytest.raises(ValueError):
         dg.requantize_fp8_cols(q.cpu(), sf)
+
+
+@pytest.mark.parametrize("spread", [0, 4, 15, 16, 30])
+def test_use_at_the_edges_of_exact_halves(spread):
+    """Rows whose scales lie `spread` powers of two apart, and columns that hold
+    nothing but the smallest codes (their scale is 2^17 below the rows')."""
+    g = torch.Generator().manual_seed(spread)
+    codes = torch.randint(0, 0x7F, (300, 256), generator=g, dtype=torch.uint8)
+    codes |= torch.randint(0, 2, codes.shape, generator=g, dtype=torch.uint8) * 128
+    codes[:, 5] = 1                     # 2^-9
+    codes[:, 6] = 0
+    codes[7, 6] = 0x83                  # one subnormal in an empty column
+    codes[:, 9] = 0x7E                  # 448
+    e = torch.randint(-20, -20 + spread + 1, (300, 2), generator=g)
+    words = torch.zeros(1, 300, 4, dtype=torch.uint8)
+    words[0, :, :2] = (e + 127).to(torch.uint8)
+    sf = words.view(torch.int32).squeeze(-1)
+    q = codes.cuda().view(torch.float8_e4m3fn)
+    qc, sfc = dg.requantize_fp8_cols(q, sf.cuda())
+    v = np.zeros((384, 256), dtype=np.float32)
+    v[:300] = R.row_values(codes.numpy(), sf.numpy())
+    oq, oe, _ = oracle.quantize_cols(v)
+    assert np.array_equal(_bytes(qc), oq)
+    assert np.array_equal(sfc.cpu().numpy(), dg_pack_cols(oe, 256))
