@@ -474,13 +474,14 @@ dg_status dg_layer_norm_backward_workspace_size(int64_t cols, int32_t num_sms, u
  * changes, not on every call), all optional, for tuning and diagnosis:
  *   DG_PRINT_CONFIGS=1   print each launch's configuration to stderr;
  *   DG_BLOCK_M=128|256, DG_BLOCK_N=128|192|224|256   force the tile size;
- *   DG_SPLIT_K=1|2|4|8   force the split-K cluster size (8: decode kernel);
+ *   DG_SPLIT_K=1|2|4|8   force the split-K cluster size (8: decode kernels);
  *   DG_CTA_PAIR=1        256-row tiles on 2-CTA pairs (cta_group::2 MMAs);
  *   DG_STREAM_K=0|1      forbid / force stream-K where a workspace allows it;
  *   DG_MULTICAST=0       256-row dense tiles and K-grouped tiles one CTA each
  *                        instead of 2-CTA clusters sharing B by TMA multicast;
  *   DG_TALL_EPI8=0       four epilogue warps for 256-row tiles instead of eight;
- *   DG_DECODE=0          tiled kernels instead of the decode kernel for M <= 128;
+ *   DG_DECODE=0          tiled kernels instead of the decode kernels for M <= 128;
+ *                        2: the gated product of one to four tokens as of more;
  *   DG_RASTER_BAND=n     M blocks per raster band (default 16).
  * Tile sizes and multicast clusters give the same bits: each output element
  * accumulates its K blocks in the same order (tested for 128- against

@@ -30,7 +30,7 @@ FLOOR_SRC = os.path.join(CSRC, "hbm_floor.cu")
 
 SOURCES = ["gemm_bn128.cu", "gemm_bn192.cu", "gemm_bn224.cu", "gemm_bn256.cu",
            "gemm2_bn192.cu", "gemm2_bn224.cu", "gemm2_bn256.cu", "gemm_splitk.cu", "gemm_tall.cu", "gemm_promote.cu", "gemm_decode.cu", "gemm_kgrouped.cu", "gemm.cu",
-           "quant.cu", "checkpoint.cu", "gated_gemm.cu", "gated_decode.cu", "gated_backward.cu", "layer_norm.cu", "host.cu", "static_ws.cu"]
+           "quant.cu", "checkpoint.cu", "gated_gemm.cu", "gated_decode.cu", "gated_gemv.cu", "gated_backward.cu", "layer_norm.cu", "host.cu", "static_ws.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -32,4 +32,10 @@ cudaError_t gated_decode_launch(int tn, int split, const CUtensorMap& a, const C
 int gated_decode_max_packs();
 int gated_decode_max_clusters(int tn, int split);  // that run at once on the current device
 
+
+// gated_gemv.cu: one to four tokens without the tensor cores
+bool gated_gemv_takes(int64_t m, int64_t f, int64_t k, bool eight_bit, int sms);
+cudaError_t gated_gemv_launch(const void* a, const void* sfa, const void* b, const void* sfb, int64_t lda, int64_t ldb,
+                              const GatedArgs& args, cudaStream_t stream);
+
 }  // namespace dg

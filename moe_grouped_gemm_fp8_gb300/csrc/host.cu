@@ -1449,6 +1449,31 @@ static dg_status gated_gemm(int mode, const char* name, const void* a, const int
   args.base.k_blocks = (int32_t)(k / kBlockK);
   const int64_t tiles = (int64_t)args.base.m_blocks * args.base.n_blocks;
   if (tiles * (mode == kMasked ? groups : 1) >= kMaxCoord) return DG_ERR_TOO_LARGE;
+  args.base.m = (int32_t)m;
+  args.base.n = (int32_t)f;
+  args.base.k = (int32_t)k;
+  args.base.num_groups = groups;
+  args.base.m_indices = mode == kContiguous ? rows : nullptr;
+  args.base.masked_m = mode == kMasked ? rows : nullptr;
+  args.base.band = raster_band(args.base.m_blocks, kBlockM, k);
+  args.base.timeout_ns = g_timeout_ns.load();
+  args.base.pdl = g_pdl.load();
+  args.base.debug_drop_load = mode == kDense ? g_debug_drop_load.load() : 0;
+  args.h = h_sf ? nullptr : static_cast<__nv_bfloat16*>(h);
+  args.hq = h_sf ? static_cast<uint8_t*>(h) : nullptr;
+  args.hsf = reinterpret_cast<uint32_t*>(h_sf);
+  args.cq = static_cast<uint8_t*>(gu);
+  args.csf = reinterpret_cast<uint32_t*>(gu_sf);
+  args.ldh = ldh;
+  args.f = (int32_t)f;
+  args.m_pad = (int32_t)align4(m);
+  args.activation = activation;
+  // one to four tokens: without the tensor cores (test hooks of the pipelines want one of those)
+  if (mode == kDense && env().decode != 0 && env().decode != 2 && args.base.debug_drop_load == 0 &&
+      gated_gemv_takes(m, f, k, h_sf || gu, sms)) {
+    print_config("fp8_gated_gemm_nt (one to four tokens)", m, f, k, 1, (int)m, 16, 0, (int)((f + 15) / 16), 0);
+    return from_cuda(gated_gemv_launch(a, sfa, b, sfb, lda, ldb, args, static_cast<cudaStream_t>(stream)));
+  }
   // a few tokens: the kernel with swapped operand roles, whose clusters split K
   const bool few = mode == kDense && m <= kBlockM && env().decode != 0;
   const int tn = m <= 32 ? 32 : 64;
@@ -1474,25 +1499,6 @@ static dg_status gated_gemm(int mode, const char* name, const void* a, const int
     return s;
   // Wg's and Wu's 128 rows of a tile are two boxes of one map
   if (split == 0 && (s = encode_b_side(o, b, sfb, groups, 2 * f, k, ldb, 128, 128)) != DG_OK) return s;
-  args.base.m = (int32_t)m;
-  args.base.n = (int32_t)f;
-  args.base.k = (int32_t)k;
-  args.base.num_groups = groups;
-  args.base.m_indices = mode == kContiguous ? rows : nullptr;
-  args.base.masked_m = mode == kMasked ? rows : nullptr;
-  args.base.band = raster_band(args.base.m_blocks, kBlockM, k);
-  args.base.timeout_ns = g_timeout_ns.load();
-  args.base.pdl = g_pdl.load();
-  args.base.debug_drop_load = mode == kDense ? g_debug_drop_load.load() : 0;
-  args.h = h_sf ? nullptr : static_cast<__nv_bfloat16*>(h);
-  args.hq = h_sf ? static_cast<uint8_t*>(h) : nullptr;
-  args.hsf = reinterpret_cast<uint32_t*>(h_sf);
-  args.cq = static_cast<uint8_t*>(gu);
-  args.csf = reinterpret_cast<uint32_t*>(gu_sf);
-  args.ldh = ldh;
-  args.f = (int32_t)f;
-  args.m_pad = (int32_t)align4(m);
-  args.activation = activation;
   if (split > 0) {
     print_config("fp8_gated_gemm_nt (few tokens, swapped operands)", m, f, k, 1, tn, 128, split,
                  args.base.n_blocks * split * token_blocks, 0);

@@ -288,14 +288,16 @@ def test_refusals():
 
 
 @pytest.mark.parametrize("out_format,checkpoint", [("bf16", False), ("fp8", True)])
-@pytest.mark.parametrize("m,f,k", [(1, 128, 128), (3, 128, 7168), (17, 256, 4224), (32, 2048, 512), (33, 128, 1408),
+@pytest.mark.parametrize("m,f,k", [(1, 128, 128), (1, 2048, 7168), (1, 384, 16512), (2, 640, 7168), (2, 256, 1024),
+                                   (3, 128, 7168), (4, 384, 1920), (3, 1024, 640), (17, 256, 4224), (32, 2048, 512), (33, 128, 1408),
                                    (64, 384, 2048), (65, 256, 896), (100, 1024, 640), (128, 128, 256)])
 def test_few_tokens_agree_with_the_tiled_kernel(m, f, k, out_format, checkpoint, monkeypatch):
-    """The kernel for a few tokens (K split over clusters) and the tiled one,
-    each against FP64; K ranges that do and do not divide among the CTAs."""
+    """The kernels for one to four tokens, for a few (K split over clusters) and
+    the tiled one, each against FP64; K ranges that do and do not divide among
+    the CTAs."""
     q, sf, qw, sw = _operands(m, f, k, m + f + k + 2)
     x, w = R.row_values(_np(q), _np(sf)), _weights(qw, sw)
-    for decode in ("1", "0"):
+    for decode in ("1", "2", "0"):
         monkeypatch.setenv("DG_DECODE", decode)
         _check(dg.fp8_gated_gemm_nt(q, sf, qw, sw, out_format=out_format, checkpoint=checkpoint), x, w, "silu")
         assert dg.get_device_error()[0] == 0
@@ -317,3 +319,19 @@ def test_few_tokens_with_a_load_that_never_lands():
     assert dg.get_device_error()[0] == 0
     assert all(np.array_equal(_np(x), _np(y)) for x, y in zip(again, want))
 
+
+
+@pytest.mark.parametrize("m", [1, 2, 4])
+def test_one_to_four_strided_tokens(m):
+    """Row strides of A, W and h other than their widths, F not a multiple of
+    the 16 columns of a CTA."""
+    f, k = 200, 640
+    q, sf, qw, sw = _operands(m, f, k, 40 + m)
+    aw = torch.full((m, k + 48), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    aw[:, :k].copy_(q)
+    bw = torch.full((2 * f, k + 16), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    bw[:, :k].copy_(qw)
+    d = torch.full((m, f + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = dg.fp8_gated_gemm_nt(aw[:, :k], sf, bw[:, :k], sw, d=d[:, :f], activation="gelu_tanh")
+    assert bool((d[:, f:] == 7).all())
+    _check(out, R.row_values(_np(q), _np(sf)), _weights(qw, sw), "gelu_tanh")
