@@ -17,6 +17,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "dg_device.cuh"
 #include "dg_ops.cuh"
@@ -32,6 +33,40 @@ template <class T> __device__ __forceinline__ T from_float(float v);
 template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+
+// Two neighbouring 16-bit elements in one word, as FP32 and back.
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return make_float2(bf16_lo(w), bf16_hi(w));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return bf16x2_bits(v.x, v.y);
+  else {
+    const __half2 h = __float22half2_rn(v);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+// 16 bytes as pairs of FP32 and back.
+template <class T>
+__device__ __forceinline__ void unpack16(const uint4& a, float2* v) {
+  if constexpr (sizeof(T) == 4) {
+    v[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+    v[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+  } else {
+    v[0] = unpack2<T>(a.x);
+    v[1] = unpack2<T>(a.y);
+    v[2] = unpack2<T>(a.z);
+    v[3] = unpack2<T>(a.w);
+  }
+}
+template <class T>
+__device__ __forceinline__ uint4 pack16(const float2* v) {
+  if constexpr (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+  else return make_uint4(pack2<T>(v[0]), pack2<T>(v[1]), pack2<T>(v[2]), pack2<T>(v[3]));
+}
 
 // VEC elements as one access of VEC * sizeof(T) bytes (16, or one element).
 // Rows are read once: they are kept out of L1, which holds weight and bias.
@@ -368,10 +403,7 @@ struct AlignedRow {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint4 a = mine[s * stage + place(lane * NV + j)];
-      const T* e = reinterpret_cast<const T*>(&a);
-#pragma unroll
-      for (int k = 0; k < V / 2; ++k) v[j * V / 2 + k] = make_float2(to_float(e[2 * k]), to_float(e[2 * k + 1]));
+      unpack16<T>(mine[s * stage + place(lane * NV + j)], &v[j * V / 2]);
     }
   }
   __device__ __forceinline__ void params(const void* p, bool fp32, bool wide, float2 (&v)[P]) const {
@@ -397,26 +429,18 @@ struct AlignedRow {
   // Into the row at y; `wide`: rows start on 32 bytes, so two pieces are one access.
   __device__ __forceinline__ void store(T* y, bool wide, void*, const float2 (&v)[P]) const {
     y += c;
-    uint32_t w[NV][4];
+    uint4 w[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      T* e = reinterpret_cast<T*>(w[j]);
-#pragma unroll
-      for (int k = 0; k < V / 2; ++k) {
-        e[2 * k] = from_float<T>(v[j * V / 2 + k].x);
-        e[2 * k + 1] = from_float<T>(v[j * V / 2 + k].y);
-      }
-    }
+    for (int j = 0; j < NV; ++j) w[j] = pack16<T>(&v[j * V / 2]);
     if (NV == 2 && wide && on == 3u) {
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y), "r"(w[0][0]), "r"(w[0][1]),
-                   "r"(w[0][2]), "r"(w[0][3]), "r"(w[NV - 1][0]), "r"(w[NV - 1][1]), "r"(w[NV - 1][2]),
-                   "r"(w[NV - 1][3])
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y), "r"(w[0].x), "r"(w[0].y),
+                   "r"(w[0].z), "r"(w[0].w), "r"(w[NV - 1].x), "r"(w[NV - 1].y), "r"(w[NV - 1].z), "r"(w[NV - 1].w)
                    : "memory");
       return;
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (on >> j & 1) *reinterpret_cast<uint4*>(y + j * V) = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+      if (on >> j & 1) *reinterpret_cast<uint4*>(y + j * V) = w[j];
   }
   // A column sum per pair element.
   __device__ __forceinline__ void store_sums(float* out, const float2 (&v)[P]) const {
@@ -501,9 +525,7 @@ struct RaggedRow {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       if constexpr (G == 2) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p + (k * 32 + lane) * 4);
-        const T* e = reinterpret_cast<const T*>(&w);
-        v[k] = make_float2(to_float(e[0]), to_float(e[1]));
+        v[k] = unpack2<T>(*reinterpret_cast<const uint32_t*>(p + (k * 32 + lane) * 4));
       } else {
         v[k] = make_float2(to_float(*reinterpret_cast<const T*>(p + (2 * k * 32 + lane) * kSize)),
                            to_float(*reinterpret_cast<const T*>(p + ((2 * k + 1) * 32 + lane) * kSize)));
@@ -545,11 +567,7 @@ struct RaggedRow {
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       if constexpr (G == 2) {
-        uint32_t w;
-        T* e = reinterpret_cast<T*>(&w);
-        e[0] = from_float<T>(v[k].x);
-        e[1] = from_float<T>(v[k].y);
-        *reinterpret_cast<uint32_t*>(p + skip + (k * 32 + lane) * 4) = w;
+        *reinterpret_cast<uint32_t*>(p + skip + (k * 32 + lane) * 4) = pack2<T>(v[k]);
       } else {
         *reinterpret_cast<T*>(p + skip + (2 * k * 32 + lane) * kSize) = from_float<T>(v[k].x);
         *reinterpret_cast<T*>(p + skip + ((2 * k + 1) * 32 + lane) * kSize) = from_float<T>(v[k].y);
@@ -659,8 +677,24 @@ __global__ void __launch_bounds__(Row::kWide ? 448 : 256, Row::kWide ? 2 : 4)
         else if constexpr (E == 8) *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
         else *reinterpret_cast<uint32_t*>(q) = o[0];
       }
-      if (c < cols && c % 128 == 0 && row < rows)
-        store_scale_byte(p.sf + (int64_t)(c / 512) * p.rows_pad + row, c / 128, c + 128 == cols, in ? e : 0u);
+      // the warp's 32 E columns are a whole scale word (E = 16), a half or a
+      // byte of one; the row's last warp zeroes what its word has left
+      constexpr int G = 128 / E, B = E / 4;  // lanes of a group, bytes of the warp
+      const int block = (c - (int)(threadIdx.x & 31) * E) / 128;
+      const uint32_t part = __reduce_or_sync(
+          0xffffffffu, in && c < cols && (threadIdx.x & 31) % G == 0 ? e << (8 * ((threadIdx.x & 31) / G)) : 0u);
+      if ((threadIdx.x & 31) == 0 && c < cols && row < rows) {
+        uint32_t* word = p.sf + (int64_t)(block >> 2) * p.rows_pad + row;
+        if constexpr (B == 4) {
+          *word = part;
+        } else {
+          uint8_t* to = reinterpret_cast<uint8_t*>(word) + (block & 3);
+          if constexpr (B == 2) *reinterpret_cast<uint16_t*>(to) = (uint16_t)part;
+          else *to = (uint8_t)part;
+          if (c + 32 * E >= cols)
+            for (int i = (block & 3) + B; i < 4; ++i) to[i - (block & 3)] = 0;
+        }
+      }
     }
     row += step;
   }
