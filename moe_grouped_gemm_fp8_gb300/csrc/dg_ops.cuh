@@ -31,12 +31,6 @@ __device__ __forceinline__ uint4 ld_stream_u4(const void* p) {
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
 // The first `bytes` (1 to 16) of them, zeros after.
 __device__ __forceinline__ void cp_async16_part(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
@@ -66,12 +60,6 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// Magnitudes compare as unsigned integers of their bits (NaN above all).
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-__device__ __forceinline__ uint32_t abs_bits_max4(float a, float b, float c, float d) {
-  return max(max(abs_bits(a), abs_bits(b)), max(abs_bits(c), abs_bits(d)));
 }
 
 // Four values (already divided by their scale) -> four E4M3 codes, first lowest.
@@ -172,7 +160,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// act(g) and act'(g).  The logistic function uses the fast exponential and
+// The logistic function uses the fast exponential and
 // reciprocal: together about 2^-21 relative, well below the 2^-9 (BF16) or
 // 2^-4 (E4M3) at which every result of these kernels is rounded.  For large
 // negative g exp(-g) is inf and s is 0, so silu and its derivative are 0.
@@ -192,19 +180,7 @@ template <int ACT>
 __device__ __forceinline__ float gate_act(float g) {
   return g * gate_logistic<ACT>(g);
 }
-template <int ACT>
-__device__ __forceinline__ void gate_act_grad(float g, float& a, float& da) {
-  const float s = gate_logistic<ACT>(g);
-  a = g * s;
-  if constexpr (ACT == DG_ACT_SILU) {
-    da = s + a * (1.0f - s);
-  } else {
-    constexpr float c2 = 1.5957691216057308f;
-    da = s + a * (1.0f - s) * (c2 + (3.0f * c2 * 0.044715f) * g * g);
-  }
-}
-
-// The same for a pair: a and act'.
+// act(g) and act'(g) of a pair.
 template <int ACT>
 __device__ __forceinline__ void gate_act_grad2(float2 g, float2& a, float2& da) {
   float2 z = g;  // logistic's argument times -log2(e)
