@@ -28,8 +28,19 @@ __device__ __forceinline__ uint4 ld_stream_u4(const void* p) {
 }
 
 // Asynchronous 16-byte copy into shared memory, past L1, in groups.
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {  // dst: a shared address
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+// 32 bytes as one access (32-byte aligned).
+__device__ __forceinline__ void st_global_32(void* p, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
 // The first `bytes` (1 to 16) of them, zeros after.
 __device__ __forceinline__ void cp_async16_part(void* dst, const void* src, int bytes) {
@@ -64,7 +75,14 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
 
 // Four values (already divided by their scale) -> four E4M3 codes, first lowest.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  return (uint32_t)cvt_e4m3x2(a, b) | ((uint32_t)cvt_e4m3x2(c, d) << 16);
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 // Four E4M3 codes -> halves and FP32, exactly (every E4M3 value is a half).
 __device__ __forceinline__ void e4m3x4_to_half(uint32_t codes, __half2& a, __half2& b) {
@@ -120,10 +138,12 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 mul2(float2 a, float b) { return __fmul2_rn(a, make_float2(b, b)); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float abs_max2(float m, float2 a) { return fmaxf(fmaxf(m, fabsf(a.x)), fabsf(a.y)); }
-__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
-  return (uint32_t)cvt_e4m3x2(a.x, a.y) | ((uint32_t)cvt_e4m3x2(b.x, b.y) << 16);
+__device__ __forceinline__ float abs_max2(float m, float2 a) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a.x)), "f"(fabsf(a.y)));
+  return r;
 }
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) { return e4m3x4(a.x, a.y, b.x, b.y); }
 // Two FP32 sums over the warp in one butterfly: lanes 0-15 end with a's, lanes
 // 16-31 with b's.
 __device__ __forceinline__ float warp_sum2(float a, float b) {
@@ -202,11 +222,12 @@ __device__ __forceinline__ void gate_act_grad2(float2 g, float2& a, float2& da) 
   da = fma2(a, t, s);
 }
 
-// Raises a kernel's dynamic shared-memory limit where it needs more than 48 KB.
+// Raises a kernel's dynamic shared-memory limit where it may need more than
+// 48 KB with the (few) bytes of its static arrays.
 // Set on every such launch: the call only writes a field of the function's state.
 template <class Kern>
 static cudaError_t set_smem(Kern kern, size_t smem) {
-  if (smem <= 48 * 1024) return cudaSuccess;
+  if (smem <= 40 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
