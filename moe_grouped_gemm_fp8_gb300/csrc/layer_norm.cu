@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kWideThreads) layer_norm_wide_kernel(const Lay
 // Rows of whole, 16-byte aligned pieces.  A warp's share is 32 NV pieces, copied
 // by its lanes side by side and read back as each lane's own NV neighbouring
 // pieces (stored crosswise so that 8 lanes meet no bank twice): they hold whole
-groups' maxima in few lanes, and the E4M3 codes leave 32 bytes a lane.
+// groups' maxima in few lanes, and the E4M3 codes leave 32 bytes a lane.
 // Pieces past the row are never copied and stay zero; rows past the last leave
 // what was there.
 template <class T_, int NV_>
