@@ -138,11 +138,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 mul2(float2 a, float b) { return __fmul2_rn(a, make_float2(b, b)); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float abs_max2(float m, float2 a) {
+// max(|m|, |a|, |b|)
+__device__ __forceinline__ float abs_max3(float m, float a, float b) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a.x)), "f"(fabsf(a.y)));
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float abs_max2(float m, float2 a) { return abs_max3(m, a.x, a.y); }
 __device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) { return e4m3x4(a.x, a.y, b.x, b.y); }
 // Two FP32 sums over the warp in one butterfly: lanes 0-15 end with a's, lanes
 // 16-31 with b's.

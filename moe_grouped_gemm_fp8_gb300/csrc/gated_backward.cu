@@ -188,12 +188,12 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
     for (int i = 0; i < 8; i += 2)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        mg[2 * c] = fmaxf(fmaxf(mg[2 * c], fabsf(dg[i][c].x)), fabsf(dg[i + 1][c].x));
-        mg[2 * c + 1] = fmaxf(fmaxf(mg[2 * c + 1], fabsf(dg[i][c].y)), fabsf(dg[i + 1][c].y));
-        mu[2 * c] = fmaxf(fmaxf(mu[2 * c], fabsf(du[i][c].x)), fabsf(du[i + 1][c].x));
-        mu[2 * c + 1] = fmaxf(fmaxf(mu[2 * c + 1], fabsf(du[i][c].y)), fabsf(du[i + 1][c].y));
-        mh[2 * c] = fmaxf(fmaxf(mh[2 * c], fabsf(h[i][c].x)), fabsf(h[i + 1][c].x));
-        mh[2 * c + 1] = fmaxf(fmaxf(mh[2 * c + 1], fabsf(h[i][c].y)), fabsf(h[i + 1][c].y));
+        mg[2 * c] = abs_max3(mg[2 * c], dg[i][c].x, dg[i + 1][c].x);
+        mg[2 * c + 1] = abs_max3(mg[2 * c + 1], dg[i][c].y, dg[i + 1][c].y);
+        mu[2 * c] = abs_max3(mu[2 * c], du[i][c].x, du[i + 1][c].x);
+        mu[2 * c + 1] = abs_max3(mu[2 * c + 1], du[i][c].y, du[i + 1][c].y);
+        mh[2 * c] = abs_max3(mh[2 * c], h[i][c].x, h[i + 1][c].x);
+        mh[2 * c + 1] = abs_max3(mh[2 * c + 1], h[i][c].y, h[i + 1][c].y);
       }
     sh.cmax[0][warp][lane] = make_float4(mg[0], mg[1], mg[2], mg[3]);
     sh.cmax[1][warp][lane] = make_float4(mu[0], mu[1], mu[2], mu[3]);
