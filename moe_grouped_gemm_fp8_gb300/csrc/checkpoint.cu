@@ -21,15 +21,16 @@
 namespace dg {
 namespace {
 
-// One warp per (group, pair of rows, 512-column pack), lane l on columns 4l ..
-// 4l+3 of each 128-column block; warps ordered row-fastest so that the scale
-// words of neighbouring warps are adjacent.  Both rows' loads are in flight
-// together: 4096 x 7168 in 14.4 us (6.1 TB/s), a row a warp 17.9.
+// One warp per (group, pair of rows, 512-column pack), lane l on columns 16l ..
+// 16l+15, so a 128-column group is eight lanes and a scale word one store; warps
+// ordered row-fastest so that the scale words of neighbouring warps are adjacent.
+// Both rows' loads are in flight together: 16384 x 7168 in 56 us (6.3 TB/s), 4096
+// x 7168 in 12.5, where a row a warp took 17.9.
 __global__ void __launch_bounds__(256) save_rows_kernel(const __nv_bfloat16* __restrict__ x,
                                                         uint8_t* __restrict__ q,
                                                         uint32_t* __restrict__ sf, int64_t groups,
                                                         int64_t rows, int64_t rows_pad,
-                                                        int64_t cols, int kblocks, int kpacks) {
+                                                        int64_t cols, int kpacks) {
   griddep_wait();
   griddep_launch_dependents();
   const int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
@@ -39,61 +40,100 @@ __global__ void __launch_bounds__(256) save_rows_kernel(const __nv_bfloat16* __r
   const int64_t r0 = w % pairs * 2;
   const int64_t j = (w / pairs) % kpacks;
   const int64_t g = w / (pairs * kpacks);
-  const int64_t at = (g * rows + r0) * cols + 4 * j * 128 + lane * 4;
-  uint2 v[2][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (r0 + i < rows && 4 * j + t < kblocks) v[i][t] = ld_stream_u2(x + at + i * cols + t * 128);
+  const int64_t c = j * 512 + lane * 16;
+  const int64_t at = (g * rows + r0) * cols + c;
+  uint4 v[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t word = 0;
-    if (r0 + i < rows) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (4 * j + t >= kblocks) break;
-        const float2 a = make_float2(bf16_lo(v[i][t].x), bf16_hi(v[i][t].x));
-        const float2 b = make_float2(bf16_lo(v[i][t].y), bf16_hi(v[i][t].y));
-        const float m = abs_max2(abs_max2(0.0f, a), b);
-        const uint32_t e = scale_byte(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m))));
-        const float inv = inverse_of_byte(e);
-        *reinterpret_cast<uint32_t*>(q + at + i * cols + t * 128) = e4m3x4(mul2(a, inv), mul2(b, inv));
-        word |= e << (8 * t);
-      }
+    v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+    if (r0 + i < rows && c < cols) {
+      v[i][0] = ld_stream_u4(x + at + i * cols);
+      v[i][1] = ld_stream_u4(x + at + i * cols + 8);
     }
-    if (lane == 0) sf[(g * kpacks + j) * rows_pad + r0 + i] = word;
   }
+  uint32_t word[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t raw[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+    float2 f[8];
+    float m = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      f[k] = make_float2(bf16_lo(raw[k]), bf16_hi(raw[k]));
+      m = abs_max2(m, f[k]);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const uint32_t e = scale_byte(m);
+    const bool in = r0 + i < rows && c < cols;
+    if (in) {
+      const float inv = inverse_of_byte(e);
+      *reinterpret_cast<uint4*>(q + at + i * cols) =
+          make_uint4(e4m3x4(mul2(f[0], inv), mul2(f[1], inv)), e4m3x4(mul2(f[2], inv), mul2(f[3], inv)),
+                     e4m3x4(mul2(f[4], inv), mul2(f[5], inv)), e4m3x4(mul2(f[6], inv), mul2(f[7], inv)));
+    }
+    word[i] = __reduce_or_sync(0xffffffffu, in ? e << (8 * (lane / 8)) : 0u);
+  }
+  if (lane == 0) *reinterpret_cast<uint2*>(sf + (g * kpacks + j) * rows_pad + r0) = make_uint2(word[0], word[1]);
 }
 
-// Same walk; each lane turns 4 codes of each block into BF16 or FP32.
+// One warp per (group, four rows, 512-column pack), lane l on columns 16l .. 16l+15
+// of each row: 16 bytes of codes in, 32 or 64 of values out, all four rows' loads
+// in flight together.  16384 x 7168 to BF16 in 55.5 us (6.3 TB/s), to
+// FP32 in 90 (6.5 TB/s); a row a warp, four codes a lane at a time, took 89 and 115.
 template <class OUT>
 __global__ void __launch_bounds__(256) restore_rows_kernel(const uint8_t* __restrict__ q,
                                                            const uint32_t* __restrict__ sf,
                                                            OUT* __restrict__ x, int64_t groups,
                                                            int64_t rows, int64_t rows_pad,
-                                                           int64_t cols, int kblocks, int kpacks) {
+                                                           int64_t cols, int kpacks, bool wide) {
   griddep_wait();
   griddep_launch_dependents();
   const int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  if (w >= groups * rows * kpacks) return;
-  const int64_t r = w % rows;
-  const int64_t j = (w / rows) % kpacks;
-  const int64_t g = w / (rows * kpacks);
-  const uint32_t word = __ldg(sf + (g * kpacks + j) * rows_pad + r);
-  const int64_t at = (g * rows + r) * cols + 4 * j * 128 + lane * 4;
+  const int64_t quads = rows_pad / 4;
+  if (w >= groups * quads * kpacks) return;
+  const int64_t r0 = w % quads * 4;
+  const int64_t j = (w / quads) % kpacks;
+  const int64_t g = w / (quads * kpacks);
+  const int64_t c = j * 512 + lane * 16;
+  if (c >= cols) return;
+  const int64_t at = (g * rows + r0) * cols + c;
+  const uint4 words = __ldg(reinterpret_cast<const uint4*>(sf + (g * kpacks + j) * rows_pad + r0));
+  const uint32_t word[4] = {words.x, words.y, words.z, words.w};
+  uint4 v[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    if (4 * j + t >= kblocks) break;
-    const float s = scale_of_byte((word >> (8 * t)) & 0xFFu);
-    float f[4];
-    e4m3x4_to_float(__ldg(reinterpret_cast<const uint32_t*>(q + at + t * 128)), f);
-    if constexpr (sizeof(OUT) == 4) {
-      *reinterpret_cast<float4*>(x + at + t * 128) = make_float4(f[0] * s, f[1] * s, f[2] * s, f[3] * s);
-    } else {
-      *reinterpret_cast<uint2*>(x + at + t * 128) =
-          make_uint2(bf16x2_bits(f[0] * s, f[1] * s), bf16x2_bits(f[2] * s, f[3] * s));
+  for (int i = 0; i < 4; ++i)
+    if (r0 + i < rows) v[i] = ld_stream_u4(q + at + i * cols);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (r0 + i >= rows) break;
+    const float s = scale_of_byte((word[i] >> (8 * (lane / 8))) & 0xFFu);
+    const uint32_t codes[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint4 out[sizeof(OUT)];  // 16 values
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float f[4];
+      e4m3x4_to_float(codes[t], f);
+      if constexpr (sizeof(OUT) == 4) {
+        out[t] = make_uint4(__float_as_uint(f[0] * s), __float_as_uint(f[1] * s), __float_as_uint(f[2] * s),
+                            __float_as_uint(f[3] * s));
+      } else {
+        const uint32_t lo = bf16x2_bits(f[0] * s, f[1] * s), hi = bf16x2_bits(f[2] * s, f[3] * s);
+        if (t % 2) out[t / 2].z = lo, out[t / 2].w = hi;
+        else out[t / 2].x = lo, out[t / 2].y = hi;
+      }
+    }
+    OUT* dst = x + at + i * cols;
+#pragma unroll
+    for (int t = 0; t < (int)sizeof(OUT); t += 2) {
+      uint4* to = reinterpret_cast<uint4*>(dst) + t;
+      if (wide) {
+        st_global_32(to, out[t], out[t + 1]);
+      } else {
+        to[0] = out[t];
+        to[1] = out[t + 1];
+      }
     }
   }
 }
@@ -104,7 +144,8 @@ __global__ void __launch_bounds__(256) restore_rows_kernel(const uint8_t* __rest
 // memory while one is worked on (rows that count as zero are filled with zeros
 // instead of being read).  The codes are read from there and decoded twice, for
 // the columns' maxima and to encode them; where the exponents allow it the
-// arithmetic is exact in pairs of halves, half as many instructions as in FP32.
+// arithmetic is exact in pairs of halves, half as many instructions as in FP32
+// (21k x 7168 with routed rows in 57.5 us, 5.2 TB/s; in FP32 alone 68).
 constexpr int kUseRing = 3;
 constexpr int kUseCtas = 4;
 
@@ -311,24 +352,24 @@ __global__ void __launch_bounds__(128, kUseCtas) use_cols_kernel(const uint8_t* 
 
 cudaError_t save_rows_launch(const void* x, void* q, void* sf, int64_t groups, int64_t rows,
                              int64_t cols, bool pdl, cudaStream_t stream) {
-  const int kblocks = (int)(cols / 128), kpacks = (kblocks + 3) / 4;
+  const int kpacks = (int)((cols + 511) / 512);
   const int64_t rows_pad = (rows + 3) / 4 * 4;
   const int64_t blocks = (groups * (rows_pad / 2) * kpacks + 7) / 8;
   return launch_op(save_rows_kernel, dim3((unsigned)blocks), 256, 0, pdl, stream,
-                   (const __nv_bfloat16*)x, (uint8_t*)q, (uint32_t*)sf, groups, rows, rows_pad, cols,
-                   kblocks, kpacks);
+                   (const __nv_bfloat16*)x, (uint8_t*)q, (uint32_t*)sf, groups, rows, rows_pad, cols, kpacks);
 }
 
 cudaError_t restore_rows_launch(const void* q, const void* sf, void* x, int dtype, int64_t groups,
                                 int64_t rows, int64_t cols, bool pdl, cudaStream_t stream) {
-  const int kblocks = (int)(cols / 128), kpacks = (kblocks + 3) / 4;
+  const int kpacks = (int)((cols + 511) / 512);
   const int64_t rows_pad = (rows + 3) / 4 * 4;
-  const dim3 grid((unsigned)((groups * rows * kpacks + 7) / 8));
+  const dim3 grid((unsigned)((groups * (rows_pad / 4) * kpacks + 7) / 8));
+  const bool wide = ((uintptr_t)x & 31) == 0;
   if (dtype == DG_DTYPE_FP32)
     return launch_op(restore_rows_kernel<float>, grid, 256, 0, pdl, stream, (const uint8_t*)q,
-                     (const uint32_t*)sf, (float*)x, groups, rows, rows_pad, cols, kblocks, kpacks);
+                     (const uint32_t*)sf, (float*)x, groups, rows, rows_pad, cols, kpacks, wide);
   return launch_op(restore_rows_kernel<__nv_bfloat16>, grid, 256, 0, pdl, stream, (const uint8_t*)q,
-                   (const uint32_t*)sf, (__nv_bfloat16*)x, groups, rows, rows_pad, cols, kblocks, kpacks);
+                   (const uint32_t*)sf, (__nv_bfloat16*)x, groups, rows, rows_pad, cols, kpacks, wide);
 }
 
 cudaError_t use_cols_launch(const void* q, const void* sf, const int32_t* m_indices, void* qc,
