@@ -140,14 +140,15 @@ __global__ void __launch_bounds__(256) restore_rows_kernel(const uint8_t* __rest
 
 // Persistent CTAs of 4 warps, kUseCtas a SM, over 128 x 128 tiles.  Warp w
 // holds rows 32w .. 32w+31: lane l columns 16 (l % 8) .. +15 (one 16-byte
-// access) of rows 4i + l / 8.  The next tiles are on their way into shared
+// access) of rows 4i + l / 8.  The next tile is on its way into shared
 // memory while one is worked on (rows that count as zero are filled with zeros
 // instead of being read).  The codes are read from there and decoded twice, for
 // the columns' maxima and to encode them; where the exponents allow it the
 // arithmetic is exact in pairs of halves, half as many instructions as in FP32
-// (21k x 7168 with routed rows in 57.5 us, 5.2 TB/s; in FP32 alone 68).
-constexpr int kUseRing = 3;
-constexpr int kUseCtas = 4;
+// (21k x 7168 with routed rows in 53.6 us, 5.6 TB/s; in FP32 alone 68).  Six CTAs
+// with one tile on its way each do better than four with two (57.5 us).
+constexpr int kUseRing = 2;
+constexpr int kUseCtas = 6;
 
 struct UseShared {
   uint4 codes[kUseRing][8][128];

@@ -37,15 +37,18 @@ struct GatedBackwardArgs {
 // holds rows 8w .. 8w+7, lane l columns 4l .. 4l+3: a row group's maximum is
 // one warp reduction, a column's 8 values in registers and one exchange
 // through shared memory, and dg, du and h (96 values a thread) stay in
-// registers from the arithmetic to the five stores.  The tile after next is on
-// its way into shared memory meanwhile; each thread copies and reads only its
-// own pieces, so no barrier guards them, and rows that count as zero are
-// filled with zeros instead of being read.
+// registers from the arithmetic to the five stores.  The next tile is on its way
+// into shared memory meanwhile; each thread copies and reads only its own
+// pieces, so no barrier guards them, and rows that count as zero are filled
+// with zeros instead of being read.
 //
-// Bound by HBM (4 bytes in and 5 out an element of h) as long as an element
-// costs no more than about 50 instructions, so arithmetic goes in pairs, and a
-// warp's 16 row scales are worked out by 16 lanes at once.
-constexpr int kBackRing = 3;
+// HBM (4 bytes in and 5 out an element of h) leaves time for about 50
+// instructions an element and it takes 42, with arithmetic in pairs and a warp's
+// 16 row scales worked out by 16 lanes at once; 96 values a thread allow 16 warps
+// an SM, whose issue slots are 57-61% busy.  37k x 2048 in 142 us (4.8 TB/s); with
+// two tiles on their way 151, with the codes collected in shared memory and
+// written by bulk copies 216, with eight columns of four rows a lane 164.
+constexpr int kBackRing = 2;
 constexpr int kBackThreads = 512;
 
 struct BackStage {
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
     float rowmax = 0.0f;  // lanes 0-7: of dg in the row (lane % 8); lanes 8-15: of du
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      // a row of the tile after next, copied row by row between the arithmetic
+      // a row of the next tile, copied row by row between the arithmetic
       fetch_row(i, free_at, live[kBackRing - 1] >> i & 1, src.d, src.c);
       if (i + 1 < src.left) {
         src.d += p.lddh;
