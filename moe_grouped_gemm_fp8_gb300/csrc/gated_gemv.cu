@@ -10,6 +10,9 @@
 // tokens wait in shared memory as FP32, their own scales multiplied in (exact),
 // in the order the lanes read them.
 //
+// One token, K = 7168, F = 2048: 8.7 us (29 MB, 3.4 TB/s; a plain streaming read
+// of as many bytes takes 7.1-7.4), F = 4096 14.1 us (4.2 TB/s).
+//
 // A group of 128 columns with one scale is 8 CTAs of 16 columns: for 8-bit
 // results they form a cluster and tell one another their columns' maxima.
 #include <algorithm>
