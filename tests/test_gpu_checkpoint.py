@@ -195,3 +195,17 @@ def test_use_at_the_edges_of_exact_halves(spread):
     oq, oe, _ = oracle.quantize_cols(v)
     assert np.array_equal(_bytes(qc), oq)
     assert np.array_equal(sfc.cpu().numpy(), dg_pack_cols(oe, 256))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(5, 640), (131, 1152)])
+def test_restored_into_memory_on_16_bytes(rows, cols, dtype):
+    g = torch.Generator().manual_seed(rows)
+    q, sf = dg.quantize_fp8(torch.randn(rows, cols, generator=g).to(torch.bfloat16).cuda(), 1)
+    skip = 128 // torch.finfo(dtype).bits  # 16 bytes
+    room = torch.full((skip + rows * cols + skip,), 7.0, dtype=dtype, device="cuda")
+    out = room[skip:skip + rows * cols].view(rows, cols)
+    assert out.data_ptr() % 32 == 16
+    dg.dequantize_fp8(q, sf, dtype=dtype, out=out)
+    assert torch.equal(out, dg.dequantize_fp8(q, sf, dtype=dtype))
+    assert (room[:skip] == 7).all() and (room[-skip:] == 7).all()

@@ -218,3 +218,50 @@ def test_rows_at_any_offset(rows, cols, dtype, left, right):
     r = dg.layer_norm(xv, w.cuda(), b.cuda(), eps=EPS)
     _check_forward(r, x, w, b)
     _check_backward(dg.layer_norm_backward(dv, xv, w.cuda(), r.mean, r.rstd), x, w, dy, r)
+
+
+# Enough rows that every SM works on several rounds of them, by each form of
+# lanes (8, 16 and 32 values, rows of one and of several warps, whole or not).
+MANY = [(9001, 40), (5001, 384), (4001, 1024), (2501, 2176), (1003, 7168)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,cols", MANY + [(4002, 1001), (3001, 1514), (1100, 7001)])
+def test_many_rows(rows, cols, dtype):
+    x, w, b, dy = _inputs(rows, cols, dtype, rows + 7 * cols)
+    r = dg.layer_norm(x.cuda(), w.cuda(), b.cuda(), eps=EPS)
+    _check_forward(r, x, w, b)
+    _check_backward(dg.layer_norm_backward(dy.cuda(), x.cuda(), w.cuda(), r.mean, r.rstd), x, w, dy, r)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,cols", [(9001, 128)] + MANY[1:])
+def test_many_rows_to_8_bits(rows, cols, dtype):
+    x, w, b, _ = _inputs(rows, cols, dtype, rows + 5 * cols)
+    _check_forward(dg.layer_norm(x.cuda(), w.cuda(), b.cuda(), eps=EPS, out_format="fp8"), x, w, b)
+
+
+@pytest.mark.parametrize("rows,cols", [(4000, 1000), (4000, 1001), (1000, 7168)])
+def test_rows_that_are_not_finite_stay_alone(rows, cols):
+    """A row of NaN or with an infinity spoils its own results and no others."""
+    x, w, b, dy = (t.cuda() for t in _inputs(rows, cols, torch.bfloat16, 21))
+    bad = x.clone()
+    rows_hit = list(range(5, rows, 97))
+    for i in rows_hit:
+        if i % 2:
+            bad[i] = float("nan")
+        else:
+            bad[i, i % cols] = float("inf")
+    fine = torch.ones(rows, dtype=torch.bool, device="cuda")
+    fine[rows_hit] = False
+    a, c = dg.layer_norm(x, w, b), dg.layer_norm(bad, w, b)
+    assert torch.equal(a.y[fine], c.y[fine]) and torch.equal(a.mean[fine], c.mean[fine])
+    assert torch.equal(a.rstd[fine], c.rstd[fine])
+    assert not torch.isfinite(c.mean[~fine]).any()
+    p = dg.layer_norm_backward(dy, x, w, a.mean, a.rstd)[0]
+    q = dg.layer_norm_backward(dy, bad, w, c.mean, c.rstd)[0]
+    assert torch.equal(p[fine], q[fine])
+    if cols % 128 == 0:
+        a, c = dg.layer_norm(x, w, b, out_format="fp8"), dg.layer_norm(bad, w, b, out_format="fp8")
+        assert torch.equal(a.y.view(torch.uint8)[fine], c.y.view(torch.uint8)[fine])
+        assert torch.equal(a.sf[:, :rows].t()[fine], c.sf[:, :rows].t()[fine])
