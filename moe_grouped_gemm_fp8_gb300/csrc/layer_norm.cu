@@ -703,9 +703,9 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(const LayerNormAr
 
 // Backward: as many rows at once as fit, as in the forward pass; every thread
 // keeps the sums dw and db of its own columns in registers (E of 16: 14 to 16
-// warps an SM; with 8 and 28 warps 197 us at 16384 x 7168 where this takes 134),
+// warps an SM; with 8 and 28 warps 197 us at 16384 x 7168 where this takes 132),
 // and at the end the CTA adds its row groups' sums up in order and writes them to
-// `part`.  BF16 with its join: 16384 x 7168 134 us (5.3 TB/s), where one row at a
+// `part`.  BF16 with its join: 16384 x 7168 132 us (5.3 TB/s), where one row at a
 // time leaves the sums' latency open, 28672 x 4096 118 us, 114688 x 1024 114 us
 // (6.2 TB/s).  Reading the row once more from shared memory a round later, to
 // wait for no sums, cost 25% more instructions: 140, 121 and 116 us.
@@ -868,23 +868,31 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const LayerNorm
 }
 
 // dw and db from the partial sums, added in a fixed order: a CTA takes 32
-// columns of one of the two, its 32 warps every 32nd part.
-__global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* __restrict__ part, float* __restrict__ dw,
-                                                               float* __restrict__ db, int parts, int64_t cols) {
-  __shared__ float sum[32][33];
+// columns of one of the two, its warps every kJoinWarps-th part, eight loads in
+// flight a lane.  At 16384 x 7168 it adds about 4 us to the kernel before it.
+constexpr int kJoinWarps = 16;
+
+__global__ void __launch_bounds__(32 * kJoinWarps) layer_norm_join_kernel(const float* __restrict__ part,
+                                                                          float* __restrict__ dw,
+                                                                          float* __restrict__ db, int parts,
+                                                                          int64_t cols) {
+  __shared__ float sum[kJoinWarps][32];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   const float* src = part + (int64_t)blockIdx.y * parts * cols;
   float s = 0.0f;
-  if (c < cols)
-    for (int i = warp; i < parts; i += 32) s += src[(int64_t)i * cols + c];
+  if (c < cols) {
+#pragma unroll 8
+    for (int i = warp; i < parts; i += kJoinWarps) s += src[(int64_t)i * cols + c];
+  }
   sum[warp][lane] = s;
   __syncthreads();
-  s = warp_sum(sum[lane][warp]);
-  const int64_t o = (int64_t)blockIdx.x * 32 + warp;
-  if (lane == 0 && o < cols) (blockIdx.y ? db : dw)[o] = s;
+  if (warp > 0 || c >= cols) return;
+#pragma unroll
+  for (int i = 1; i < kJoinWarps; ++i) s += sum[i][lane];
+  (blockIdx.y ? db : dw)[c] = s;
 }
 
 // Two neighbouring elements can be read at once where rows start on 4 bytes.
@@ -895,7 +903,7 @@ bool pairs_aligned(const LayerNormArgs& p, bool backward) {
          (((uintptr_t)p.x | (uintptr_t)p.y | (backward ? (uintptr_t)p.dy : 0)) & 3) == 0;
 }
 
-// Values a thread of the forward ring kernel takes: a row costs its warps about
+// Values a thread of the ring kernels takes: a row costs its warps about
 // as many instructions as E + 8 values a warp do.
 int norm_values(int64_t cols) {
   int best = 32;
@@ -1088,7 +1096,7 @@ cudaError_t layer_norm_backward_launch(const void* dy, const void* x, int dtype,
                                  : backward<__half>(p, vec, parts, &used, pdl, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_op(layer_norm_join_kernel, dim3((unsigned)((cols + 31) / 32), 2), 1024, 0, pdl, stream,
+  return launch_op(layer_norm_join_kernel, dim3((unsigned)((cols + 31) / 32), 2), 32 * kJoinWarps, 0, pdl, stream,
                    (const float*)part, dw, db, used, cols);
 }
 
