@@ -45,7 +45,7 @@ struct GatedBackwardArgs {
 // HBM (4 bytes in and 5 out an element of h) leaves time for about 50
 // instructions an element and it takes 42, with arithmetic in pairs and a warp's
 // 16 row scales worked out by 16 lanes at once; 96 values a thread allow 16 warps
-// an SM, whose issue slots are 57-61% busy.  37k x 2048 in 142 us (4.8 TB/s); with
+// an SM, whose issue slots are 57-61% busy.  37k x 2048 in 141 us (4.9 TB/s); with
 // two tiles on their way 151, with the codes collected in shared memory and
 // written by bulk copies 216, with eight columns of four rows a lane 164.
 constexpr int kBackRing = 2;
@@ -202,7 +202,21 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
     sh.cmax[1][warp][lane] = make_float4(mu[0], mu[1], mu[2], mu[3]);
     sh.cmax[2][warp][lane] = make_float4(mh[0], mh[1], mh[2], mh[3]);
 
-    // the rows' scales and codes
+    __syncthreads();
+    if (tid < 384) {
+      const int k = tid / 128, c = tid % 128;
+      const float* s = reinterpret_cast<const float*>(&sh.cmax[k][0][0]) + c;
+      float a = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 16; ++w) a = fmaxf(a, s[w * 128]);
+      const uint32_t b = scale_byte(a);
+      reinterpret_cast<float*>(sh.cinv[k])[c] = inverse_of_byte(b);
+      const int64_t cc = (int64_t)fb * 128 + c;
+      uint32_t* w = k == 2 ? p.hsfc + (int64_t)(rb >> 2) * p.f + cc
+                           : p.sfc + (int64_t)(rb >> 2) * f2 + (k ? p.f : 0) + cc;
+      store_scale_byte(w, rb, rb == p.rblocks - 1, b);
+    }
+    // the rows' scales and codes, while the columns' scales are worked out
     const uint32_t byte = scale_byte(rowmax);
     const float inv = inverse_of_byte(byte);
     if (lane < 16 && row0 + (lane & 7) < m_pad) {
@@ -219,20 +233,6 @@ __global__ void __launch_bounds__(kBackThreads, 1) gated_backward_kernel(const G
         *reinterpret_cast<uint32_t*>(qr + p.f) = e4m3x4(mul2(du[i][0], iu), mul2(du[i][1], iu));
       }
       qr += f2;
-    }
-    __syncthreads();
-    if (tid < 384) {
-      const int k = tid / 128, c = tid % 128;
-      const float* s = reinterpret_cast<const float*>(&sh.cmax[k][0][0]) + c;
-      float a = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 16; ++w) a = fmaxf(a, s[w * 128]);
-      const uint32_t b = scale_byte(a);
-      reinterpret_cast<float*>(sh.cinv[k])[c] = inverse_of_byte(b);
-      const int64_t cc = (int64_t)fb * 128 + c;
-      uint32_t* w = k == 2 ? p.hsfc + (int64_t)(rb >> 2) * p.f + cc
-                           : p.sfc + (int64_t)(rb >> 2) * f2 + (k ? p.f : 0) + cc;
-      store_scale_byte(w, rb, rb == p.rblocks - 1, b);
     }
     __syncthreads();
     const float4 ig = sh.cinv[0][lane], iu = sh.cinv[1][lane], ih = sh.cinv[2][lane];
