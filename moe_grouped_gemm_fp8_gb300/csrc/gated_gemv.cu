@@ -67,6 +67,9 @@ __global__ void __launch_bounds__(32 * kGvWarps, 2) fp8_gated_gemv_kernel(const 
   float4* const xs = shared + kGvRingBytes / 16;         // [M][steps of 512 columns][4][32 lanes]
   __shared__ float vals[3][M][kGvWarps];              // g, u, h of the CTA's columns
   __shared__ uint32_t maxima[3][M][kGvCluster];       // of every CTA of the cluster
+  // A CTA's shared memory may be written by the others of its cluster once it
+  // runs: every thread says so here, and the maxima are sent only after all have.
+  if constexpr (CLUSTER) cluster_arrive();
   const GatedArgs& ga = p.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int K = ga.base.k, m = ga.base.m;
@@ -148,6 +151,7 @@ __global__ void __launch_bounds__(32 * kGvWarps, 2) fp8_gated_gemv_kernel(const 
   if constexpr (CLUSTER) {
     const uint32_t rank = cluster_ctarank();
     __syncthreads();
+    cluster_wait();
     // warp w: the maximum of one of the 3 M rows of values, told to all 8 CTAs
     for (int i = warp; i < 3 * M; i += kGvWarps) {
       const float v = lane < kGvWarps ? vals[i / M][i % M][lane] : 0.0f;
