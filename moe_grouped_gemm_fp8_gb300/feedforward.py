@@ -255,7 +255,8 @@ def m_grouped_fp8_gated_gemm_nt_contiguous(a: torch.Tensor, sfa: torch.Tensor, b
     dev = _device()
     f, k, usual = _gated_operands(a, sfa, b, sfb, dev, 1, 3)
     m = a.shape[0]
-    if not usual or not _usual(m_indices, _I32, (m,), dev):
+    usual = usual and _usual(m_indices, _I32, (m,), dev)
+    if not usual:
         _need(m_indices, "m_indices", (torch.int32,), 1)
         _row_index(m_indices, m)
         _contiguous(a=a, b=b)
@@ -283,7 +284,8 @@ def m_grouped_fp8_gated_gemm_nt_masked(a: torch.Tensor, sfa: torch.Tensor, b: to
     g, max_m = a.shape[:2]
     if b.shape[0] != g:
         raise ValueError("shape mismatch")
-    if not usual or not _usual(masked_m, _I32, (g,), dev):
+    usual = usual and _usual(masked_m, _I32, (g,), dev)
+    if not usual:
         _need(masked_m, "masked_m", (torch.int32,), 1)
         if masked_m.numel() != g:
             raise ValueError("shape mismatch")
