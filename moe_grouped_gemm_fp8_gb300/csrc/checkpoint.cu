@@ -379,7 +379,7 @@ cudaError_t use_cols_launch(const void* q, const void* sf, const int32_t* m_indi
   const int rblocks = (int)((rows + 127) / 128), kblocks = (int)(cols / 128);
   const int64_t tiles = (int64_t)rblocks * kblocks;
   const dim3 grid((unsigned)std::min<int64_t>(tiles, (int64_t)kUseCtas * sms));
-  cudaError_t e = set_smem(use_cols_kernel, sizeof(UseShared));
+  cudaError_t e = set_smem(use_cols_kernel, sizeof(UseShared), sizeof(UseShared));
   if (e != cudaSuccess) return e;
   return launch_op(use_cols_kernel, grid, 128, sizeof(UseShared), pdl, stream, (const uint8_t*)q,
                    (const uint32_t*)sf, m_indices, (uint8_t*)qc, (uint32_t*)sfc, rows, (rows + 3) / 4 * 4, cols,

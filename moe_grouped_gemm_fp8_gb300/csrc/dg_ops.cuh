@@ -218,13 +218,16 @@ __device__ __forceinline__ void gate_act_grad2(float2 g, float2& a, float2& da) 
   da = fma2(a, t, s);
 }
 
-// Raises a kernel's dynamic shared-memory limit where it may need more than
-// 48 KB with the (few) bytes of its static arrays.
-// Set on every such launch: the call only writes a field of the function's state.
+// Raises a kernel's dynamic shared-memory limit where a launch of `smem` bytes
+// may need more than 48 KB with the (few) bytes of its static arrays: always to
+// `most`, the largest a launch of this kernel asks for. The limit belongs to the
+// kernel, not to the launch: set to each launch's own size, a host thread with a
+// small launch would lower it between another's call here and its launch.
 template <class Kern>
-static cudaError_t set_smem(Kern kern, size_t smem) {
+static cudaError_t set_smem(Kern kern, size_t smem, size_t most) {
+  if (smem > most) return cudaErrorInvalidValue;
   if (smem <= 40 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
 
 // The (row block, column block) of tiles t, t + grid, ...: one division per CTA.

@@ -283,7 +283,7 @@ cudaError_t gated_backward_launch(const void* dh, int64_t lddh, const void* gu, 
   const int tiles = p.fblocks * p.rblocks;
   const dim3 grid((unsigned)(tiles < sms ? tiles : sms));
   auto kern = activation == DG_ACT_SILU ? gated_backward_kernel<DG_ACT_SILU> : gated_backward_kernel<DG_ACT_GELU_TANH>;
-  cudaError_t e = set_smem(kern, sizeof(BackShared));
+  cudaError_t e = set_smem(kern, sizeof(BackShared), sizeof(BackShared));
   if (e != cudaSuccess) return e;
   return launch_op(kern, grid, kBackThreads, sizeof(BackShared), pdl, stream, p);
 }

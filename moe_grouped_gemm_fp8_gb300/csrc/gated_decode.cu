@@ -447,7 +447,7 @@ template <int TN, int S>
 int gd_max_clusters() {
   auto kern = fp8_gated_decode_kernel<TN, S>;
   constexpr int smem = GdLayout<TN, S>::kSmem;
-  if (set_smem(kern, smem) != cudaSuccess) return 0;
+  if (set_smem(kern, smem, smem) != cudaSuccess) return 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = S;
@@ -468,7 +468,7 @@ cudaError_t gd_launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensor
                       const GatedArgs& args, int strips, int token_blocks, cudaStream_t stream) {
   using L = GdLayout<TN, S>;
   auto kern = fp8_gated_decode_kernel<TN, S>;
-  cudaError_t e = set_smem(kern, L::kSmem);
+  cudaError_t e = set_smem(kern, L::kSmem, L::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   unsigned n_attr = 0;

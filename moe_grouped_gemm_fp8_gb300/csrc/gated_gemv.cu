@@ -28,6 +28,7 @@ constexpr int kGvWarps = 16;   // columns of h a CTA
 constexpr int kGvCluster = 8;  // CTAs of a group of 128 columns
 constexpr int kGvRing = 4;     // steps of 512 columns of W on their way into shared memory
 constexpr int kGvRingBytes = kGvRing * 2 * kGvWarps * 32 * 16;
+constexpr int kGvMaxSmem = 220 * 1024;  // dynamic shared memory of a CTA, at most
 
 // Sixteen products of a lane: codes w with the tokens' values at xs.
 template <int M>
@@ -189,7 +190,7 @@ template <int M>
 cudaError_t gv_launch(const GemvArgs& p, size_t smem, cudaStream_t stream) {
   const bool cluster = p.g.hq || p.g.cq;
   auto kern = cluster ? fp8_gated_gemv_kernel<M, true> : fp8_gated_gemv_kernel<M, false>;
-  cudaError_t e = set_smem(kern, smem);
+  cudaError_t e = set_smem(kern, smem, kGvMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   unsigned n = 0;
@@ -229,9 +230,9 @@ bool gated_gemv_takes(int64_t m, int64_t f, int64_t k, bool eight_bit, int sms) 
   if (m < 1 || m > 4) return false;
   const int64_t tokens = m <= 2 ? m : 4;
   const int64_t smem = tokens * ((k + 511) / 512) * 2048 + kGvRingBytes;  // the tokens as FP32
-  if (smem > 220 * 1024) return false;
+  if (smem > kGvMaxSmem) return false;
   if (m == 1) return true;
-  const int64_t per_sm = std::min<int64_t>(2, 220 * 1024 / (smem + 2048));
+  const int64_t per_sm = std::min<int64_t>(2, kGvMaxSmem / (smem + 2048));
   const bool once = (f + kGvWarps - 1) / kGvWarps <= per_sm * sms && (!eight_bit || per_sm == 2);
   return once && (m == 2 || k <= 2048);
 }

@@ -502,6 +502,7 @@ struct RaggedRow {
 // latency of the sums between), to BF16 73 us (6.4 TB/s); 114688 x 1024 to 8 bits
 // 57 us (6.1 TB/s).
 constexpr int kNormThreads = 768;
+constexpr int64_t kNormMaxSmem = 220 * 1024;  // dynamic shared memory of a CTA, at most (forward and backward)
 
 template <class Row, bool FP8>
 __global__ void __launch_bounds__(kNormThreads, 1) layer_norm_ring_kernel(const LayerNormArgs p) {
@@ -923,8 +924,8 @@ cudaError_t forward(const LayerNormArgs& a, bool vec, int sms, bool pdl, cudaStr
     using Row = decltype(row);
     const int64_t tpr = (p.cols + 32 * n - 1) / (32 * n) * 32;
     const int64_t par = tpr * Row::P * 16, each = Row::kRing * Row::bytes(tpr);
-    if (tpr > 512 || par + each > 220 * 1024) return (int64_t)0;
-    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kNormThreads / tpr, (220 * 1024 - par) / each),
+    if (tpr > 512 || par + each > kNormMaxSmem) return (int64_t)0;
+    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kNormThreads / tpr, (kNormMaxSmem - par) / each),
                                                   (rows + sms - 1) / sms));
   };
   auto ring = [&](auto kern, auto row, int n) {
@@ -934,7 +935,7 @@ cudaError_t forward(const LayerNormArgs& a, bool vec, int sms, bool pdl, cudaStr
     const int64_t threads = rpc * p.tpr;
     p.par_at = Row::kRing * Row::bytes(threads);
     const size_t smem = (size_t)(p.par_at + (int64_t)p.tpr * Row::P * 16);
-    cudaError_t e = set_smem(kern, smem);
+    cudaError_t e = set_smem(kern, smem, kNormMaxSmem);
     if (e != cudaSuccess) return e;
     return launch_op(kern, dim3((unsigned)std::min<int64_t>((rows + rpc - 1) / rpc, sms)), (unsigned)threads, smem, pdl,
                      st, p);
@@ -987,8 +988,8 @@ cudaError_t backward(const LayerNormArgs& a, bool vec, int parts, int* used, boo
     using Row = decltype(row);
     const int64_t tpr = (p.cols + 32 * n - 1) / (32 * n) * 32;
     const int64_t par = tpr * Row::P * 8, each = 2 * Row::kBackRing * Row::bytes(tpr);
-    if (tpr > kNormBackThreads || par + each > 220 * 1024) return (int64_t)0;
-    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kNormBackThreads / tpr, (220 * 1024 - par) / each),
+    if (tpr > kNormBackThreads || par + each > kNormMaxSmem) return (int64_t)0;
+    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kNormBackThreads / tpr, (kNormMaxSmem - par) / each),
                                                   (p.rows + sms - 1) / sms));
   };
   auto ring = [&](auto kern, auto row, int n) {
@@ -1001,7 +1002,7 @@ cudaError_t backward(const LayerNormArgs& a, bool vec, int parts, int* used, boo
     const int64_t sums = rpc > 1 ? threads * 2 * Row::P * (int64_t)sizeof(float2) : 0;
     const size_t smem = (size_t)std::max<int64_t>(p.par_at + (int64_t)p.tpr * Row::P * 8, sums);
     *used = (int)std::min<int64_t>((p.rows + rpc - 1) / rpc, sms);
-    cudaError_t e = set_smem(kern, smem);
+    cudaError_t e = set_smem(kern, smem, kNormMaxSmem);
     if (e != cudaSuccess) return e;
     return launch_op(kern, dim3((unsigned)*used), (unsigned)threads, smem, pdl, st, p);
   };
