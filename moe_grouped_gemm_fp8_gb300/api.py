@@ -45,6 +45,27 @@ def _stream(stream) -> C.c_void_p:
     return C.c_void_p(int(stream))
 
 
+def _under(stream, call, *args):
+    """call(*args) with `stream` (a torch.cuda.Stream or a raw handle) as the
+    current stream, as torch's own operators run under torch.cuda.stream(...):
+    copies of unusual arguments, workspaces and results are made, used and given
+    back in that stream's order.  Tensors returned are also kept from being handed out
+    again before the caller's own stream is past their release."""
+    here = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        # handle 0 is the default stream, which ExternalStream does not take
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError("stream of %s, but the current CUDA device is cuda:%d" % (
+            stream.device, torch.cuda.current_device()))
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in (out,) if isinstance(out, torch.Tensor) else out:
+        if t is not None:
+            t.record_stream(here)
+    return out
+
+
 def _on_current_device(stream, *tensors) -> None:
     """The library launches on the current CUDA device: every tensor (and an
     explicit torch stream) must live there.  A pointer of another device would
@@ -202,7 +223,9 @@ def quantize_fp8(x: torch.Tensor, block_rows: int, packed: bool = True, out=None
     packed=False FP32 scales [G?, ceil(rows/block_rows), cols/128].
     BF16 input (saving an activation in 8 bits) takes block_rows=1 and
     packed=True.  out=(q, sf) writes into preallocated tensors of those shapes."""
-    if x.dtype is torch.bfloat16 and out is None and stream is None and block_rows == 1 and packed and \
+    if stream is not None:
+        return _under(stream, quantize_fp8, x, block_rows, packed, out)
+    if x.dtype is torch.bfloat16 and out is None and block_rows == 1 and packed and \
             x.dim() == 2 and x.get_device() == torch.cuda.current_device() and x.is_contiguous():
         rows, cols = x.shape  # the usual form of saving an activation, where a call's own time counts
         q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=x.device)
@@ -236,14 +259,14 @@ def quantize_fp8(x: torch.Tensor, block_rows: int, packed: bool = True, out=None
         if tuple(q.shape) != tuple(x.shape) or tuple(sf.shape) != tuple(sf_shape) or \
                 not q.is_contiguous() or not sf.is_contiguous():
             raise ValueError("out tensors must be contiguous %s / %s" % (tuple(x.shape), sf_shape))
-    _on_current_device(stream, x, q, sf)
+    _on_current_device(None, x, q, sf)
     if x.dtype == torch.bfloat16:
-        _check(_lib.lib().dg_quantize_fp8_bf16(_ptr(x), _ptr(q), _ptr(sf), groups, rows, cols, _stream(stream)),
+        _check(_lib.lib().dg_quantize_fp8_bf16(_ptr(x), _ptr(q), _ptr(sf), groups, rows, cols, _stream(None)),
                "dg_quantize_fp8_bf16")
         return q, sf
     st = _lib.lib().dg_quantize_fp8(_ptr(x), _ptr(q), _ptr(sf), groups, rows, cols, int(block_rows),
                                     _lib.DG_SF_UE8M0_PACKED if packed else _lib.DG_SF_FP32,
-                                    _stream(stream))
+                                    _stream(None))
     _check(st, "dg_quantize_fp8")
     return q, sf
 
@@ -253,6 +276,8 @@ def quantize_fp8_cols(x: torch.Tensor, packed: bool = True, out=None, stream=Non
     scale per 128 rows of each column, the grouping of the K-grouped GEMM's
     operands.  packed=True gives int32 [ceil(rows/512), align(cols, 4)];
     packed=False FP32 [rows/128, cols]."""
+    if stream is not None:
+        return _under(stream, quantize_fp8_cols, x, packed, out)
     _need(x, "x", (torch.float32,), 2)
     x = x.contiguous()
     rows, cols = x.shape
@@ -270,10 +295,10 @@ def quantize_fp8_cols(x: torch.Tensor, packed: bool = True, out=None, stream=Non
         if tuple(q.shape) != tuple(x.shape) or tuple(sf.shape) != tuple(sf_shape) or \
                 not q.is_contiguous() or not sf.is_contiguous():
             raise ValueError("out tensors must be contiguous %s / %s" % (tuple(x.shape), sf_shape))
-    _on_current_device(stream, x, q, sf)
+    _on_current_device(None, x, q, sf)
     st = _lib.lib().dg_quantize_fp8_cols(_ptr(x), _ptr(q), _ptr(sf), rows, cols,
                                          _lib.DG_SF_UE8M0_PACKED if packed else _lib.DG_SF_FP32,
-                                         _stream(stream))
+                                         _stream(None))
     _check(st, "dg_quantize_fp8_cols")
     return q, sf
 
@@ -282,15 +307,17 @@ def transform_sf_into_required_layout(sf: torch.Tensor, mn: int, k: int, block_r
                                       stream=None) -> torch.Tensor:
     """FP32 scales [G?, ceil(mn/block_rows), ceil(k/128)] -> packed UE8M0
     int32 [G?, ceil(k/512), align(mn, 4)]."""
+    if stream is not None:
+        return _under(stream, transform_sf_into_required_layout, sf, mn, k, block_rows)
     _need(sf, "sf", (torch.float32,), sf.dim())
     grouped = sf.dim() == 3
     groups = sf.shape[0] if grouped else 1
     sf = sf.contiguous()
     out = torch.empty(sf_packed_shape(mn, k, groups if grouped else None), dtype=torch.int32,
                       device=sf.device)
-    _on_current_device(stream, sf, out)
+    _on_current_device(None, sf, out)
     st = _lib.lib().dg_transform_sf(_ptr(sf), _ptr(out), groups, int(mn), int(k), int(block_rows),
-                                    _stream(stream))
+                                    _stream(None))
     _check(st, "dg_transform_sf")
     return out
 

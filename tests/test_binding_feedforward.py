@@ -82,3 +82,60 @@ def test_an_index_tensor_of_another_device_is_refused(make, calls):
     with pytest.raises(ValueError, match="current CUDA device is cuda:0"):
         make(1)()
     assert len(calls) == 1  # nothing reached the library
+
+
+class Side:
+    """A stand-in for a CUDA stream."""
+    device = torch.device("cuda", 0)
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.fixture
+def current(calls, monkeypatch):
+    """The streams made current, innermost last; raw handle 7 stands for a side stream."""
+    from contextlib import contextmanager
+    stack = [Side(0)]
+
+    @contextmanager
+    def under(s):
+        stack.append(s)
+        yield
+        stack.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", under)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: stack[-1])
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: stack[0])
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Side)
+    monkeypatch.setattr(api, "_raw_stream", lambda dev: stack[-1].cuda_stream)
+    monkeypatch.setattr(feedforward, "_raw_stream", lambda dev: stack[-1].cuda_stream)
+    return stack
+
+
+class Copied(On):
+    """A tensor of unusual strides whose copy notes the stream it is made on."""
+    def is_contiguous(self):
+        return False
+
+    def contiguous(self):
+        self.log.append(torch.cuda.current_stream().cuda_stream)
+        return self
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("handle", [7, 0])
+def test_a_copy_of_the_input_is_made_on_the_calls_stream(dtype, handle, calls, current, monkeypatch):
+    used = []
+    monkeypatch.setattr(On, "record_stream", lambda t, s: used.append(s.cuda_stream), raising=False)
+    current.append(Side(3))  # the caller's own stream
+    x = on(0, dtype, 4, 128).as_subclass(Copied)
+    x.log = []
+    api.quantize_fp8(x, 1, stream=handle)
+    if dtype is F32:
+        api.quantize_fp8_cols(x, stream=handle)
+        api.transform_sf_into_required_layout(x, 4, 512, 1, stream=handle)
+    assert x.log == [handle] * (3 if dtype is F32 else 1)
+    # the results are not handed out again before the caller's stream is past their release
+    assert used == [3] * (5 if dtype is F32 else 2)
+    assert current[-1].cuda_stream == 3
