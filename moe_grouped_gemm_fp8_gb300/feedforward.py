@@ -2,7 +2,9 @@
 8-bit activation checkpoints, the gated product's backward pass and layer norm.
 
 Argument marshalling only, as in ``api``: every step of the computation runs
-in libdg.so's kernels; there is no fallback.
+in libdg.so's kernels; there is no fallback.  With ``stream=`` a call runs as
+under ``torch.cuda.stream(stream)``: its results and workspaces are that
+stream's memory.
 """
 import ctypes as C
 import functools
@@ -11,7 +13,7 @@ from typing import NamedTuple, Optional, Tuple
 import torch
 
 from . import _lib
-from .api import (FP8_DTYPES, _check, _need, _on_current_device, _ptr, _raw_stream, _stream, get_num_sms,
+from .api import (FP8_DTYPES, _check, _need, _on_current_device, _ptr, _raw_stream, _stream, _under, get_num_sms,
                   sf_packed_shape)
 
 ACTIVATIONS = {"silu": _lib.DG_ACT_SILU, "gelu_tanh": _lib.DG_ACT_GELU_TANH}
@@ -37,8 +39,9 @@ def _sf(rows: int, cols: int):
     return (cols + 511) // 512, (rows + 3) // 4 * 4
 
 
-def _handle(stream, dev):
-    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+def _handle(dev):
+    """The current stream's; a call on an explicit one runs with that one current."""
+    return _raw_stream(dev) if _raw_stream is not None else _stream(None)
 
 
 def _activation(name: str) -> int:
@@ -51,17 +54,6 @@ def _contiguous(**tensors) -> None:
     for name, t in tensors.items():
         if t is not None and not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-
-
-def _used_on(stream, *tensors) -> None:
-    """Temporary tensors used on an explicit stream: their memory is not
-    handed out again before that stream is past this call."""
-    if stream is None:
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    for t in tensors:
-        t.record_stream(stream)
 
 
 def _row_index(m_indices: Optional[torch.Tensor], rows: int) -> None:
@@ -78,6 +70,8 @@ def dequantize_fp8(q: torch.Tensor, sf: torch.Tensor, dtype: torch.dtype = torch
                    stream=None) -> torch.Tensor:
     """E4M3 codes [rows, cols] or [G, rows, cols] with packed 1x128 row-group
     scales -> the values they stand for, in BF16 or FP32."""
+    if stream is not None:
+        return _under(stream, dequantize_fp8, q, sf, dtype, out)
     if q.dim() not in (2, 3):
         raise ValueError("q must be [rows, cols] or [groups, rows, cols]")
     if dtype not in (torch.float32, torch.bfloat16):
@@ -95,9 +89,9 @@ def dequantize_fp8(q: torch.Tensor, sf: torch.Tensor, dtype: torch.dtype = torch
     _need(out, "out", (dtype,), q.dim())
     if out.shape != q.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous %s" % (tuple(q.shape),))
-    _on_current_device(stream, q, sf, out)
+    _on_current_device(None, q, sf, out)
     _check(_lib.lib().dg_dequantize_fp8(_ptr(q), _ptr(sf), _ptr(out), _DTYPES[dtype], groups, rows, cols,
-                                        _stream(stream)), "dg_dequantize_fp8")
+                                        _stream(None)), "dg_dequantize_fp8")
     return out
 
 
@@ -110,9 +104,11 @@ def requantize_fp8_cols(q: torch.Tensor, sf: torch.Tensor, m_indices: Optional[t
 
     m_indices: int32 [rows]; rows with a negative entry (padding of the
     contiguous layout) and rows past `rows` are zero in the result."""
+    if stream is not None:
+        return _under(stream, requantize_fp8_cols, q, sf, m_indices, out)
     dev = _device()
     rows, cols = q.shape if q.dim() == 2 else (0, 0)
-    if stream is not None or out is not None or q.dim() != 2 or not _usual(q, _E4M3, q.shape, dev) or \
+    if out is not None or q.dim() != 2 or not _usual(q, _E4M3, q.shape, dev) or \
             not _usual(sf, _I32, _sf(rows, cols), dev) or \
             not (m_indices is None or _usual(m_indices, _I32, (rows,), dev)):
         _need(q, "q", FP8_DTYPES, 2)
@@ -121,11 +117,11 @@ def requantize_fp8_cols(q: torch.Tensor, sf: torch.Tensor, m_indices: Optional[t
             raise ValueError("scale shape %s, expected %s" % (tuple(sf.shape), sf_packed_shape(rows, cols)))
         _contiguous(q=q, sf=sf)
         _row_index(m_indices, rows)
-        _on_current_device(stream, q, sf, m_indices, *(out or ()))
+        _on_current_device(None, q, sf, m_indices, *(out or ()))
     qc, sfc = _cols_out(out, (rows + 127) // 128 * 128, cols, q.device, "out")
     rc = _lib.lib().dg_requantize_fp8_cols(q.data_ptr(), sf.data_ptr(),
                                            None if m_indices is None else m_indices.data_ptr(), qc.data_ptr(),
-                                           sfc.data_ptr(), rows, cols, _handle(stream, dev))
+                                           sfc.data_ptr(), rows, cols, _handle(dev))
     if rc:
         _check(rc, "dg_requantize_fp8_cols")
     return qc, sfc
@@ -226,6 +222,8 @@ def fp8_gated_gemm_nt(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: 
     the next GEMM's operand (F % 128 == 0).  checkpoint=True also keeps
     [g | u] in 8 bits for fp8_gated_backward (F % 128 == 0).  d, checkpoint:
     preallocated results (a BF16 tensor, or (codes, scales))."""
+    if stream is not None:
+        return _under(stream, fp8_gated_gemm_nt, a, sfa, b, sfb, d, activation, out_format, checkpoint)
     act = _activation(activation)
     dev = _device()
     f, k, usual = _gated_operands(a, sfa, b, sfb, dev, 1, 2)
@@ -233,12 +231,12 @@ def fp8_gated_gemm_nt(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: 
     h, h_sf, gu, gu_sf = _gated_out(d, checkpoint, out_format, (m,), f, a.device)
     lda = ldb = k
     ldh = f
-    if not usual or stream is not None or d is not None or not isinstance(checkpoint, bool):
-        _on_current_device(stream, a, sfa, b, sfb, h, h_sf, gu, gu_sf)
+    if not usual or d is not None or not isinstance(checkpoint, bool):
+        _on_current_device(None, a, sfa, b, sfb, h, h_sf, gu, gu_sf)
         lda, ldb, ldh = a.stride(0) if m > 1 else k, b.stride(0), h.stride(0) if m > 1 else f
     rc = _lib.lib().dg_fp8_gated_gemm_nt(a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), h.data_ptr(),
                                          _p(h_sf), _p(gu), _p(gu_sf), m, f, k, lda, ldb, ldh, act,
-                                         _handle(stream, dev))
+                                         _handle(dev))
     if rc:
         _check(rc, "dg_fp8_gated_gemm_nt")
     return GatedOutput(h, h_sf, gu, gu_sf)
@@ -251,6 +249,9 @@ def m_grouped_fp8_gated_gemm_nt_contiguous(a: torch.Tensor, sfa: torch.Tensor, b
     """fp8_gated_gemm_nt for the experts of the contiguous layout: rows of A
     [m_sum, K] routed to B [G, 2F, K] by m_indices (-1 = padding: those rows
     of the results are left as they are)."""
+    if stream is not None:
+        return _under(stream, m_grouped_fp8_gated_gemm_nt_contiguous, a, sfa, b, sfb, m_indices, d, activation,
+                      out_format, checkpoint)
     act = _activation(activation)
     dev = _device()
     f, k, usual = _gated_operands(a, sfa, b, sfb, dev, 1, 3)
@@ -261,12 +262,12 @@ def m_grouped_fp8_gated_gemm_nt_contiguous(a: torch.Tensor, sfa: torch.Tensor, b
         _row_index(m_indices, m)
         _contiguous(a=a, b=b)
     h, h_sf, gu, gu_sf = _gated_out(d, checkpoint, out_format, (m,), f, a.device)
-    if not usual or stream is not None or d is not None or not isinstance(checkpoint, bool):
+    if not usual or d is not None or not isinstance(checkpoint, bool):
         _contiguous(d=h)
-        _on_current_device(stream, a, sfa, b, sfb, m_indices, h, h_sf, gu, gu_sf)
+        _on_current_device(None, a, sfa, b, sfb, m_indices, h, h_sf, gu, gu_sf)
     rc = _lib.lib().dg_m_grouped_fp8_gated_gemm_nt_contiguous(
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), h.data_ptr(), _p(h_sf), _p(gu), _p(gu_sf),
-        m_indices.data_ptr(), m, f, k, b.shape[0], act, _handle(stream, dev))
+        m_indices.data_ptr(), m, f, k, b.shape[0], act, _handle(dev))
     if rc:
         _check(rc, "dg_m_grouped_fp8_gated_gemm_nt_contiguous")
     return GatedOutput(h, h_sf, gu, gu_sf)
@@ -278,6 +279,9 @@ def m_grouped_fp8_gated_gemm_nt_masked(a: torch.Tensor, sfa: torch.Tensor, b: to
                                        stream=None) -> GatedOutput:
     """fp8_gated_gemm_nt for the masked layout: A [G, max_m, K] x B [G, 2F, K];
     rows at or past masked_m[g] (read on the device) are left as they are."""
+    if stream is not None:
+        return _under(stream, m_grouped_fp8_gated_gemm_nt_masked, a, sfa, b, sfb, masked_m, expected_m, d, activation,
+                      out_format)
     act = _activation(activation)
     dev = _device()
     f, k, usual = _gated_operands(a, sfa, b, sfb, dev, 2, 3)
@@ -291,12 +295,12 @@ def m_grouped_fp8_gated_gemm_nt_masked(a: torch.Tensor, sfa: torch.Tensor, b: to
             raise ValueError("shape mismatch")
         _contiguous(a=a, b=b, masked_m=masked_m)
     h, h_sf, _, _ = _gated_out(d, False, out_format, (g, max_m), f, a.device)
-    if not usual or stream is not None or d is not None:
+    if not usual or d is not None:
         _contiguous(d=h)
-        _on_current_device(stream, a, sfa, b, sfb, masked_m, h, h_sf)
+        _on_current_device(None, a, sfa, b, sfb, masked_m, h, h_sf)
     rc = _lib.lib().dg_m_grouped_fp8_gated_gemm_nt_masked(
         a.data_ptr(), sfa.data_ptr(), b.data_ptr(), sfb.data_ptr(), h.data_ptr(), _p(h_sf), masked_m.data_ptr(), g,
-        max_m, f, k, int(expected_m), act, _handle(stream, dev))
+        max_m, f, k, int(expected_m), act, _handle(dev))
     if rc:
         _check(rc, "dg_m_grouped_fp8_gated_gemm_nt_masked")
     return GatedOutput(h, h_sf, None, None)
@@ -323,11 +327,13 @@ def fp8_gated_backward(dh: torch.Tensor, gu: torch.Tensor, gu_sf: torch.Tensor,
     row-group scales gu_sf (what the gated product keeps with
     checkpoint=True); F % 128 == 0.  m_indices: int32 [M]; rows with a
     negative entry count as zero, whatever dh and gu hold there."""
+    if stream is not None:
+        return _under(stream, fp8_gated_backward, dh, gu, gu_sf, m_indices, activation)
     act = _activation(activation)
     dev = _device()
     m, f = dh.shape if dh.dim() == 2 else (0, 0)
     ld = f
-    if stream is not None or dh.dim() != 2 or not _usual(dh, _BF16, dh.shape, dev) or \
+    if dh.dim() != 2 or not _usual(dh, _BF16, dh.shape, dev) or \
             not _usual(gu, _E4M3, (m, 2 * f), dev) or not _usual(gu_sf, _I32, _sf(m, 2 * f), dev) or \
             not (m_indices is None or _usual(m_indices, _I32, (m,), dev)):
         _need(dh, "dh", (torch.bfloat16,), 2)
@@ -341,7 +347,7 @@ def fp8_gated_backward(dh: torch.Tensor, gu: torch.Tensor, gu_sf: torch.Tensor,
             raise ValueError("dh needs unit column stride")
         _contiguous(gu=gu, gu_sf=gu_sf)
         _row_index(m_indices, m)
-        _on_current_device(stream, dh, gu, gu_sf, m_indices)
+        _on_current_device(None, dh, gu, gu_sf, m_indices)
         ld = dh.stride(0) if m > 1 else f
     device = dh.device
     m128 = (m + 127) // 128 * 128
@@ -350,7 +356,7 @@ def fp8_gated_backward(dh: torch.Tensor, gu: torch.Tensor, gu_sf: torch.Tensor,
     hc, hsfc = _cols_out(None, m128, f, device, "h_cols")
     rc = _lib.lib().dg_fp8_gated_backward(dh.data_ptr(), ld, gu.data_ptr(), gu_sf.data_ptr(), _p(m_indices),
                                           q.data_ptr(), sf.data_ptr(), qc.data_ptr(), sfc.data_ptr(), hc.data_ptr(),
-                                          hsfc.data_ptr(), m, f, act, _handle(stream, dev))
+                                          hsfc.data_ptr(), m, f, act, _handle(dev))
     if rc:
         _check(rc, "dg_fp8_gated_backward")
     return GatedGradients(q, sf, qc, sfc, hc, hsfc)
@@ -394,13 +400,15 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     type.  out_format "same": y in x's type; "fp8": y as E4M3 codes with
     packed 1x128 row-group scales (cols % 128 == 0), the operand of the FP8
     GEMMs and at the same time the 8-bit checkpoint of the normed activation."""
+    if stream is not None:
+        return _under(stream, layer_norm, x, weight, bias, eps, out_format)
     dev = _device()
     rows, cols = x.shape if x.dim() == 2 else (0, 0)
     ld = cols
-    if stream is not None or cols < 1 or x.dtype not in _DTYPES or not _usual(x, x.dtype, x.shape, dev) or \
+    if cols < 1 or x.dtype not in _DTYPES or not _usual(x, x.dtype, x.shape, dev) or \
             not _usual(weight, _F32, (cols,), dev) or not (bias is None or _usual(bias, _F32, (cols,), dev)):
         _norm_args(x, weight, bias)
-        _on_current_device(stream, x, weight, bias)
+        _on_current_device(None, x, weight, bias)
         ld = _row_stride(x)
     sf = None
     device = x.device
@@ -416,7 +424,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tenso
     rstd = torch.empty(rows, dtype=_F32, device=device)
     rc = _lib.lib().dg_layer_norm(x.data_ptr(), _DTYPES[x.dtype], weight.data_ptr(), _p(bias), _DTYPES[weight.dtype],
                                   y.data_ptr(), _p(sf), mean.data_ptr(), rstd.data_ptr(), rows, cols, ld, float(eps),
-                                  _handle(stream, dev))
+                                  _handle(dev))
     if rc:
         _check(rc, "dg_layer_norm")
     return LayerNormOutput(y, sf, mean, rstd)
@@ -426,10 +434,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                         rstd: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dx, dweight, dbias) of layer_norm: dx in x's type, the parameters'
     gradients in FP32 (summed in a fixed order)."""
+    if stream is not None:
+        return _under(stream, layer_norm_backward, dy, x, weight, mean, rstd)
     dev = _device()
     rows, cols = x.shape if x.dim() == 2 else (0, 0)
     ldx = ldy = cols
-    if stream is not None or cols < 1 or x.dtype not in _DTYPES or not _usual(x, x.dtype, x.shape, dev) or \
+    if cols < 1 or x.dtype not in _DTYPES or not _usual(x, x.dtype, x.shape, dev) or \
             not _usual(dy, x.dtype, x.shape, dev) or not _usual(weight, _F32, (cols,), dev) or \
             not _usual(mean, _F32, (rows,), dev) or not _usual(rstd, _F32, (rows,), dev):
         _norm_args(x, weight, None)
@@ -441,7 +451,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
         if mean.numel() != rows or rstd.numel() != rows:
             raise ValueError("mean and rstd must be [%d]" % rows)
         _contiguous(mean=mean, rstd=rstd)
-        _on_current_device(stream, dy, x, weight, mean, rstd)
+        _on_current_device(None, dy, x, weight, mean, rstd)
         ldx, ldy = _row_stride(x), _row_stride(dy)
     device = x.device
     dx = torch.empty((rows, cols), dtype=x.dtype, device=device)
@@ -449,11 +459,10 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     db = torch.empty(cols, dtype=_F32, device=device)
     need = _backward_workspace(cols, get_num_sms())
     ws = torch.empty(need, dtype=torch.uint8, device=device)
-    _used_on(stream, ws)
     rc = _lib.lib().dg_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], weight.data_ptr(),
                                            _DTYPES[weight.dtype], mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
                                            dw.data_ptr(), db.data_ptr(), ws.data_ptr(), need, rows, cols, ldy, ldx,
-                                           _handle(stream, dev))
+                                           _handle(dev))
     if rc:
         _check(rc, "dg_layer_norm_backward")
     return dx, dw, db

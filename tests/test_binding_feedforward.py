@@ -139,3 +139,40 @@ def test_a_copy_of_the_input_is_made_on_the_calls_stream(dtype, handle, calls, c
     # the results are not handed out again before the caller's stream is past their release
     assert used == [3] * (5 if dtype is F32 else 2)
     assert current[-1].cuda_stream == 3
+
+
+def _tensors():
+    """One call of every operator, on ordinary arguments."""
+    x, w = on(0, BF16, M, K), on(0, F32, K)
+    q, sf = on(0, FP8, M, K), words(0, M, K)
+    b, sfb = on(0, FP8, 2 * F, K), words(0, 2 * F, K)
+    bg, sfg = on(0, FP8, G, 2 * F, K), words(0, 2 * F, K, G)
+    gu, gu_sf = on(0, FP8, M, 2 * F), words(0, M, 2 * F)
+    r = on(0, F32, M)
+    f = feedforward
+    return {
+        "quantize_fp8": lambda s: api.quantize_fp8(x, 1, stream=s),
+        "dequantize_fp8": lambda s: f.dequantize_fp8(q, sf, stream=s),
+        "requantize_fp8_cols": lambda s: f.requantize_fp8_cols(q, sf, stream=s),
+        "fp8_gated_gemm_nt": lambda s: f.fp8_gated_gemm_nt(q, sf, b, sfb, out_format="fp8", checkpoint=True, stream=s),
+        "contiguous": lambda s: f.m_grouped_fp8_gated_gemm_nt_contiguous(q, sf, bg, sfg, on(0, I32, M), stream=s),
+        "masked": lambda s: f.m_grouped_fp8_gated_gemm_nt_masked(
+            on(0, FP8, G, M, K), words(0, M, K, G), bg, sfg, on(0, I32, G), stream=s),
+        "fp8_gated_backward": lambda s: f.fp8_gated_backward(on(0, BF16, M, F), gu, gu_sf, stream=s),
+        "layer_norm": lambda s: f.layer_norm(x, w, w, stream=s),
+        "layer_norm_backward": lambda s: f.layer_norm_backward(x, x, w, r, r, stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", _tensors())
+def test_results_and_workspaces_are_allocated_on_the_calls_stream(name, calls, current, monkeypatch):
+    """What a call writes comes from its stream's memory: memory of the
+    current stream may still be in use there."""
+    where, inner = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: where.append(torch.cuda.current_stream().cuda_stream) or
+                        inner(*a, **kw))
+    monkeypatch.setattr(On, "record_stream", lambda t, s: None, raising=False)
+    monkeypatch.setattr(feedforward, "_backward_workspace", lambda cols, sms: 64)
+    current.append(Side(3))
+    _tensors()[name](7)
+    assert where and set(where) == {7} and len(calls) >= 1
