@@ -357,15 +357,17 @@ def _new_workspace(nbytes: int, device) -> torch.Tensor:
 _WS_MAX_BLOCK_N = 224
 
 
-def _stream_workspace(stream_handle, device) -> torch.Tensor:
+def _stream_workspace(stream_handle, device, stream=None) -> torch.Tensor:
     """The binding's workspace for this device and stream (its handle), of
     the largest size a stream-K launch on the current SM count can use
-    (about 35 MB on 152 SMs); created with zeroed flags on first use."""
+    (about 35 MB on 152 SMs); created with zeroed flags on first use, on
+    `stream` where that is not the current one."""
     key = (device.index, stream_handle or 0)
     ws = _WORKSPACES.get(key)
     if ws is None:
         nbytes = WORKSPACE_FLAG_BYTES + get_num_sms() * 2 * 128 * _WS_MAX_BLOCK_N * 4
-        ws = _WORKSPACES[key] = _new_workspace(nbytes, device)
+        ws = _new_workspace(nbytes, device) if stream is None else _under(stream, _new_workspace, nbytes, device)
+        _WORKSPACES[key] = ws
     return ws
 
 
@@ -379,6 +381,8 @@ def fp8_gemm_nt(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.
     graph's pool) for the stream-K form when that is faster; False runs
     without one (dg_fp8_gemm_nt); a uint8 CUDA tensor is used as given (its
     flag words zero before its first use, see dg_fp8_gemm_nt_ws)."""
+    if stream is not None and d is None:
+        return _under(stream, fp8_gemm_nt, a, sfa, b, sfb, d, c, None, workspace)
     _need(a, "a", FP8_DTYPES, 2)
     _need(b, "b", FP8_DTYPES, 2)
     _need(sfa, "sfa", (torch.int32,), 2)
@@ -410,9 +414,10 @@ def fp8_gemm_nt(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb: torch.
             # only when its plan uses one
             need = fp8_gemm_nt_workspace_size(m, n, k, c is not None)
             if need:
-                ws = _new_workspace(need, d.device)
+                ws = _new_workspace(need, d.device) if stream is None else \
+                    _under(stream, _new_workspace, need, d.device)
         else:
-            ws = _stream_workspace(st.value, d.device)
+            ws = _stream_workspace(st.value, d.device, stream)
     elif workspace is not False:
         _need(workspace, "workspace", (torch.uint8,), 1)
         _on_current_device(stream, workspace)
@@ -440,6 +445,8 @@ def fp8_gemm_nt_fp32_sf(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb
     """D = C + A @ B.T with arbitrary FP32 scales: sfa float32 [ceil(K/128),
     align(M, 4)] (one per 1x128 group of A, K-block-major), sfb float32
     [ceil(N/128), K/128] (one per 128x128 block of B)."""
+    if stream is not None and d is None:
+        return _under(stream, fp8_gemm_nt_fp32_sf, a, sfa, b, sfb, d, c)
     _need(a, "a", FP8_DTYPES, 2)
     _need(b, "b", FP8_DTYPES, 2)
     _need(sfa, "sfa", (torch.float32,), 2)
@@ -476,6 +483,8 @@ def fp8_gemm_nt_fp32_sf(a: torch.Tensor, sfa: torch.Tensor, b: torch.Tensor, sfb
 def _dense_layout(layout: str, a, sfa, b, sfb, d, c, stream):
     """Shared marshalling of fp8_gemm_{nn, tn, tt}: A is [M,K] ('n') or
     [K,M] ('t'); B is [K,N] ('n') or [N,K] ('t')."""
+    if stream is not None and d is None:
+        return _under(stream, _dense_layout, layout, a, sfa, b, sfb, d, c, None)
     _need(a, "a", FP8_DTYPES, 2)
     _need(b, "b", FP8_DTYPES, 2)
     _need(sfa, "sfa", (torch.int32,), 2)
@@ -527,6 +536,8 @@ def m_grouped_fp8_gemm_nt_contiguous(a: torch.Tensor, sfa: torch.Tensor, b: torc
                                      sfb: torch.Tensor, m_indices: torch.Tensor,
                                      d: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rows of A [m_sum,K] routed to experts B [G,N,K] by m_indices (-1 = padding)."""
+    if stream is not None and d is None:
+        return _under(stream, m_grouped_fp8_gemm_nt_contiguous, a, sfa, b, sfb, m_indices)
     _need(a, "a", FP8_DTYPES, 2)
     _need(b, "b", FP8_DTYPES, 3)
     _need(sfa, "sfa", (torch.int32,), 2)
@@ -561,6 +572,8 @@ def k_grouped_fp8_gemm_tn_contiguous(a: torch.Tensor, sfa: torch.Tensor, b: torc
     """Experts stacked along K: A [sum_k, M], B [sum_k, N] (E4M3, M / N
     innermost), ks [G] int32 on the device (rows per expert, multiples of
     128).  D[g] = C[g] + A_g^T B_g, FP32 [G, M, N]."""
+    if stream is not None and d is None:
+        return _under(stream, k_grouped_fp8_gemm_tn_contiguous, a, sfa, b, sfb, ks, d, c)
     _need(a, "a", FP8_DTYPES, 2)
     _need(b, "b", FP8_DTYPES, 2)
     _need(sfa, "sfa", (torch.int32,), 2)
@@ -597,6 +610,8 @@ def m_grouped_fp8_gemm_nt_masked(a: torch.Tensor, sfa: torch.Tensor, b: torch.Te
                                  sfb: torch.Tensor, masked_m: torch.Tensor, expected_m: int = 0,
                                  d: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """A [G,max_m,K] x B [G,N,K]; rows >= masked_m[g] are left untouched."""
+    if stream is not None and d is None:
+        return _under(stream, m_grouped_fp8_gemm_nt_masked, a, sfa, b, sfb, masked_m, expected_m)
     _need(a, "a", FP8_DTYPES, 3)
     _need(b, "b", FP8_DTYPES, 3)
     _need(sfa, "sfa", (torch.int32,), 3)

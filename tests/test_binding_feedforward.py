@@ -176,3 +176,53 @@ def test_results_and_workspaces_are_allocated_on_the_calls_stream(name, calls, c
     current.append(Side(3))
     _tensors()[name](7)
     assert where and set(where) == {7} and len(calls) >= 1
+
+
+def _products():
+    """One call of every product, on ordinary arguments; without a result it allocates its own."""
+    q, sf = on(0, FP8, M, K), words(0, M, K)
+    bg, sfg = on(0, FP8, G, 2 * F, K), words(0, 2 * F, K, G)
+    b, sfb = on(0, FP8, 2 * F, K), words(0, 2 * F, K)
+    square = on(0, FP8, M, M), words(0, M, M)
+    return {
+        "fp8_gemm_nt": lambda s, **kw: api.fp8_gemm_nt(q, sf, b, sfb, stream=s, **kw),
+        "fp8_gemm_nt, no workspace": lambda s, **kw: api.fp8_gemm_nt(q, sf, b, sfb, stream=s, workspace=False, **kw),
+        "fp8_gemm_nt_fp32_sf": lambda s, **kw: api.fp8_gemm_nt_fp32_sf(
+            q, on(0, F32, K // 128, M), b, on(0, F32, 2 * F // 128, K // 128), stream=s, **kw),
+        "fp8_gemm_nn": lambda s, **kw: api.fp8_gemm_nn(*square, *square, stream=s, **kw),
+        "contiguous": lambda s, **kw: api.m_grouped_fp8_gemm_nt_contiguous(q, sf, bg, sfg, on(0, I32, M), stream=s, **kw),
+        "masked": lambda s, **kw: api.m_grouped_fp8_gemm_nt_masked(
+            on(0, FP8, G, M, K), words(0, M, K, G), bg, sfg, on(0, I32, G), stream=s, **kw),
+        "k_grouped": lambda s, **kw: api.k_grouped_fp8_gemm_tn_contiguous(
+            on(0, FP8, K, M), words(0, M, K), on(0, FP8, K, M), words(0, M, K), on(0, I32, G), stream=s, **kw),
+    }
+
+
+@pytest.fixture
+def allocations(calls, current, monkeypatch):
+    """The current stream at every allocation."""
+    where, inner = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: where.append(torch.cuda.current_stream().cuda_stream) or
+                        inner(*a, **kw))
+    monkeypatch.setattr(On, "record_stream", lambda t, s: None, raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(api, "get_num_sms", lambda: 1)
+    monkeypatch.setattr(api, "get_tma_aligned_size", lambda x, size: (x + 3) // 4 * 4)
+    monkeypatch.setattr(api, "_WORKSPACES", {})
+    current.append(Side(3))
+    return where
+
+
+@pytest.mark.parametrize("name", _products())
+def test_the_products_results_are_allocated_on_the_calls_stream(name, allocations, calls):
+    _products()[name](7)
+    assert allocations and set(allocations) == {7} and len(calls) == 1
+
+
+def test_a_workspace_is_made_on_the_stream_that_uses_it(allocations, calls):
+    """With a given result only the binding's workspace (and its zeros) is left."""
+    d = on(0, BF16, M, 2 * F)
+    _products()["fp8_gemm_nt"](7, d=d)
+    assert allocations == [7] and len(calls) == 1
+    _products()["fp8_gemm_nt"](7, d=d)
+    assert len(allocations) == 1 and len(calls) == 2  # kept

@@ -104,3 +104,32 @@ def test_a_stream_of_the_current_device_by_object_or_handle(handle):
         s.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, _bits(call(None)))), name
         assert all(torch.equal(a, b) for a, b in zip(_bits(call(0)), _bits(call(None)))), name  # the default stream
+
+
+def test_the_products_on_an_explicit_stream():
+    """New results and the binding's own workspace, while the current stream is busy."""
+    g = torch.Generator().manual_seed(8)
+    q, sf = dg.quantize_fp8(torch.randn(256, 512, generator=g).cuda(), 1)
+    qb, sfb = dg.quantize_fp8(torch.randn(256, 512, generator=g).cuda(), 128)
+    e, sfe = dg.quantize_fp8(torch.randn(2, 256, 512, generator=g).cuda(), 128)
+    xm, sfm = dg.quantize_fp8(torch.randn(2, 128, 512, generator=g).cuda(), 1)
+    index = torch.tensor([0] * 128 + [1] * 128, dtype=torch.int32).cuda()
+    counts = torch.tensor([128, 128], dtype=torch.int32).cuda()
+    xc, sfc = dg.quantize_fp8_cols(torch.randn(256, 128, generator=g).cuda())
+    calls = {
+        "dense": lambda s: dg.fp8_gemm_nt(q, sf, qb, sfb, stream=s),
+        "contiguous": lambda s: dg.m_grouped_fp8_gemm_nt_contiguous(q, sf, e, sfe, index, stream=s),
+        "masked": lambda s: dg.m_grouped_fp8_gemm_nt_masked(xm, sfm, e, sfe, counts, stream=s),
+        "k-grouped": lambda s: dg.k_grouped_fp8_gemm_tn_contiguous(xc, sfc, xc, sfc, counts, stream=s),
+    }
+    s = torch.cuda.Stream()
+    for name, call in calls.items():
+        want = call(None).clone()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY)
+        junk = [torch.empty_like(want).fill_(7) for _ in range(4)]
+        del junk
+        got = call(s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), name
+    assert dg.get_device_error()[0] == 0
