@@ -299,6 +299,9 @@ dg_status dg_k_grouped_fp8_gemm_tn_contiguous(const void* a, const int32_t* sfa,
  * Scale rule: s = 2^e, e the smallest integer with 448 * 2^e >= amax of the
  * group (e clamped to [-127, 127]; an all-zero group gets e = 0), then
  * q = E4M3(x / s), rounding to nearest even and saturating at +-448.
+ * A NaN is passed over by amax and becomes the code NaN; an infinity in a
+ * group gives e = 127 and the code +-448.  Every kernel that writes codes and
+ * their scales follows this rule.
  * Cited: same page, section "Interface GEMM e restrições de layout" (casting
  * to FP8 is left to the user; the library offers simple utilities). */
 dg_status dg_quantize_fp8(const float* x, void* q, void* sf, int64_t groups, int64_t rows,

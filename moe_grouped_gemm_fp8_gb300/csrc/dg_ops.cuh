@@ -118,27 +118,34 @@ __device__ __forceinline__ void e4m3x4_to_float(uint32_t codes, float (&f)[4]) {
   f[3] = b.y;
 }
 
-// scale_exponent(amax) + 127 for a finite amax, without branches: adding
-// 0x1FFFFF carries into the exponent exactly when the fraction is above 1.75.
+// scale_exponent(amax) + 127 without branches: adding 0x1FFFFF carries into the
+// exponent exactly when the fraction is above 1.75; an infinity gets 2^127.
+// amax: the maximum of magnitudes that passes over NaN (abs_max2, abs_max3).
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
   const int t = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 8;
-  return amax > 0.0f ? (uint32_t)max(t, 0) : 127u;
+  const uint32_t b = amax > 0.0f ? (uint32_t)max(t, 0) : 127u;
+  return amax == INFINITY ? 254u : b;
 }
-// 2^(127 - byte), the factor that brings a group into E4M3's range (byte <= 253).
-__device__ __forceinline__ float inverse_of_byte(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^(127 - byte), the factor that brings a group into E4M3's range (byte <= 254,
+// where it is the subnormal 2^-127).
+__device__ __forceinline__ float inverse_of_byte(uint32_t byte) {
+  return __uint_as_float(max((254u - byte) << 23, 1u << 22));
+}
 
 // Pairs of FP32 (one instruction for two).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 mul2(float2 a, float b) { return __fmul2_rn(a, make_float2(b, b)); }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-// max(|m|, |a|, |b|)
+// max(|m|, |a|, |b|) of those that are numbers
 __device__ __forceinline__ float abs_max3(float m, float a, float b) {
   float r;
   asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
   return r;
 }
 __device__ __forceinline__ float abs_max2(float m, float2 a) { return abs_max3(m, a.x, a.y); }
+// The bits of |v|, 0 for NaN: ordered like the magnitudes.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(fmaxf(fabsf(v), 0.0f)); }
 __device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) { return e4m3x4(a.x, a.y, b.x, b.y); }
 // Two FP32 sums over the warp in one butterfly: lanes 0-15 end with a's, lanes
 // 16-31 with b's.

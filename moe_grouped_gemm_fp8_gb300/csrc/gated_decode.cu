@@ -379,11 +379,11 @@ __global__ void __launch_bounds__(kGdThreads, 1)
     if (ga.hq || ga.cq) {
 #pragma unroll
       for (int j = 0; j < W; ++j) {
-        const uint32_t mh = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(h[j])));
+        const uint32_t mh = __reduce_max_sync(0xffffffffu, magnitude(h[j]));
         if (lane == 0) xch[(2 * W + j) * 4 + q] = mh;
         if (ga.cq) {
-          const uint32_t mg = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(f[0][j])));
-          const uint32_t mu = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(f[1][j])));
+          const uint32_t mg = __reduce_max_sync(0xffffffffu, magnitude(f[0][j]));
+          const uint32_t mu = __reduce_max_sync(0xffffffffu, magnitude(f[1][j]));
           if (lane == 0) {
             xch[j * 4 + q] = mg;
             xch[(W + j) * 4 + q] = mu;

@@ -69,12 +69,12 @@ __device__ __forceinline__ void pair_sync(int id) {
 }
 
 __device__ __forceinline__ uint32_t abs_max64(const uint32_t (&r)[2][32]) {
-  uint32_t m = 0;
+  float m = 0.0f;
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) m = max(m, r[c][i] & 0x7FFFFFFFu);
-  return m;
+    for (int i = 0; i < 32; i += 2) m = abs_max3(m, __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
+  return __float_as_uint(m);
 }
 
 // 64 columns of one row, times inv, as E4M3 codes (16-byte aligned).

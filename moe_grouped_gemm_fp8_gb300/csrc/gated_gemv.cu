@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(32 * kGvWarps, 2) fp8_gated_gemv_kernel(const 
     // warp w: the maximum of one of the 3 M rows of values, told to all 8 CTAs
     for (int i = warp; i < 3 * M; i += kGvWarps) {
       const float v = lane < kGvWarps ? vals[i / M][i % M][lane] : 0.0f;
-      const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(v)));
+      const uint32_t mx = __reduce_max_sync(0xffffffffu, magnitude(v));
       if (lane < kGvCluster)
         st_shared_cluster_u32(mapa_shared(smem_u32(&maxima[i / M][i % M][rank]), (uint32_t)lane), mx);
     }
