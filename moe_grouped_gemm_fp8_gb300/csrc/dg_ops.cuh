@@ -215,7 +215,9 @@ __device__ __forceinline__ void gate_act_grad2(float2 g, float2& a, float2& da) 
     constexpr float c2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
     const float2 gg = mul2(g, g);
     z = mul2(mul2(g, -kLog2e), fma2(gg, make_float2(c2 * 0.044715f, c2 * 0.044715f), make_float2(c2, c2)));
-    dz = fma2(gg, make_float2(3.0f * c2 * 0.044715f, 3.0f * c2 * 0.044715f), make_float2(c2, c2));
+    // finite where g^2 is not: there a or 1 - s is 0, and 0 dz has to be too
+    const float2 most = make_float2(fminf(gg.x, 1e30f), fminf(gg.y, 1e30f));
+    dz = fma2(most, make_float2(3.0f * c2 * 0.044715f, 3.0f * c2 * 0.044715f), make_float2(c2, c2));
   }
   const float2 q = add2(make_float2(exp2_approx(z.x), exp2_approx(z.y)), make_float2(1.0f, 1.0f));
   const float2 s = make_float2(rcp_approx(q.x), rcp_approx(q.y));
