@@ -114,10 +114,11 @@ __device__ __forceinline__ float row_sum(float v, float* red, int slot) {
   return warp_sum(lane < (int)blockDim.x / 32 ? red[lane] : 0.0f);
 }
 
-// 1 / sqrt(v): the hardware's estimate and one Newton step.
+// 1 / sqrt(v): the hardware's estimate and one Newton step (which would make a
+// NaN of the infinity that a row without spread has for eps = 0).
 __device__ __forceinline__ float rsqrt_newton(float v) {
   const float r = rsqrtf(v);
-  return r * (1.5f - (0.5f * v * r) * r);
+  return v > 0.0f ? r * (1.5f - (0.5f * v * r) * r) : r;
 }
 
 struct LayerNormArgs {
