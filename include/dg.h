@@ -481,7 +481,9 @@ dg_status dg_layer_norm_backward_workspace_size(int64_t cols, int32_t num_sms, u
  *   DG_CTA_PAIR=1        256-row tiles on 2-CTA pairs (cta_group::2 MMAs);
  *   DG_STREAM_K=0|1      forbid / force stream-K where a workspace allows it;
  *   DG_MULTICAST=0       256-row dense tiles and K-grouped tiles one CTA each
- *                        instead of 2-CTA clusters sharing B by TMA multicast;
+ *                        instead of 2-CTA clusters sharing B by TMA multicast
+ *                        (as they always are where WORLD_SIZE, the ranks of the
+ *                        job, is above 1 or the process sees several GPUs);
  *   DG_TALL_EPI8=0       four epilogue warps for 256-row tiles instead of eight;
  *   DG_DECODE=0          tiled kernels instead of the decode kernels for M <= 128;
  *                        2: the gated product of one to four tokens as of more;
@@ -538,7 +540,8 @@ dg_status dg_plan_fp8_gemm_nt(int64_t m, int64_t n, int64_t k, int32_t has_c, in
  * same choice) and multicast (1 when the 256-row tiles run in clusters of two
  * CTAs on adjacent M blocks and one column block of B, each CTA loading half
  * of the B tile into both with TMA multicast; dg_fp8_gemm_nt makes the same
- * choice; DG_MULTICAST = 0 turns it off).  Same checks. */
+ * choice; DG_MULTICAST = 0 turns it off, and so do WORLD_SIZE > 1 and, once
+ * the library has used a device, several visible ones).  Same checks. */
 dg_status dg_plan_fp8_gemm_nt_ws(int64_t m, int64_t n, int64_t k, int32_t has_c, int32_t num_sms,
                                  int32_t* block_m, int32_t* block_n, int32_t* split_k,
                                  int32_t* cta_pair, int32_t* stream_k, int32_t* swap_ab,

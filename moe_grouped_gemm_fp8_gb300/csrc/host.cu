@@ -29,6 +29,7 @@ std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 std::atomic<int> g_pdl{0};
 std::atomic<int32_t> g_debug_drop_load{0};  // test hook, see dg_debug_set_drop_load
 std::atomic<int32_t> g_debug_plant_check{0};  // test hook, see dg_debug_plant_check
+std::atomic<int> g_visible_devices{0};  // CUDA devices this process sees, once one is used
 std::atomic<int32_t> g_mk_alignment{kBlockM};  // dg_set_mk_alignment_for_contiguous_layout
 
 struct DeviceInfo {
@@ -60,7 +61,7 @@ struct EnvConfig {
   uintptr_t fingerprint = 0;
   bool valid = false;
   int block_m = 0, block_n = 0, split_k = 0, cta_pair = 0, stream_k = -1, tall_epi8 = 1,
-      raster_band = 16, decode = 1, multicast = 1;
+      raster_band = 16, decode = 1, multicast = 1, world_size = 1;
   bool print_configs = false;
 };
 
@@ -85,11 +86,18 @@ const EnvConfig& env() {
     c.raster_band = env_int("DG_RASTER_BAND", 16);
     c.decode = env_int("DG_DECODE", 1);
     c.multicast = env_int("DG_MULTICAST", 1);
+    c.world_size = env_int("WORLD_SIZE", 1);  // ranks of a job, as launchers set it
     c.print_configs = env_flag("DG_PRINT_CONFIGS");
     c.fingerprint = f;
     c.valid = true;
   }
   return c;
+}
+
+// TMA multicast is for processes that have one GPU to themselves and no other
+// ranks: one of several, by either count, runs one CTA per tile (the same bits).
+bool multicast_on() {
+  return env().multicast != 0 && env().world_size <= 1 && g_visible_devices.load(std::memory_order_relaxed) <= 1;
 }
 
 dg_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DG_OK : DG_ERR_CUDA; }
@@ -107,6 +115,9 @@ dg_status current_device(int* sms) {
       d.err = cudaDeviceGetAttribute(&d.cc_minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (d.err == cudaSuccess)
       d.err = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    int visible = 0;
+    if (d.err == cudaSuccess) d.err = cudaGetDeviceCount(&visible);
+    if (d.err == cudaSuccess) g_visible_devices.store(visible);
   });
   if (d.err != cudaSuccess) return DG_ERR_CUDA;
   if (d.cc_major != 10 || d.cc_minor != 3) return DG_ERR_UNSUPPORTED_ARCH;
@@ -635,11 +646,11 @@ DensePlan plan_dense(int mode, int64_t m, int64_t n, int64_t k, bool with_c, int
   // a single M block of at most 64 rows: 64-row A slots, more stages
   p.short_a = mode == kDense && !p.tall && m <= kBlockM / 2 && gemm_short_supported(p.block_n);
   // 256-row dense tiles (eight epilogue warps, tile by tile) share B between
-  // the two CTAs of a cluster; DG_MULTICAST = 0 turns it off.  Measured on
+  // the two CTAs of a cluster; DG_MULTICAST = 0 turns it off, and so does a
+  // second GPU (multicast_on).  Measured on
   // GB300: 1.3-1.6% faster on the prefill shapes that take 256-row tiles,
   // none slower.
-  p.multicast = mode == kDense && p.tall && !p.stream_k && env().tall_epi8 != 0 && env().multicast != 0 &&
-                sms >= 2;
+  p.multicast = mode == kDense && p.tall && !p.stream_k && env().tall_epi8 != 0 && multicast_on() && sms >= 2;
   return p;
 }
 
@@ -1226,14 +1237,15 @@ dg_status dg_k_grouped_fp8_gemm_tn_contiguous(const void* a, const int32_t* sfa,
   // 256-column tiles drain their accumulator with eight epilogue warps
   // (DG_TALL_EPI8 = 0: four, each reading its 256 columns in two halves);
   // with them, clusters of two CTAs on adjacent M blocks of one expert share
-  // each B tile by TMA multicast (DG_MULTICAST = 0 turns it off), on an even grid
+  // each B tile by TMA multicast (multicast_on), on an even grid
   args.epi8 = (block_n == 256 && env().tall_epi8 != 0) ? 1 : 0;
-  args.mc = (args.epi8 && env().multicast != 0 && sms >= 2 && args.m_blocks >= 2) ? 1 : 0;
+  args.mc = (args.epi8 && multicast_on() && sms >= 2 && args.m_blocks >= 2) ? 1 : 0;
   const int64_t pair_tiles = (int64_t)num_groups * ((args.m_blocks + 1) / 2) * args.n_blocks;
   const int grid = args.mc ? 2 * (int)(pair_tiles < sms / 2 ? pair_tiles : sms / 2)
                            : (int)(tiles < sms ? tiles : sms);
-  print_config(args.epi8 ? "k_grouped_fp8_gemm_tn_contiguous (eight epilogue warps)"
-                         : "k_grouped_fp8_gemm_tn_contiguous",
+  print_config(args.mc     ? "k_grouped_fp8_gemm_tn_contiguous (eight epilogue warps, clusters of 2 sharing B by multicast)"
+               : args.epi8 ? "k_grouped_fp8_gemm_tn_contiguous (eight epilogue warps)"
+                           : "k_grouped_fp8_gemm_tn_contiguous",
                m, n, sum_k, num_groups, kBlockM, block_n, gemm_stages(block_n), grid, args.band);
   return from_cuda(gemm_launch(kKGrouped, block_n, o.a, o.b, o.sfa, o.sfb, o.d, args, grid, st));
 }
