@@ -34,7 +34,8 @@ int gated_decode_max_clusters(int tn, int split);  // that run at once on the cu
 
 
 // gated_gemv.cu: one to four tokens without the tensor cores
-bool gated_gemv_takes(int64_t m, int64_t f, int64_t k, bool eight_bit, int sms);
+// sms: SMs it may use; limited: fewer than the device has
+bool gated_gemv_takes(int64_t m, int64_t f, int64_t k, bool eight_bit, int sms, bool limited);
 cudaError_t gated_gemv_launch(const void* a, const void* sfa, const void* b, const void* sfb, int64_t lda, int64_t ldb,
                               const GatedArgs& args, cudaStream_t stream);
 

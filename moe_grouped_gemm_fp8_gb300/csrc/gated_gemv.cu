@@ -226,11 +226,14 @@ cudaError_t gv_launch(const GemvArgs& p, size_t smem, cudaStream_t stream) {
 // K = 1024, 4 tokens 7.0 / 9.6.  So: one token always; two where all CTAs run
 // at once; three and four where they do and K is short, since each token adds
 // its own products to every code.  Clusters of 8 need two CTAs an SM for that.
-bool gated_gemv_takes(int64_t m, int64_t f, int64_t k, bool eight_bit, int sms) {
+// The grid is as large as F asks, each CTA on whichever SM is free: under a limit
+// of the SMs to use it is taken only where it has no more CTAs than those.
+bool gated_gemv_takes(int64_t m, int64_t f, int64_t k, bool eight_bit, int sms, bool limited) {
   if (m < 1 || m > 4) return false;
   const int64_t tokens = m <= 2 ? m : 4;
   const int64_t smem = tokens * ((k + 511) / 512) * 2048 + kGvRingBytes;  // the tokens as FP32
   if (smem > kGvMaxSmem) return false;
+  if (limited && (f + kGvWarps - 1) / kGvWarps > sms) return false;
   if (m == 1) return true;
   const int64_t per_sm = std::min<int64_t>(2, kGvMaxSmem / (smem + 2048));
   const bool once = (f + kGvWarps - 1) / kGvWarps <= per_sm * sms && (!eight_bit || per_sm == 2);

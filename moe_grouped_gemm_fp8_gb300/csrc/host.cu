@@ -1428,6 +1428,14 @@ static int gated_decode_split(int64_t clusters, int64_t kb, int tn, int sms) {
   return best;
 }
 
+// A dg_set_num_sms limit below the current device's SMs (current_device has
+// succeeded).
+static bool sms_limited() {
+  const int limit = g_num_sms_limit.load();
+  int dev = 0;
+  return limit > 0 && cudaGetDevice(&dev) == cudaSuccess && limit < g_devices[dev].sms;
+}
+
 // The three forms of the gated product (mode kDense, kContiguous, kMasked).
 static dg_status gated_gemm(int mode, const char* name, const void* a, const int32_t* sfa, const void* b,
                             const int32_t* sfb, void* h, int32_t* h_sf, void* gu, int32_t* gu_sf,
@@ -1482,7 +1490,7 @@ static dg_status gated_gemm(int mode, const char* name, const void* a, const int
   args.activation = activation;
   // one to four tokens: without the tensor cores (test hooks of the pipelines want one of those)
   if (mode == kDense && env().decode != 0 && env().decode != 2 && args.base.debug_drop_load == 0 &&
-      gated_gemv_takes(m, f, k, h_sf || gu, sms)) {
+      gated_gemv_takes(m, f, k, h_sf || gu, sms, sms_limited())) {
     print_config("fp8_gated_gemm_nt (one to four tokens)", m, f, k, 1, (int)m, 16, 0, (int)((f + 15) / 16), 0);
     return from_cuda(gated_gemv_launch(a, sfa, b, sfb, lda, ldb, args, static_cast<cudaStream_t>(stream)));
   }
