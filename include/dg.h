@@ -403,9 +403,10 @@ dg_status dg_m_grouped_fp8_gated_gemm_nt_contiguous(const void* a, const int32_t
 
 /* The same for the masked layout: a [num_groups, max_m, k], b [num_groups,
  * 2f, k], h [num_groups, max_m, f] (h_sf [num_groups, ceil(f/512),
- * align(max_m, 4)]), masked_m and expected_m as
- * dg_m_grouped_fp8_gemm_nt_masked takes them.  Rows past masked_m[g] keep
- * what h and its scale words held. */
+ * align(max_m, 4)]), masked_m as dg_m_grouped_fp8_gemm_nt_masked takes it.
+ * expected_m stands in the same place as there and is checked (>= 0); this
+ * form has one tile, so it chooses nothing.  Rows past masked_m[g] keep what h
+ * and its scale words held. */
 dg_status dg_m_grouped_fp8_gated_gemm_nt_masked(const void* a, const int32_t* sfa, const void* b,
                                                 const int32_t* sfb, void* h, int32_t* h_sf,
                                                 const int32_t* masked_m, int32_t num_groups,

@@ -10,11 +10,12 @@
 // tokens wait in shared memory as FP32, their own scales multiplied in (exact),
 // in the order the lanes read them.
 //
-// One token, K = 7168, F = 2048: 8.7 us (29 MB, 3.4 TB/s; a plain streaming read
-// of as many bytes takes 7.1-7.4), F = 4096 14.1 us (4.2 TB/s).
+// One token, K = 7168, F = 2048: 8.5-8.8 us (29 MB, 3.4 TB/s; a plain streaming
+// read of as many bytes takes 7.1-7.4), F = 4096 13.8 us (4.2 TB/s).
 //
 // A group of 128 columns with one scale is 8 CTAs of 16 columns: for 8-bit
-// results they form a cluster and tell one another their columns' maxima.
+// results they form a cluster and tell one another their columns' maxima, which
+// at F = 2048 costs 5 us (13.4-13.9; K = 1024 1-1.6 us).
 #include <algorithm>
 
 #include "dg_device.cuh"
@@ -220,10 +221,10 @@ cudaError_t gv_launch(const GemvArgs& p, size_t smem, cudaStream_t stream) {
 
 // Measured against the kernel with swapped operand roles (weights from HBM, us
 // in a graph, this kernel / that one).  F = 2048, BF16: K = 7168, 1 token 8.7 /
-// 13.7, 2 tokens 10.7 / 14.1, 4 tokens 17.0 / 14.1; K = 1024, 4 tokens 5.4 /
-// 7.2; F = 4096, K = 7168: 1 token 14.1 / 15.2, 2 tokens 19.0 / 15.2.  With
-// 8-bit results, F = 2048: K = 7168, 1 token 13.6 / 16.6, 2 tokens 21.4 / 16.5;
-// K = 1024, 4 tokens 7.0 / 9.6.  So: one token always; two where all CTAs run
+// 13.7, 2 tokens 10.4 / 13.9, 4 tokens 17.0 / 14.1; K = 1024, 4 tokens 5.3 /
+// 7.2; F = 4096, K = 7168: 1 token 13.8 / 14.9, 2 tokens 19.0 / 15.2.  With
+// 8-bit results, F = 2048: K = 7168, 1 token 13.4 / 14.7, 2 tokens 21.4 / 14.9;
+// K = 1024, 4 tokens 7.5 / 8.0; F = 4096, K = 7168, 1 token 14.9 / 16.0.  So: one token always; two where all CTAs run
 // at once; three and four where they do and K is short, since each token adds
 // its own products to every code.  Clusters of 8 need two CTAs an SM for that.
 // The grid is as large as F asks, each CTA on whichever SM is free: under a limit

@@ -278,7 +278,9 @@ def m_grouped_fp8_gated_gemm_nt_masked(a: torch.Tensor, sfa: torch.Tensor, b: to
                                        activation: str = "silu", out_format: str = "bf16",
                                        stream=None) -> GatedOutput:
     """fp8_gated_gemm_nt for the masked layout: A [G, max_m, K] x B [G, 2F, K];
-    rows at or past masked_m[g] (read on the device) are left as they are."""
+    rows at or past masked_m[g] (read on the device) are left as they are.
+    expected_m is taken as m_grouped_fp8_gemm_nt_masked takes it, and chooses
+    nothing here: this form has one tile."""
     if stream is not None:
         return _under(stream, m_grouped_fp8_gated_gemm_nt_masked, a, sfa, b, sfb, masked_m, expected_m, d, activation,
                       out_format)
