@@ -104,6 +104,9 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// The one nearer to zero; a where b is NaN.
+__device__ __forceinline__ float nearer(float a, float b) { return fabsf(b) < fabsf(a) ? b : a; }
+
 // Sum over the CTA; every thread gets it.  Two calls use different slots.
 __device__ __forceinline__ float row_sum(float v, float* red, int slot) {
   v = warp_sum(v);
@@ -293,9 +296,13 @@ struct AlignedRow {
 #pragma unroll
     for (int j = 0; j < NV; ++j) unpack16<T>(ld_shared_u4(from ^ (j * 16)), &v[j * V / 2]);
   }
-  // Of the pairs v[0] .. v[kPilot - 1]: values inside the row.
+  // Pairs of a lane whose means can stand for the warp's; one over how many of
+  // their first and of their second values lie inside the row (past it they are 0).
   static constexpr int kPilot = P < 8 ? P : 8;
-  __device__ __forceinline__ int pilot_count() const { return min(on * V, 2 * kPilot); }
+  __device__ __forceinline__ float2 pilot_weights() const {
+    const float r = 1.0f / (float)max(min(on * V / 2, kPilot), 1);
+    return make_float2(r, r);
+  }
   __device__ __forceinline__ void params(const void* p, bool fp32, bool wide, float2 (&v)[P]) const {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -405,12 +412,15 @@ struct RaggedRow {
     }
     src += step;
   }
-  static constexpr int kPilot = P < 8 ? P : 8;
-  __device__ __forceinline__ int pilot_count() const {
-    int n = 0;
+  static constexpr int kPilot = 2;  // (eight cost 16384 x 7167 BF16 5%)
+  __device__ __forceinline__ float2 pilot_weights() const {
+    int a = 0, b = 0;
 #pragma unroll
-    for (int k = 0; k < kPilot; ++k) n += (col(k, 0) < cols) + (col(k, 1) < cols);
-    return n;
+    for (int k = 0; k < kPilot; ++k) {
+      a += col(k, 0) < cols;
+      b += col(k, 1) < cols;
+    }
+    return make_float2(1.0f / (float)max(a, 1), 1.0f / (float)b);  // none: 0 inf, which is never nearer
   }
   __device__ __forceinline__ void read(int off, float2 (&v)[P]) {
     const uint8_t* p = reinterpret_cast<const uint8_t*>(mine) + off + (at & 15u);
@@ -543,7 +553,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) layer_norm_ring_kernel(const 
   }
   __syncthreads();
   const float rn = 1.0f / (float)cols;
-  const float r_pilot = 1.0f / (float)max(src.pilot_count(), 1);
+  const float2 r_pilot = src.pilot_weights();
   const float r_warp = 1.0f / (float)max(min(cols - (tid - lane) * 2 * P, 64 * P), 1);
   const int peer = lane & (warps > 8 ? 15 : 7);  // the warp whose part of the row's sums the lane takes
   const float n_peer = (float)max(min(cols - peer * 64 * P, 64 * P), 0);
@@ -560,12 +570,15 @@ __global__ void __launch_bounds__(kNormThreads, 1) layer_norm_ring_kernel(const 
     src.read(at, v);
     const int slot = at;
     at = at == last ? 0 : at + src.stage;
-    // Both sums at once, around a value near the warp's mean (the mean of up to
-    // 16 values of its first lane, so one stray value moves it little).
+    // Both sums at once, around a value near the warp's mean: the mean of a few
+    // values of its first lane, or of as many others where those are nearer to
+    // zero, so that one loud channel does not move it (every value is rounded at
+    // the size of its distance from it).
     float2 s = v[0];
 #pragma unroll
     for (int k = 1; k < Row::kPilot; ++k) s = add2(s, v[k]);
-    const float pilot = __shfl_sync(0xffffffffu, (s.x + s.y) * r_pilot, 0);
+    s = mul2(s, r_pilot);
+    const float pilot = __shfl_sync(0xffffffffu, nearer(s.x, s.y), 0);
     src.shift(v, -pilot);
     s = v[0];
     float2 d2 = mul2(v[0], v[0]);
@@ -581,7 +594,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) layer_norm_ring_kernel(const 
       s2 += __shfl_xor_sync(0xffffffffu, s2, o);
     }
     // The warp's mean and sum of squares around it; the row's from the warps',
-    // around the first warp's mean.
+    // around the reader's own pilot (so two warps' may differ in the last bit).
     float mean = pilot + s1 * r_warp;
     s2 -= s1 * s1 * r_warp;
     if (warps > 1) {
@@ -589,8 +602,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) layer_norm_ring_kernel(const 
       if (lane == 0) r[tid >> 5] = make_float2(mean, s2);
       asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
       const float2 of = r[min(peer, warps - 1)];
-      const float m0 = r[0].x;
-      const float d = of.x - m0;
+      const float d = of.x - pilot;
       s1 = n_peer * d;
       s2 = peer < warps ? s1 * d + of.y : 0.0f;
       if (warps > 8) {
@@ -602,7 +614,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) layer_norm_ring_kernel(const 
         s1 += __shfl_xor_sync(0xffffffffu, s1, o);
         s2 += __shfl_xor_sync(0xffffffffu, s2, o);
       }
-      mean = m0 + s1 * rn;
+      mean = pilot + s1 * rn;
       s2 -= s1 * s1 * rn;
     }
     const float rstd = rsqrt_newton((s2 < 0.0f ? 0.0f : s2) * rn + p.eps);

@@ -1,5 +1,5 @@
 """Layer norm at its edges: rows without spread at eps = 0, rows too wide for the
-ring, and what lies around its results."""
+ring, loud channels and large means, and what lies around its results."""
 import pytest
 import torch
 
@@ -77,3 +77,26 @@ def test_nothing_around_the_results_is_written(dtype, rows, cols, at):
     for big, part in (y, mean, rstd, dx, dw, db):
         assert intact(big, part, at)
     assert bool((ws[:room] == 7).all()) and bool((ws[room + need // 4:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [40, 256, 1001, 2048, 7168, 16384])
+def test_one_loud_channel(dtype, cols):
+    """A value a thousand to a million times the others, wherever it lies: the
+    others keep their digits (the bound is that of any row)."""
+    at = [c for c in (0, 1, 2, 3, 5, 8, 15, 16, 31, 33, 64, 200, 511, 1000, 2047, 7000) if c < cols]
+    x, w, b, _ = L._inputs(len(at) * 3, cols, torch.float32, cols, mean=0.0)
+    for i, c in enumerate(at):
+        for j, loud in enumerate((1e3, -3e4, 1e6)):
+            x[3 * i + j, c] = loud
+    x = x.to(dtype)
+    L._check_forward(dg.layer_norm(x.cuda(), w.cuda(), b.cuda(), eps=L.EPS), x, w, b)
+
+
+@pytest.mark.parametrize("cols", [1, 2, 3, 4, 5, 33, 65, 66, 67, 96, 130, 513, 1025, 2049, 4100, 7169])
+def test_a_large_mean_at_any_width(cols):
+    """Rows whose mean is 2^12 times their spread, also where a warp's first
+    values are partly past the row's end."""
+    x, w, b, _ = L._inputs(9, cols, torch.float32, cols, mean=0.0)
+    x += 4096.0 * torch.arange(1, 10)[:, None]
+    L._check_forward(dg.layer_norm(x.cuda(), w.cuda(), b.cuda(), eps=L.EPS), x, w, b)
