@@ -94,17 +94,9 @@ class Side:
 
 @pytest.fixture
 def current(calls, monkeypatch):
-    """The streams made current, innermost last; raw handle 7 stands for a side stream."""
-    from contextlib import contextmanager
+    """The current stream, last; raw handle 7 stands for a side stream."""
     stack = [Side(0)]
-
-    @contextmanager
-    def under(s):
-        stack.append(s)
-        yield
-        stack.pop()
-
-    monkeypatch.setattr(torch.cuda, "stream", under)
+    monkeypatch.setattr(torch.cuda, "set_stream", lambda s: stack.__setitem__(-1, s))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda: stack[-1])
     monkeypatch.setattr(torch.cuda, "default_stream", lambda: stack[0])
     monkeypatch.setattr(torch.cuda, "ExternalStream", Side)
