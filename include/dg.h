@@ -471,6 +471,82 @@ dg_status dg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, c
 dg_status dg_layer_norm_backward_workspace_size(int64_t cols, int32_t num_sms, uint64_t* bytes);
 
 /* ------------------------------------------------------------------------ */
+/* A mixture-of-experts layer for a few tokens                               */
+/* ------------------------------------------------------------------------ */
+
+/* Scores of the experts, from the logits l = x router^T of a token:
+ *   SOFTMAX   s = exp(l) / sum of exp(l) over the experts
+ *   SIGMOID   s = 1 / (1 + exp(-l)) */
+typedef enum dg_score { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
+
+/* The whole layer, gate included, for 0 to 64 tokens:
+ *   the top_k experts of each token with the largest logits (with a
+ *   router_bias: the largest s + bias), ties to the lowest index, what is no
+ *   number after every number; weights w = s of those, divided by their sum
+ *   with renormalize != 0, times scale;
+ *   h = act(x Wg^T) * (x Wu^T) of each chosen expert,
+ *   y = c + sum over the chosen of w h Wd^T.
+ * Logits are summed so exactly (about 48 bits) that near scores keep their
+ * order; x and h enter the products with 11 bits at least (no rounding to 8
+ * bits), all sums are FP32 and y is rounded once.
+ *   x        BF16 [tokens, d], row stride ldx (ldx >= d, ldx % 8 == 0)
+ *   router   [num_experts, d] of router_dtype (DG_DTYPE_FP32 or _BF16)
+ *   router_bias  float [num_experts] or NULL; only with DG_SCORE_SIGMOID
+ *   up, up_sf    E4M3 [num_experts, 2f, d] (gate rows, then up rows) and packed
+ *            scales int32 [num_experts, ceil(d/512), 2f]
+ *   down, down_sf  E4M3 [num_experts, d, f], int32 [num_experts, ceil(f/512), d]
+ *   c        BF16 [tokens, d], row stride ldc, or NULL; may be y or x
+ *   num_tokens  int32 on the device or NULL: only rows below it are tokens
+ *            (the rest of a captured graph's batch); y's other rows are not
+ *            written.  Outside [0, tokens]: DG_ERR_DEVICE_BAD_INDEX is
+ *            recorded and the nearest bound taken.
+ *   y        BF16 [tokens, d], row stride ldy; may be x
+ *   experts  int32 [tokens, top_k], weights float [tokens, top_k]: the choice
+ *            of each token, best first; -1 and 0 in rows that are no tokens
+ *   workspace  dg_fp8_moe_few_tokens_workspace_size bytes, 16-byte aligned;
+ *            needs no initialisation.  Calls that can overlap on the device
+ *            need separate ones.
+ * d % 128 == 0, f % 128 == 0, both at most 65536; num_experts <= 512, top_k <=
+ * 16.  Results are reproducible bit for bit on the same SM count.  Two kernels;
+ * the second is a cooperative launch with one barrier over its grid, whose
+ * wait is bounded by dg_set_wait_timeout_ns. */
+dg_status dg_fp8_moe_few_tokens(const void* x, int64_t ldx, const void* router, int32_t router_dtype,
+                                const float* router_bias, const void* up, const int32_t* up_sf,
+                                const void* down, const int32_t* down_sf, const void* c, int64_t ldc,
+                                const int32_t* num_tokens, void* y, int64_t ldy, int32_t* experts,
+                                float* weights, void* workspace, uint64_t workspace_bytes,
+                                int32_t tokens, int64_t d, int64_t f, int32_t num_experts,
+                                int32_t top_k, int32_t score, int32_t renormalize, float scale,
+                                int32_t activation, void* stream);
+dg_status dg_fp8_moe_few_tokens_workspace_size(int32_t tokens, int64_t d, int64_t f,
+                                               int32_t num_experts, int32_t top_k, uint64_t* bytes);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit integers with a scale per token and per channel                     */
+/* ------------------------------------------------------------------------ */
+
+/* D[m, n] = C[m, n] + sa[m] sb[n] sum over k of a[m, k] b[n, k]
+ *   a        int8 [m, k], row stride lda (lda >= k, lda % 16 == 0), 16-byte aligned
+ *   sa       float [m], one scale per row (token)
+ *   b        int8 [n, k], row stride ldb likewise;  sb  float [n], one per row (channel)
+ *   c        [m, n] of out_dtype, row stride ldc >= n, or NULL; may be d when ldc == ldd
+ *   d        [m, n] of out_dtype (DG_DTYPE_BF16 or DG_DTYPE_FP16), row stride ldd >= n
+ * k % 16 == 0, any m and n, all 256 codes.  Products are exact, sums FP32, one
+ * rounding.  (Rows of d and c on 16 bytes are written 16 bytes at a time.) */
+dg_status dg_int8_gemm_nt(const void* a, const float* sa, const void* b, const float* sb, const void* c,
+                          void* d, int64_t m, int64_t n, int64_t k, int64_t lda, int64_t ldb, int64_t ldc,
+                          int64_t ldd, int32_t out_dtype, void* stream);
+
+/* Rows of x [rows, cols] of `dtype`, row stride ldx >= cols, as codes and one
+ * scale each: scale = amax / 127, code = the integer nearest to 127 x / amax,
+ * ties to even (of the exact quotient); a row of zeros has scale 0.  A row with
+ * an infinity or NaN has NaN as its scale and codes 0, so that products with it
+ * show it.
+ *   q  int8 [rows, cols] (contiguous), scales  float [rows]; cols >= 1 */
+dg_status dg_quantize_int8(const void* x, int32_t dtype, void* q, float* scales, int64_t rows,
+                           int64_t cols, int64_t ldx, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Utilities (same page, section "Utilitários e variáveis de ambiente")      */
 /* ------------------------------------------------------------------------ */
 

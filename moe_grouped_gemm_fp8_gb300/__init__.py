@@ -50,5 +50,11 @@ from .feedforward import (  # noqa: F401
     m_grouped_fp8_gated_gemm_nt_masked,
     requantize_fp8_cols,
 )
+from .serving import (  # noqa: F401
+    MoeOutput,
+    fp8_moe_few_tokens,
+    int8_gemm_nt,
+    quantize_int8,
+)
 
 __version__ = "0.1.0"

@@ -21,6 +21,7 @@ from .api import (fp8_gemm_nn, fp8_gemm_nt, k_grouped_fp8_gemm_tn_contiguous, m_
 from .feedforward import (fp8_gated_backward, fp8_gated_gemm_nt, layer_norm, layer_norm_backward,
                           m_grouped_fp8_gated_gemm_nt_contiguous, m_grouped_fp8_gated_gemm_nt_masked,
                           requantize_fp8_cols)
+from .serving import MoeOutput, fp8_moe_few_tokens
 
 
 class Weight(NamedTuple):
@@ -119,6 +120,12 @@ class GatedExperts:
         r = m_grouped_fp8_gated_gemm_nt_masked(x, x_sf, self.up.q, self.up.sf, masked_m, expected_m=expected_m,
                                                activation=self.activation, out_format="fp8")
         return m_grouped_fp8_gemm_nt_masked(r.h, r.h_sf, self.down.q, self.down.sf, masked_m, expected_m=expected_m)
+
+    def few_tokens(self, x: torch.Tensor, router: torch.Tensor, top_k: int, **options) -> MoeOutput:
+        """The whole layer for up to 64 tokens, gate included: x BF16 [T, D], router
+        [G, D]; options as fp8_moe_few_tokens takes them (c: the residual)."""
+        return fp8_moe_few_tokens(x, router, self.up.q, self.up.sf, self.down.q, self.down.sf, top_k,
+                                  activation=self.activation, **options)
 
     def backward(self, dy: torch.Tensor, x: torch.Tensor, x_sf: torch.Tensor, checkpoint, m_indices: torch.Tensor,
                  ks: torch.Tensor):

@@ -62,6 +62,8 @@ enum ErrorSite : uint32_t {
   kSiteContiguousIndex = 16,
   kSiteMaskedCount = 17,
   kSiteKGroupSize = 18,
+  kSiteMoeTokens = 19,
+  kSiteMoeBarrier = 20,
   kSiteTransformScale = 32,
 };
 

@@ -17,6 +17,8 @@
 
 #include "dg_internal.h"
 #include "gated_gemm.h"
+#include "int8_gemm.h"
+#include "moe.h"
 
 namespace dg {
 namespace {
@@ -1647,6 +1649,143 @@ dg_status dg_layer_norm_backward(const void* dy, const void* x, int32_t dtype, c
                                               dweight, dbias, static_cast<float*>(workspace),
                                               layer_norm_backward_parts(sms), rows, cols, lddy, ldx,
                                               g_pdl.load() != 0, static_cast<cudaStream_t>(stream)));
+}
+
+static dg_status check_moe(int32_t tokens, int64_t d, int64_t f, int32_t num_experts, int32_t top_k) {
+  if (tokens < 0 || d < 1 || f < 1 || num_experts < 1 || top_k < 1 || top_k > num_experts) return DG_ERR_INVALID_ARG;
+  if (d % kBlockK != 0 || f % kBlockK != 0) return DG_ERR_ALIGNMENT;
+  if (tokens > kMoeMaxTokens || top_k > kMoeMaxTopK || num_experts > kMoeMaxExperts || d > 65536 || f > 65536)
+    return DG_ERR_TOO_LARGE;
+  return DG_OK;
+}
+
+static bool aligned_to(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+static MoeArgs moe_sizes(int32_t tokens, int64_t d, int64_t f, int32_t num_experts, int32_t top_k) {
+  MoeArgs a = {};
+  a.tokens = tokens;
+  a.d = (int32_t)d;
+  a.f = (int32_t)f;
+  a.experts = num_experts;
+  a.top_k = top_k;
+  return a;
+}
+
+dg_status dg_fp8_moe_few_tokens_workspace_size(int32_t tokens, int64_t d, int64_t f, int32_t num_experts,
+                                               int32_t top_k, uint64_t* bytes) {
+  if (!bytes) return DG_ERR_INVALID_ARG;
+  dg_status s = check_moe(tokens, d, f, num_experts, top_k);
+  if (s != DG_OK) return s;
+  MoeArgs a = moe_sizes(tokens, d, f, num_experts, top_k);
+  *bytes = moe_few_tokens_layout(a, nullptr);
+  return DG_OK;
+}
+
+dg_status dg_fp8_moe_few_tokens(const void* x, int64_t ldx, const void* router, int32_t router_dtype,
+                                const float* router_bias, const void* up, const int32_t* up_sf,
+                                const void* down, const int32_t* down_sf, const void* c, int64_t ldc,
+                                const int32_t* num_tokens, void* y, int64_t ldy, int32_t* experts,
+                                float* weights, void* workspace, uint64_t workspace_bytes, int32_t tokens,
+                                int64_t d, int64_t f, int32_t num_experts, int32_t top_k, int32_t score,
+                                int32_t renormalize, float scale, int32_t activation, void* stream) {
+  dg_status s = check_moe(tokens, d, f, num_experts, top_k);
+  if (s != DG_OK) return s;
+  if (router_dtype != DG_DTYPE_FP32 && router_dtype != DG_DTYPE_BF16) return DG_ERR_INVALID_ARG;
+  if (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID) return DG_ERR_INVALID_ARG;
+  if (router_bias && score != DG_SCORE_SIGMOID) return DG_ERR_INVALID_ARG;
+  if (activation != DG_ACT_SILU && activation != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
+  if (ldx < d || ldy < d || (c && ldc < d)) return DG_ERR_INVALID_ARG;
+  if (tokens == 0) return DG_OK;
+  if (!x || !router || !up || !up_sf || !down || !down_sf || !y || !experts || !weights || !workspace)
+    return DG_ERR_INVALID_ARG;
+  if (ldx % 8 != 0 || !aligned16(x) || !aligned16(router) || !aligned16(up) || !aligned16(down) ||
+      !aligned_to(up_sf, 4) || !aligned_to(down_sf, 4) || !aligned_to(router_bias, 4) || !aligned_to(c, 2) ||
+      !aligned_to(y, 2) || !aligned_to(num_tokens, 4) || !aligned_to(experts, 4) || !aligned_to(weights, 4) ||
+      !aligned16(workspace))
+    return DG_ERR_ALIGNMENT;
+  MoeArgs a = moe_sizes(tokens, d, f, num_experts, top_k);
+  if (workspace_bytes < moe_few_tokens_layout(a, workspace)) return DG_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((s = current_device(&sms)) != DG_OK) return s;
+  a.x = static_cast<const __nv_bfloat16*>(x);
+  a.router = router;
+  a.router_bias = router_bias;
+  a.up = static_cast<const uint8_t*>(up);
+  a.up_sf = reinterpret_cast<const uint32_t*>(up_sf);
+  a.down = static_cast<const uint8_t*>(down);
+  a.down_sf = reinterpret_cast<const uint32_t*>(down_sf);
+  a.c = static_cast<const __nv_bfloat16*>(c);
+  a.num_tokens = num_tokens;
+  a.y = static_cast<__nv_bfloat16*>(y);
+  a.chosen_out = experts;
+  a.weight_out = weights;
+  a.ldx = ldx;
+  a.ldc = ldc;
+  a.ldy = ldy;
+  a.score = score;
+  a.renormalize = renormalize != 0;
+  a.activation = activation;
+  a.scale = scale;
+  a.timeout_ns = g_timeout_ns.load();
+  return from_cuda(moe_few_tokens_launch(a, router_dtype == DG_DTYPE_FP32, sms, g_pdl.load() != 0,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_int8_gemm_nt(const void* a, const float* sa, const void* b, const float* sb, const void* c,
+                          void* d, int64_t m, int64_t n, int64_t k, int64_t lda, int64_t ldb, int64_t ldc,
+                          int64_t ldd, int32_t out_dtype, void* stream) {
+  if (m < 0 || n < 0 || k < 1) return DG_ERR_INVALID_ARG;
+  if (out_dtype != DG_DTYPE_BF16 && out_dtype != DG_DTYPE_FP16) return DG_ERR_INVALID_ARG;
+  if (k % 16 != 0) return DG_ERR_ALIGNMENT;
+  if (m == 0 || n == 0) return DG_OK;
+  if (!a || !sa || !b || !sb || !d) return DG_ERR_INVALID_ARG;
+  if (lda < k || ldb < k || ldd < n || (c && ldc < n)) return DG_ERR_INVALID_ARG;
+  if (c == d && ldc != ldd) return DG_ERR_INVALID_ARG;
+  if (lda % 16 != 0 || ldb % 16 != 0 || !aligned16(a) || !aligned16(b) || !aligned_to(sa, 4) || !aligned_to(sb, 4) ||
+      !aligned_to(c, 2) || !aligned_to(d, 2))
+    return DG_ERR_ALIGNMENT;
+  if (m >= kMaxCoord / 2 || n >= kMaxCoord / 2 || k >= kMaxCoord / 2 ||
+      ((m + 127) / 128) * ((n + 63) / 64) >= kMaxCoord / 2)
+    return DG_ERR_TOO_LARGE;
+  Int8Args p = {};
+  int sms = 0;
+  dg_status s = current_device(&sms);
+  if (s != DG_OK) return s;
+  p.a = static_cast<const int8_t*>(a);
+  p.sa = sa;
+  p.b = static_cast<const int8_t*>(b);
+  p.sb = sb;
+  p.c = c;
+  p.d = d;
+  p.lda = lda;
+  p.ldb = ldb;
+  p.ldc = c ? ldc : 0;
+  p.ldd = ldd;
+  p.m = (int32_t)m;
+  p.n = (int32_t)n;
+  p.k = (int32_t)k;
+  p.fp16 = out_dtype == DG_DTYPE_FP16;
+  p.vector = aligned16(d) && ldd % 8 == 0 && (!c || (aligned16(c) && ldc % 8 == 0));
+  p.sms = sms;
+  p.timeout_ns = g_timeout_ns.load();
+  const bool pdl = g_pdl.load() != 0;
+  return from_cuda(m <= int8_stream_max_tokens() ? int8_stream_launch(p, pdl, static_cast<cudaStream_t>(stream))
+                                                 : int8_gemm_launch(p, pdl, static_cast<cudaStream_t>(stream)));
+}
+
+dg_status dg_quantize_int8(const void* x, int32_t dtype, void* q, float* scales, int64_t rows, int64_t cols,
+                           int64_t ldx, void* stream) {
+  if (rows < 0 || cols < 1 || ldx < cols) return DG_ERR_INVALID_ARG;
+  if (dtype != DG_DTYPE_FP32 && dtype != DG_DTYPE_BF16 && dtype != DG_DTYPE_FP16) return DG_ERR_INVALID_ARG;
+  if (rows == 0) return DG_OK;
+  if (!x || !q || !scales) return DG_ERR_INVALID_ARG;
+  if (!aligned_to(x, dtype == DG_DTYPE_FP32 ? 4 : 2) || !aligned_to(scales, 4)) return DG_ERR_ALIGNMENT;
+  if (rows >= kMaxCoord - 8 || cols >= kMaxCoord / 2) return DG_ERR_TOO_LARGE;
+  int sms = 0;
+  dg_status s = current_device(&sms);
+  if (s != DG_OK) return s;
+  return from_cuda(quantize_int8_launch(x, dtype, static_cast<int8_t*>(q), scales, rows, cols, ldx, g_pdl.load() != 0,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 int64_t dg_get_tma_aligned_size(int64_t x, int32_t element_size) {

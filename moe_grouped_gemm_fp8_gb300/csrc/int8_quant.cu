@@ -1,0 +1,213 @@
+// Rows to 8-bit integers: scale = amax / 127, code = the integer nearest to
+// 127 x / amax, ties to even, of the exact quotient (so the codes do not depend
+// on how a division or a reciprocal rounds).
+//
+// Bound by HBM.  A row is read once and stays in registers between its maximum
+// and its codes.  The quotient is estimated as x (127 / amax), off by at most
+// 2^-16 at 127; only where it lies nearer than that to a half integer are
+// 254 |x| and (2 n + 1) amax compared, in FP64, which holds both exactly.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "dg_device.cuh"
+#include "dg_ops.cuh"
+#include "int8_gemm.h"
+
+namespace dg {
+namespace {
+
+constexpr int kQiItems = 32;  // values a thread keeps (16-bit types; FP32: 16)
+
+template <class T>
+__device__ __forceinline__ float qi_float(T v) {
+  if constexpr (std::is_same<T, float>::value) return v;
+  else if constexpr (std::is_same<T, __half>::value) return __half2float(v);
+  else return __bfloat162float(v);
+}
+template <class T>
+__device__ __forceinline__ void qi_unpack(const uint4& a, float* v) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
+    else if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    } else {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
+}
+
+// max(m, |v|), NaN where either is
+__device__ __forceinline__ float qi_max(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
+
+// The code of v by comparison in FP64.  Tiny amax: 127 v / amax itself, whose
+// FP64 rounding cannot reach a half integer (31 bits over 24).
+__device__ __noinline__ int qi_exact(float v, float amax) {
+  const double a = fabs((double)v), top = (double)amax;
+  double n = floor(127.0 * a / top);
+  n = fmin(n, 127.0);
+  const double twice = 254.0 * a, mid = (2.0 * n + 1.0) * top;
+  if (twice > mid || (twice == mid && ((int)n & 1))) n += 1.0;
+  return v < 0.0f ? -(int)n : (int)n;
+}
+
+// Four values -> four codes in a word.  far: the largest distance of an
+// estimate from its integer.
+__device__ __forceinline__ uint32_t qi_four(const float* v, float inv, float& far) {
+  const float2 magic = make_float2(12582912.0f, 12582912.0f), back = make_float2(-12582912.0f, -12582912.0f);
+  const float2 t0 = mul2(make_float2(v[0], v[1]), inv), t1 = mul2(make_float2(v[2], v[3]), inv);
+  const float2 u0 = add2(t0, magic), u1 = add2(t1, magic);
+  const float2 n0 = add2(u0, back), n1 = add2(u1, back);
+  const float2 f0 = fma2(n0, make_float2(-1.0f, -1.0f), t0), f1 = fma2(n1, make_float2(-1.0f, -1.0f), t1);
+  far = abs_max3(abs_max3(far, f0.x, f0.y), f1.x, f1.y);
+  const uint32_t a = __byte_perm(__float_as_uint(u0.x), __float_as_uint(u0.y), 0x0040);
+  const uint32_t b = __byte_perm(__float_as_uint(u1.x), __float_as_uint(u1.y), 0x0040);
+  return __byte_perm(a, b, 0x5410);
+}
+
+// Estimates off by more than this from a half integer round as the exact
+// quotient does: 127 (2^-24 + 2^-24) < 2^-16 for the reciprocal's and the
+// product's rounding.
+constexpr float kQiSafe = 0.5f - 1.0f / 32768.0f;
+constexpr float kQiTiny = 1e-30f;  // below it 127 / amax may overflow
+
+// W warps a row.  VEC: rows of x on 16 bytes and of codes on 16 / sizeof(T);
+// else a value at a time.
+template <class T, int W, bool VEC>
+__global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W)
+    quantize_int8_kernel(const T* __restrict__ x, int8_t* __restrict__ q, float* __restrict__ scales, int64_t rows,
+                         int cols, int64_t ldx) {
+  constexpr int E = 16 / sizeof(T), V = kQiItems * 2 / sizeof(T) / E, PER = E * V;
+  constexpr int kThreads = W <= 8 ? 256 : 32 * W, kRows = kThreads / (32 * W);
+  __shared__ float part[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int at = threadIdx.x % (32 * W);  // in the row's threads
+  const int64_t row = (int64_t)blockIdx.x * kRows + warp / W;
+  const bool on = row < rows;
+  const T* xr = x + (on ? row : 0) * ldx;
+  const int n = on ? cols : 0;
+  constexpr int kWide = 32 * W * PER;  // columns of a pass; more than one only at the widest W
+  float v[PER];
+  float m = 0.0f;
+  auto load = [&](int c0) {
+    if constexpr (VEC) {
+      uint4 w[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = c0 + (i * 32 * W + at) * E;
+        w[i] = c < n ? ld_stream_u4(xr + c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) qi_unpack<T>(w[i], v + i * E);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = c0 + i * 32 * W + at;
+        v[i] = c < n ? qi_float(xr[c]) : 0.0f;
+      }
+    }
+  };
+  const bool once = cols <= kWide;
+  for (int c0 = 0; c0 == 0 || c0 < cols; c0 += kWide) {
+    load(c0);
+#pragma unroll
+    for (int i = 0; i < PER; i += 2) m = qi_max(m, v[i], v[i + 1]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = qi_max(m, __shfl_xor_sync(0xffffffffu, m, o), 0.0f);
+  if constexpr (W > 1) {
+    if (lane == 0) part[warp] = m;
+    __syncthreads();
+    const int first = warp / W * W;
+#pragma unroll
+    for (int i = 0; i < W; ++i) m = qi_max(m, part[first + i], 0.0f);
+  }
+  if (!on) return;
+  const bool finite = m < INFINITY;
+  // a row that is not finite: no number as its scale, codes 0
+  if (at == 0) scales[row] = finite ? m / 127.0f : __uint_as_float(0x7FC00000u);
+  const bool tiny = m < kQiTiny;
+  const float inv = finite && !tiny ? 127.0f / m : 0.0f;
+  int8_t* qr = q + row * cols;
+  for (int c0 = 0; c0 == 0 || c0 < cols; c0 += kWide) {
+    if (!once) load(c0);
+    if (!finite) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+    }
+    float far = 0.0f;
+    uint32_t w[PER / 4];
+#pragma unroll
+    for (int i = 0; i < PER / 4; ++i) w[i] = qi_four(v + 4 * i, inv, far);
+    if (far > kQiSafe || (tiny && m > 0.0f)) {
+#pragma unroll
+      for (int i = 0; i < PER / 4; ++i) {
+        w[i] = 0;
+        for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)qi_exact(v[4 * i + j], m) & 0xFFu) << (8 * j);
+      }
+    }
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = c0 + (i * 32 * W + at) * E;
+        if (c < n) {
+          if constexpr (E == 8) *reinterpret_cast<uint2*>(qr + c) = make_uint2(w[2 * i], w[2 * i + 1]);
+          else *reinterpret_cast<uint32_t*>(qr + c) = w[i];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = c0 + i * 32 * W + at;
+        if (c < n) qr[c] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
+      }
+    }
+  }
+}
+
+template <class T, int W>
+cudaError_t qi_launch(const void* x, int8_t* q, float* scales, int64_t rows, int64_t cols, int64_t ldx, bool pdl,
+                      cudaStream_t stream) {
+  constexpr int kThreads = W <= 8 ? 256 : 32 * W, kRows = kThreads / (32 * W), E = 16 / sizeof(T);
+  const bool vec = cols % E == 0 && ldx % E == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(q) % E == 0;
+  const dim3 grid((unsigned)((rows + kRows - 1) / kRows));
+  const T* xt = static_cast<const T*>(x);
+  return vec ? launch_op(quantize_int8_kernel<T, W, true>, grid, kThreads, 0, pdl, stream, xt, q, scales, rows, (int)cols, ldx)
+             : launch_op(quantize_int8_kernel<T, W, false>, grid, kThreads, 0, pdl, stream, xt, q, scales, rows, (int)cols, ldx);
+}
+
+template <class T>
+cudaError_t qi_dispatch(const void* x, int8_t* q, float* scales, int64_t rows, int64_t cols, int64_t ldx, bool pdl,
+                        cudaStream_t stream) {
+  constexpr int kPer = kQiItems * 2 / sizeof(T) * 32;  // columns of a warp
+  if (cols <= kPer) return qi_launch<T, 1>(x, q, scales, rows, cols, ldx, pdl, stream);
+  if (cols <= 2 * kPer) return qi_launch<T, 2>(x, q, scales, rows, cols, ldx, pdl, stream);
+  if (cols <= 4 * kPer) return qi_launch<T, 4>(x, q, scales, rows, cols, ldx, pdl, stream);
+  if (cols <= 8 * kPer) return qi_launch<T, 8>(x, q, scales, rows, cols, ldx, pdl, stream);
+  return qi_launch<T, 16>(x, q, scales, rows, cols, ldx, pdl, stream);
+}
+
+}  // namespace
+
+cudaError_t quantize_int8_launch(const void* x, int dtype, int8_t* q, float* scales, int64_t rows, int64_t cols,
+                                 int64_t ldx, bool pdl, cudaStream_t stream) {
+  if (dtype == DG_DTYPE_FP32) return qi_dispatch<float>(x, q, scales, rows, cols, ldx, pdl, stream);
+  if (dtype == DG_DTYPE_FP16) return qi_dispatch<__half>(x, q, scales, rows, cols, ldx, pdl, stream);
+  return qi_dispatch<__nv_bfloat16>(x, q, scales, rows, cols, ldx, pdl, stream);
+}
+
+}  // namespace dg
