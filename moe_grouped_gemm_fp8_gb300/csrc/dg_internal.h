@@ -64,6 +64,7 @@ enum ErrorSite : uint32_t {
   kSiteKGroupSize = 18,
   kSiteMoeTokens = 19,
   kSiteMoeBarrier = 20,
+  kSiteMoeSums = 21,
   kSiteTransformScale = 32,
 };
 

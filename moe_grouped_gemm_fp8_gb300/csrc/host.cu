@@ -1699,7 +1699,7 @@ dg_status dg_fp8_moe_few_tokens(const void* x, int64_t ldx, const void* router, 
   if (!x || !router || !up || !up_sf || !down || !down_sf || !y || !experts || !weights || !workspace)
     return DG_ERR_INVALID_ARG;
   if (ldx % 8 != 0 || !aligned16(x) || !aligned16(router) || !aligned16(up) || !aligned16(down) ||
-      !aligned_to(up_sf, 4) || !aligned_to(down_sf, 4) || !aligned_to(router_bias, 4) || !aligned_to(c, 2) ||
+      !aligned16(up_sf) || !aligned16(down_sf) || !aligned_to(router_bias, 4) || !aligned_to(c, 2) ||
       !aligned_to(y, 2) || !aligned_to(num_tokens, 4) || !aligned_to(experts, 4) || !aligned_to(weights, 4) ||
       !aligned16(workspace))
     return DG_ERR_ALIGNMENT;
@@ -1710,9 +1710,7 @@ dg_status dg_fp8_moe_few_tokens(const void* x, int64_t ldx, const void* router, 
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.router = router;
   a.router_bias = router_bias;
-  a.up = static_cast<const uint8_t*>(up);
   a.up_sf = reinterpret_cast<const uint32_t*>(up_sf);
-  a.down = static_cast<const uint8_t*>(down);
   a.down_sf = reinterpret_cast<const uint32_t*>(down_sf);
   a.c = static_cast<const __nv_bfloat16*>(c);
   a.num_tokens = num_tokens;
@@ -1727,7 +1725,14 @@ dg_status dg_fp8_moe_few_tokens(const void* x, int64_t ldx, const void* router, 
   a.activation = activation;
   a.scale = scale;
   a.timeout_ns = g_timeout_ns.load();
-  return from_cuda(moe_few_tokens_launch(a, router_dtype == DG_DTYPE_FP32, sms, g_pdl.load() != 0,
+  if ((s = get_encoder()) != DG_OK) return s;
+  const MoeEncode map = [](CUtensorMap* to, const void* base, uint64_t cols, uint64_t rows,
+                           uint32_t box_rows, uint32_t slices) {
+    const uint64_t dims[3] = {128, rows, cols / 128}, strides[2] = {cols, 128};
+    const uint32_t box[3] = {128, box_rows, slices};
+    return encode(to, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == DG_OK;
+  };
+  return from_cuda(moe_few_tokens_launch(a, up, down, map, router_dtype == DG_DTYPE_FP32, sms, g_pdl.load() != 0,
                                          static_cast<cudaStream_t>(stream)));
 }
 

@@ -5,7 +5,7 @@
 // Bound by HBM.  A row is read once and stays in registers between its maximum
 // and its codes.  The quotient is estimated as x (127 / amax), off by at most
 // 2^-16 at 127; only where it lies nearer than that to a half integer are
-// 254 |x| and (2 n + 1) amax compared, in FP64, which holds both exactly.
+// 254 |x| and (2 n + 1) amax compared, exactly.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -51,16 +51,23 @@ __device__ __forceinline__ float qi_max(float m, float a, float b) {
   return r;
 }
 
-// The code of v by comparison in FP64.  Tiny amax: 127 v / amax itself, whose
-// FP64 rounding cannot reach a half integer (31 bits over 24).
-__device__ __noinline__ int qi_exact(float v, float amax) {
-  const double a = fabs((double)v), top = (double)amax;
-  double n = floor(127.0 * a / top);
-  n = fmin(n, 127.0);
-  const double twice = 254.0 * a, mid = (2.0 * n + 1.0) * top;
-  if (twice > mid || (twice == mid && ((int)n & 1))) n += 1.0;
-  return v < 0.0f ? -(int)n : (int)n;
+// The code of v where its estimate lies near a half integer: 254 |v| against
+// (2 n + 1) amax, n below that half.  Both products are kept exactly as an FP32
+// and its rounding error; near each other, their difference is exact too.
+__device__ __forceinline__ int qi_settle(float v, float amax, float inv) {
+  // (2^-8 of both: 255 amax may be too large; every bit stays above 2^-149, as amax >= kQiTiny)
+  const float n = floorf(fabsf(v) * inv), odd = fmaf(2.0f, n, 1.0f);
+  const float a = fabsf(v) * 0.00390625f;
+  amax *= 0.00390625f;
+  const float p = __fmul_rn(254.0f, a), m = __fmul_rn(odd, amax);
+  const float d = (p - m) + (fmaf(254.0f, a, -p) - fmaf(odd, amax, -m));
+  const int c = (int)n;
+  const int code = d > 0.0f || (d == 0.0f && (c & 1)) ? c + 1 : c;
+  return v < 0.0f ? -code : code;
 }
+// The code of v where 127 / amax may overflow: the quotient in FP64, whose
+// rounding cannot reach a half integer (a 31-bit number over one of 24).
+__device__ __noinline__ int qi_tiny(float v, float amax) { return (int)rint(127.0 * (double)v / (double)amax); }
 
 // Four values -> four codes in a word.  far: the largest distance of an
 // estimate from its integer.
@@ -152,11 +159,21 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W)
     uint32_t w[PER / 4];
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i) w[i] = qi_four(v + 4 * i, inv, far);
-    if (far > kQiSafe || (tiny && m > 0.0f)) {
+    if (far > kQiSafe) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float t = v[i] * inv;
+        if (fabsf(t - rintf(t)) > kQiSafe) {
+          const int shift = 8 * (i % 4);
+          w[i / 4] = (w[i / 4] & ~(0xFFu << shift)) | ((uint32_t)qi_settle(v[i], m, inv) & 0xFFu) << shift;
+        }
+      }
+    }
+    if (tiny && m > 0.0f) {
 #pragma unroll
       for (int i = 0; i < PER / 4; ++i) {
         w[i] = 0;
-        for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)qi_exact(v[4 * i + j], m) & 0xFFu) << (8 * j);
+        for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)qi_tiny(v[4 * i + j], m) & 0xFFu) << (8 * j);
       }
     }
     if constexpr (VEC) {

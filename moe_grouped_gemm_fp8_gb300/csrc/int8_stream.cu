@@ -91,21 +91,22 @@ __global__ void __launch_bounds__(kIsThreads, 1) int8_stream_kernel(const Int8Ar
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) tokens(nb, x[nb]);
       cp_async_wait<RING - 1>();
-      uint32_t w[8][4];
-      stream_decode<DecodeInt8>(ring + stage * kIsStage, lane, w);
+      const uint8_t* at = ring + stage * kIsStage;
       stage = stage + 1 == RING ? 0 : stage + 1;
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        if constexpr (NB > 2) tokens(nb, x[0]);
-        const uint4(&xs)[2] = x[NB <= 2 ? nb : 0];
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[4][4];
+        stream_decode<DecodeInt8>(at, h, lane, w);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t xw[4] = {xs[h].x, xs[h].y, xs[h].z, xs[h].w};
+        for (int nb = 0; nb < NB; ++nb) {
+          if constexpr (NB > 2) tokens(nb, x[0]);
+          const uint4 xs = x[NB <= 2 ? nb : 0][h];
+          const uint32_t xw[4] = {xs.x, xs.y, xs.z, xs.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t b0, b1;
             DecodeInt8::four(xw[i], b0, b1);
-            mma_f16(acc[nb], w[h * 4 + i], b0, b1);
+            mma_f16(acc[nb], w[i], b0, b1);
           }
         }
       }

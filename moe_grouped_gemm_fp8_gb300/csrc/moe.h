@@ -1,8 +1,8 @@
 // Arguments and launch of the mixture-of-experts layer for a few tokens.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "dg_internal.h"
@@ -12,15 +12,19 @@ namespace dg {
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxTopK = 16;
 constexpr int kMoeMaxExperts = 512;
-constexpr int kMoeBarrierWords = 32;  // the grid barrier's counter, on a line of its own
+constexpr int kMoeMaxParts = 16;       // shares of the hit experts in the second product
+constexpr int kMoeBarrierWords = 32;  // the grid barrier's counter and those of the units
+
+// Encodes weights of `rows` rows and `cols` columns as bytes [cols / 128][rows][128]
+// in boxes of slices x box_rows x 128, 128-byte swizzle.
+using MoeEncode = bool (*)(CUtensorMap* to, const void* base, uint64_t cols, uint64_t rows,
+                           uint32_t box_rows, uint32_t slices);
 
 struct MoeArgs {
   const __nv_bfloat16* x;      // [tokens, d], row stride ldx
   const void* router;          // FP32 or BF16 [experts, d]
   const float* router_bias;    // nullable, [experts]
-  const uint8_t* up;           // E4M3 [experts, 2f, d] and packed scales
-  const uint32_t* up_sf;
-  const uint8_t* down;         // E4M3 [experts, d, f] and packed scales
+  const uint32_t* up_sf;       // packed scales of the weights
   const uint32_t* down_sf;
   const __nv_bfloat16* c;      // nullable, [tokens, d], row stride ldc
   const int32_t* num_tokens;   // nullable, on the device
@@ -34,19 +38,21 @@ struct MoeArgs {
   uint64_t timeout_ns;
   unsigned long long* err;
   // the workspace (moe_few_tokens_layout)
-  uint32_t* counter;           // grid barrier, then octets done of each (hit expert, 128 columns of h)
-  int32_t counters;
-  double* logits;              // [tokens, experts]
-  double* select;              // [tokens, experts]: scores with the bias, where there is one
-  __half* xh;                  // [tokens, d] in the streams' order, and a scale per 128
-  float* xs;
+  uint32_t* counter;           // grid barrier, units taken; octets done of each (hit expert, 128 columns of h);
+                               // from tile_counter: shares done of each rows of y
+  int32_t counters, tile_counter;
+  float2* logits;              // [tokens, experts], an FP32 and what it lacks
+  uint64_t* keys;              // [tokens, experts]: ordered as what the choice goes by
+  uint8_t* xh;                 // [tokens, d / 128] chunks as the products read them
   float* h;                    // [tokens * top_k, f], pairs in the order of their experts
-  __half* hh;                  // the same as halves in the streams' order, and a scale per 128
-  float* hs;
+  uint8_t* hh;                 // [tokens * top_k, f / 128] chunks
+  float* part;                 // [shares, tokens, d]
 };
 
 // Sets the workspace's pointers; the bytes it takes.
 uint64_t moe_few_tokens_layout(MoeArgs& a, void* workspace);
-cudaError_t moe_few_tokens_launch(MoeArgs p, bool router_fp32, int sms, bool pdl, cudaStream_t stream);
+// up: E4M3 [experts, 2f, d]; down: E4M3 [experts, d, f]
+cudaError_t moe_few_tokens_launch(MoeArgs p, const void* up, const void* down, MoeEncode encode, bool router_fp32,
+                                  int sms, bool pdl, cudaStream_t stream);
 
 }  // namespace dg

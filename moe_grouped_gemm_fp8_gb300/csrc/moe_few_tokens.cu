@@ -10,11 +10,17 @@
 // out the rows of the hit experts' Wg and Wu, meet at a barrier over the grid,
 // and share out the rows of Wd.
 //
-// Bound by reading the hit experts' weights once.  Each goes through the tensor
-// cores with all tokens of its expert at once (stream_mma.cuh).  x and h are
-// carried as halves with a power of two per 128 columns: 11 bits (BF16 x
-// exactly, but for values 2^29 below the largest of the 128), so that the only
-// roundings are those and the result's own.
+// Bound by reading the hit experts' weights once.  A producer warp keeps TMA
+// copies of 32 KB of weights and of their expert's tokens in flight; 16 warps
+// decode E4M3 to halves in registers (exact) and multiply by mma m16n8k16 with
+// all tokens of the expert at once, 16 rows x 128 columns a warp and stage.
+// tcgen05 would read the tokens' side at a 128-column tile's price for one to a
+// few tokens and, in its block-scaled form, round them to 8 bits.  Units of work
+// are taken from a counter: SMs read at rates that differ by a quarter.
+//
+// x and h are carried as halves with a power of two per 128 columns: 11 bits
+// (BF16 x exactly, but for values 2^29 below the largest of the 128), so that
+// the only roundings are those and the result's own.
 #include <algorithm>
 
 #include "dg_device.cuh"
@@ -25,13 +31,21 @@
 namespace dg {
 namespace {
 
-constexpr int kMoeWarps = 16;
-constexpr int kMoeThreads = 32 * kMoeWarps;
-constexpr int kMoeRing = 4;
-constexpr int kMoeSplit = 4;  // warps that share the columns of 16 rows of Wg and Wu
-constexpr int kMoeSlots = 1024;  // results of 16 rows of Wd waiting for their sum: (part, pair)
+constexpr int kMoeWarps = 16;     // that multiply
+constexpr int kMoeFinishers = 3;  // that finish units; one more fetches
+constexpr int kMoeThreads = 32 * (kMoeWarps + kMoeFinishers + 1);
+constexpr int kMoeStages = 6;        // at most
+constexpr int kMoeSmem = 209 * 1024;  // ring and exchange
 constexpr int kScoreThreads = 256;
 constexpr int kScoreTokens = 8;  // tokens of a CTA of the first kernel
+
+// A token's 128 columns: 128 halves in the order in which the lanes read them,
+// then their scale, and nothing up to a multiple of 16 bytes.  Lane (r, q) of a
+// warp holds, of weight rows r and r + 8, columns 32 q to 32 q + 31; product j
+// (0..7) multiplies columns 32 q + 4 j + 0..3 of every q.  Of the halves, unit
+// j / 2 comes first, then q, then 8 columns.
+constexpr int kMoeChunkBytes = 272;
+__device__ __forceinline__ int moe_half_at(int k) { return ((k >> 3) & 3) * 32 + (k >> 5) * 8 + (k & 7); }
 
 // ---------------------------------------------------------------- scores, and x as halves
 
@@ -82,18 +96,93 @@ __device__ __forceinline__ void load8(const R* p, float (&f)[8]) {
   }
 }
 
-// CTA (expert, 8 tokens): their scores; CTAs after those: a token's halves.
+// Order-preserving 64-bit integers of scores, 0 for what is no number.
+__device__ __forceinline__ uint64_t score_key(double v) {
+  if (!(v == v)) return 0;
+  const int64_t b = __double_as_longlong(v);
+  return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;
+}
+
+// Scores of expert e for tokens t0 .. t0 + n - 1 (n <= N), by a CTA.
 //
 // The order of near scores decides which expert runs, so they are summed as if
 // in 48 bits: BF16 products are exact in FP32 (with FP32 weights the product's
 // rounding error is added too), and every sum keeps its rounding error.
+template <class R, int N>
+__device__ __forceinline__ void moe_score(const MoeArgs& p, int e, int t0, int n) {
+  constexpr int kDeep = N == 1 ? 4 : 1;  // steps whose loads are in flight at once
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const R* w = reinterpret_cast<const R*>(p.router) + (int64_t)e * p.d;
+  const __nv_bfloat16* x = p.x + (int64_t)t0 * p.ldx;
+  float hi[N] = {}, lo[N] = {};
+  for (int c0 = tid * 8; c0 < p.d; c0 += kDeep * kScoreThreads * 8) {
+    float wf[kDeep][8];
+    uint4 xw[kDeep][N];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) {
+      const int c = c0 + k * kScoreThreads * 8;
+      if (c < p.d) {
+        load8(w + c, wf[k]);
+#pragma unroll
+        for (int t = 0; t < N; ++t)  // (tokens past the last: the last again, unused)
+          xw[k][t] = __ldg(reinterpret_cast<const uint4*>(x + (int64_t)min(t, n - 1) * p.ldx + c));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wf[k][i] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < N; ++t) xw[k][t] = make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k)
+#pragma unroll
+      for (int t = 0; t < N; ++t) {
+        const uint32_t xs[4] = {xw[k][t].x, xw[k][t].y, xw[k][t].z, xw[k][t].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float xf = i & 1 ? bf16_hi(xs[i / 2]) : bf16_lo(xs[i / 2]);
+          const float v = __fmul_rn(wf[k][i], xf);  // (not joined with the sum)
+          if constexpr (sizeof(R) == 4) lo[t] += fmaf(wf[k][i], xf, -v);
+          add_exactly(hi[t], lo[t], v);
+        }
+      }
+  }
+  // pairs (hi, lo) over the warp and the CTA: FP64 is slow here
+  __shared__ float2 sums[kScoreThreads / 32][N];
+#pragma unroll
+  for (int t = 0; t < N; ++t) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float h = __shfl_xor_sync(0xffffffffu, hi[t], o), l = __shfl_xor_sync(0xffffffffu, lo[t], o);
+      add_exactly(hi[t], lo[t], h);
+      lo[t] += l;
+    }
+    if (lane == 0) sums[warp][t] = make_float2(hi[t], lo[t]);
+  }
+  __syncthreads();
+  if (tid < n) {
+    double v = 0.0;
+    for (int i = 0; i < kScoreThreads / 32; ++i) {
+      const float2 f = sums[i][tid];
+      v += (double)f.x;
+      if (fabsf(f.y) < INFINITY) v += (double)f.y;  // where a sum overflowed its error is no number
+    }
+    v += 0.0;  // -0 and 0 are one score
+    const int64_t to = (int64_t)(t0 + tid) * p.experts + e;
+    const float h = (float)v;
+    p.logits[to] = make_float2(h, fabsf(h) < INFINITY ? (float)(v - (double)h) : 0.0f);
+    p.keys[to] = score_key(p.router_bias ? 1.0 / (1.0 + exp(-v)) + (double)__ldg(p.router_bias + e) : v);
+  }
+}
+
+// CTA (expert, 8 tokens): their scores; CTAs after those: a token's halves.
 template <class R>
 __global__ void __launch_bounds__(kScoreThreads) moe_scores_kernel(const MoeArgs p) {
   griddep_wait();
   griddep_launch_dependents();
   const int live = live_tokens(p);
   const int groups = (p.tokens + kScoreTokens - 1) / kScoreTokens;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   int at = blockIdx.x;
   // the second kernel's counters
   for (int i = blockIdx.x * kScoreThreads + tid; i < p.counters; i += gridDim.x * kScoreThreads) p.counter[i] = 0;
@@ -117,9 +206,9 @@ __global__ void __launch_bounds__(kScoreThreads) moe_scores_kernel(const MoeArgs
         __half2 h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(f[2 * i] * inv, f[2 * i + 1] * inv);
-        *reinterpret_cast<uint4*>(p.xh + (int64_t)at * p.d + (c & ~127) + stream_half_at(c & 127)) =
-            *reinterpret_cast<const uint4*>(h);
-        if ((c & 127) == 0) p.xs[(int64_t)at * (p.d / 128) + c / 128] = s;
+        uint8_t* to = p.xh + ((int64_t)at * (p.d / 128) + c / 128) * kMoeChunkBytes;
+        *reinterpret_cast<uint4*>(to + 2 * moe_half_at(c & 127)) = *reinterpret_cast<const uint4*>(h);
+        if ((c & 127) == 0) *reinterpret_cast<float*>(to + 256) = s;
       }
     }
     return;
@@ -127,93 +216,63 @@ __global__ void __launch_bounds__(kScoreThreads) moe_scores_kernel(const MoeArgs
   const int e = at % p.experts, t0 = at / p.experts * kScoreTokens;
   const int n = min(live - t0, kScoreTokens);
   if (n <= 0) return;
-  const R* w = reinterpret_cast<const R*>(p.router) + (int64_t)e * p.d;
-  const __nv_bfloat16* x = p.x + (int64_t)t0 * p.ldx;
-  float hi[kScoreTokens], lo[kScoreTokens];
-#pragma unroll
-  for (int t = 0; t < kScoreTokens; ++t) hi[t] = lo[t] = 0.0f;
-  for (int c = tid * 8; c < p.d; c += kScoreThreads * 8) {
-    float wf[8];
-    load8(w + c, wf);
-#pragma unroll
-    for (int t = 0; t < kScoreTokens; ++t) {
-      if (t < n) {
-        float xf[8];
-        load8(x + (int64_t)t * p.ldx + c, xf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = wf[i] * xf[i];
-          if constexpr (sizeof(R) == 4) lo[t] += fmaf(wf[i], xf[i], -v);
-          add_exactly(hi[t], lo[t], v);
-        }
-      }
-    }
-  }
-  __shared__ double sums[kScoreThreads / 32][kScoreTokens];
-#pragma unroll
-  for (int t = 0; t < kScoreTokens; ++t) {
-    if (t < n) {
-      double v = (double)hi[t] + (double)lo[t];
-      // where a sum overflowed its error is no number
-      if (!(fabsf(lo[t]) < INFINITY)) v = (double)hi[t];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) sums[warp][t] = v;
-    }
-  }
-  __syncthreads();
-  if (tid < n) {
-    double v = 0.0;
-    for (int i = 0; i < kScoreThreads / 32; ++i) v += sums[i][tid];
-    v += 0.0;  // -0 and 0 are one score
-    const int64_t to = (int64_t)(t0 + tid) * p.experts + e;
-    p.logits[to] = v;
-    if (p.router_bias) p.select[to] = 1.0 / (1.0 + exp(-v)) + (double)__ldg(p.router_bias + e);
-  }
+  if (n > 4) moe_score<R, 8>(p, e, t0, n);
+  else if (n > 1) moe_score<R, 4>(p, e, t0, n);
+  else moe_score<R, 1>(p, e, t0, n);
 }
 
-// ---------------------------------------------------------------- the layer
+// ---------------------------------------------------------------- routing
 
-struct MoeShared {
-  int32_t pair_token[kMoeMaxTokens * kMoeMaxTopK];  // pairs in the order of their experts: the token
-  int16_t pair_of[kMoeMaxTokens * kMoeMaxTopK];     // (token, j) -> its pair
-  int16_t chosen[kMoeMaxTokens * kMoeMaxTopK];      // (token, j) -> expert
-  float weight[kMoeMaxTokens * kMoeMaxTopK];        // (token, j)
-  int16_t hit_expert[kMoeMaxExperts];               // hit experts, ascending
-  int16_t hit_first[kMoeMaxExperts + 1];            // their first pairs
-  int32_t scan[kMoeWarps];
-  int32_t hits;
-  int32_t last;  // abort flag of the barrier
+constexpr int kMoePairs = kMoeMaxTokens * kMoeMaxTopK;
+
+// What a stage of the ring holds.
+struct alignas(16) MoeStage {
+  int16_t hit;    // hit expert, -1: no more
+  uint8_t begin;  // the unit's first stage of a team
+  uint8_t end;    // and its last
+  int32_t chunk;  // the first 128 columns; past the last: nothing
+  int32_t row;    // the unit's first row: column of h, or of y
+  int16_t first;  // the expert's first pair
+  uint8_t count;  // and their number
+  uint8_t part;   // which share of the hit experts (y only)
 };
 
-// Order-preserving 64-bit integers of scores, 0 for what is no number.
-__device__ __forceinline__ uint64_t score_key(double v) {
-  if (!(v == v)) return 0;
-  const int64_t b = __double_as_longlong(v);
-  return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;
-}
+struct MoeShared {
+  uint64_t mask[kMoeMaxExperts];          // of an expert: its tokens
+  int16_t chosen[kMoePairs];              // (token, j) -> expert
+  float weight[kMoePairs];                // (token, j)
+  uint8_t pair_token[kMoePairs];          // pairs in the order of (expert, token)
+  uint8_t pair_slot[kMoePairs];           // and their j
+  int16_t hit_expert[kMoeMaxExperts];     // hit experts, ascending
+  int16_t hit_first[kMoeMaxExperts + 1];  // their first pairs
+  int16_t first[kMoeMaxExperts];          // the same by expert
+  uint64_t full[kMoeStages], empty[kMoeStages];  // of the ring's slots
+  uint64_t summed[4], taken[4];                   // of the exchange's buffers
+  MoeStage stage[kMoeStages], unit[4];
+  int32_t scan[kMoeThreads / 32], most[kMoeThreads / 32];
+  int32_t hits, most_tokens;
+  int32_t abort;
+  int32_t last;
+};
 
-// A warp picks the experts of token t and their weights.
+// A warp picks the experts of token t and their weights, from 32 PER experts.
+template <int PER>
 __device__ void moe_pick(const MoeArgs& p, MoeShared& sh, int t, int lane) {
-  const double* logits = p.logits + (int64_t)t * p.experts;
-  const double* by = p.router_bias ? p.select + (int64_t)t * p.experts : logits;
-  constexpr int kPer = kMoeMaxExperts / 32;
-  uint64_t key[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = e < p.experts ? score_key(__ldg(by + e)) : 0;
-  }
+  const float2* logits = p.logits + (int64_t)t * p.experts;
+  uint64_t key[PER];
   uint32_t taken = 0;  // bit i: expert i * 32 + lane is chosen, or is none
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (i * 32 + lane >= p.experts) taken |= 1u << i;
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e < p.experts ? __ldg(reinterpret_cast<const unsigned long long*>(p.keys) + (int64_t)t * p.experts + e) : 0;
+    if (e >= p.experts) taken |= 1u << i;
+  }
   int mine = 0;  // lane j: the j-th choice
   for (int j = 0; j < p.top_k; ++j) {
     uint64_t best = 0;
     int at = 0x7fffffff;
 #pragma unroll
-    for (int i = kPer - 1; i >= 0; --i)  // among equals the lowest stays
+    for (int i = PER - 1; i >= 0; --i)  // among equals the lowest stays
       if (!(taken >> i & 1u) && (key[i] >= best || at == 0x7fffffff)) {
         best = key[i];
         at = i * 32 + lane;
@@ -229,25 +288,25 @@ __device__ void moe_pick(const MoeArgs& p, MoeShared& sh, int t, int lane) {
   }
   // weights: softmax over the chosen (renormalised) or over all, or the logistic function
   const bool on = lane < p.top_k;
-  const double l = on ? __ldg(logits + mine) : -INFINITY;
+  const float2 l = on ? __ldg(logits + mine) : make_float2(0.0f, 0.0f);
   float w;
   if (p.score == DG_SCORE_SOFTMAX) {
-    double m = l;
-    if (!p.renormalize)
-      for (int e = lane; e < p.experts; e += 32) m = fmax(m, __ldg(logits + e));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    w = on ? expf((float)(l - m)) : 0.0f;
+    // the first choice has the largest
+    const float mh = __shfl_sync(0xffffffffu, l.x, 0), ml = __shfl_sync(0xffffffffu, l.y, 0);
+    w = on ? expf((l.x - mh) + (l.y - ml)) : 0.0f;
     float sum = w;
     if (!p.renormalize) {
       sum = 0.0f;
-      for (int e = lane; e < p.experts; e += 32) sum += expf((float)(__ldg(logits + e) - m));
+      for (int e = lane; e < p.experts; e += 32) {
+        const float2 o = __ldg(logits + e);
+        sum += expf((o.x - mh) + (o.y - ml));
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     w /= sum;
   } else {
-    w = on ? 1.0f / (1.0f + expf((float)-l)) : 0.0f;
+    w = on ? 1.0f / (1.0f + expf(-l.x)) : 0.0f;
     if (p.renormalize) {
       float sum = w;
 #pragma unroll
@@ -258,6 +317,7 @@ __device__ void moe_pick(const MoeArgs& p, MoeShared& sh, int t, int lane) {
   w *= p.scale;
   if (on) {
     sh.chosen[t * p.top_k + lane] = (int16_t)mine;
+    atomicOr(reinterpret_cast<unsigned long long*>(&sh.mask[mine]), 1ull << t);
     sh.weight[t * p.top_k + lane] = w;
     if (blockIdx.x == 0) {
       p.chosen_out[(int64_t)t * p.top_k + lane] = mine;
@@ -266,143 +326,242 @@ __device__ void moe_pick(const MoeArgs& p, MoeShared& sh, int t, int lane) {
   }
 }
 
-// Pairs (token, j) in the order of (expert, token).
-__device__ void moe_sort(const MoeArgs& p, MoeShared& sh, int live) {
+// The choices of all live tokens, then the pairs (token, j) in the order of
+// (expert, token).
+__device__ __forceinline__ void moe_route(const MoeArgs& p, MoeShared& sh, int live) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int pairs = live * p.top_k;
-  int count = 0;
-  if (tid < p.experts)
-    for (int i = 0; i < pairs; ++i) count += sh.chosen[i] == tid;
+  for (int i = tid; i < p.experts; i += kMoeThreads) sh.mask[i] = 0;
+  __syncthreads();
+  for (int t = warp; t < live; t += kMoeThreads / 32) {
+    if (p.experts <= 64) moe_pick<2>(p, sh, t, lane);
+    else if (p.experts <= 256) moe_pick<8>(p, sh, t, lane);
+    else moe_pick<kMoeMaxExperts / 32>(p, sh, t, lane);
+  }
+  if (blockIdx.x == 0)  // rows past the last token: no expert
+    for (int i = pairs + tid; i < p.tokens * p.top_k; i += kMoeThreads) {
+      p.chosen_out[i] = -1;
+      p.weight_out[i] = 0.0f;
+    }
+  __syncthreads();
   // prefix sums over the experts of (pairs, hit experts) in one word
+  const int count = tid < p.experts ? __popcll(sh.mask[tid]) : 0;
   int v = count | (count > 0 ? 1 << 16 : 0);
-  const int own = v;
+  const int own = v, most = __reduce_max_sync(0xffffffffu, count);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
-  if (lane == 31) sh.scan[warp] = v;
+  if (lane == 31) {
+    sh.scan[warp] = v;
+    sh.most[warp] = most;
+  }
   __syncthreads();
-  int before = v - own;
-  for (int i = 0; i < warp; ++i) before += sh.scan[i];
-  if (count > 0) {
-    const int hit = before >> 16;
-    int at = before & 0xffff;
-    sh.hit_expert[hit] = (int16_t)tid;
-    sh.hit_first[hit] = (int16_t)at;
-    for (int i = 0; i < pairs; ++i)
-      if (sh.chosen[i] == tid) {
-        sh.pair_token[at] = i / p.top_k;
-        sh.pair_of[i] = (int16_t)at++;
-      }
+  if (tid < p.experts) {
+    int before = v - own;
+    for (int i = 0; i < warp; ++i) before += sh.scan[i];
+    sh.first[tid] = (int16_t)(before & 0xffff);
+    if (count > 0) {
+      sh.hit_expert[before >> 16] = (int16_t)tid;
+      sh.hit_first[before >> 16] = (int16_t)(before & 0xffff);
+    }
   }
   if (tid == kMoeThreads - 1) {
-    sh.hits = (before + own) >> 16;
-    sh.hit_first[(before + own) >> 16] = (int16_t)pairs;
+    int all = 0, m = 0;
+    for (int i = 0; i < kMoeThreads / 32; ++i) {
+      all += sh.scan[i];
+      m = max(m, sh.most[i]);
+    }
+    sh.hits = all >> 16;
+    sh.hit_first[all >> 16] = (int16_t)pairs;
+    sh.most_tokens = m;
+  }
+  __syncthreads();
+  for (int i = tid; i < pairs; i += kMoeThreads) {
+    const int e = sh.chosen[i], t = i / p.top_k;
+    const int at = sh.first[e] + __popcll(sh.mask[e] & ((1ull << t) - 1));
+    sh.pair_token[at] = (uint8_t)t;
+    sh.pair_slot[at] = (uint8_t)(i - t * p.top_k);
   }
   __syncthreads();
 }
 
-// One stage of a warp's stream into its ring: rows row0 + 0..7 and row1 + 0..7
-// of a matrix of cols columns, 128 columns at 128 chunk, and their scale words.
-struct Rows {
-  const uint8_t* a;    // the lane's first byte of row0 + r
-  const uint8_t* b;    // and of row1 + r
-  const uint32_t* sf;  // lanes 0..15: the row's first scale word
-  int sf_ld;
-  __device__ __forceinline__ void set(const uint8_t* w, const uint32_t* words, int rows, int cols, int row0, int row1,
-                                      int lane) {
-    const int r = lane >> 2, q = lane & 3;
-    a = w + (int64_t)(row0 + r) * cols + q * 16;
-    b = w + (int64_t)(row1 + r) * cols + q * 16;
-    sf = words + (lane < 8 ? row0 + lane : row1 + (lane & 7));
-    sf_ld = (rows + 3) / 4 * 4;
+// ---------------------------------------------------------------- the layer
+
+// How the stages of one of the two products lie: 2^LG tiles of 16 rows by
+// 16 / 2^LG slices of 128 columns, a warp each ([slice][row][128 bytes], of Wg and
+// Wu one after the other); then the rows' scale words; then the tokens.  More rows share a token's bytes, fewer make finer units: with 8
+// tokens of one expert at least three stages of 32 rows fit, with 64 two of 128.
+constexpr int up_lg(int max) { return max == 1 ? 1 : max <= 4 ? 2 : 3; }
+constexpr int down_lg(int max) { return max == 1 ? 0 : max <= 4 ? 2 : 3; }
+template <int LG>
+struct MoeShape {
+  static constexpr int lg = LG, slices = kMoeWarps >> LG;
+  static constexpr int kBytes = slices * kMoeChunkBytes;
+  // a token's place: its chunks, and up to 64 past a multiple of 128 (no bank conflicts)
+  static constexpr int token_bytes = kBytes + ((64 - kBytes) & 127);
+  static __device__ __forceinline__ int stage_bytes(int most_tokens) {
+    return (32768 + 512 + most_tokens * token_bytes + 1023) & ~1023;
   }
-  __device__ __forceinline__ void copy(uint32_t to, int chunk, int lane) const {
-    const int64_t at = (int64_t)chunk * kStreamCols;
-    cp_async16(to + lane * 16, a + at);
-    cp_async16(to + 512 + lane * 16, b + at);
-    cp_async16(to + 1024 + lane * 16, a + at + 64);
-    cp_async16(to + 1536 + lane * 16, b + at + 64);
-    if (lane < 16)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 2048 + lane * 4),
-                   "l"(sf + (int64_t)(chunk >> 2) * sf_ld)
-                   : "memory");
+};
+// Teams of warps that take the stages by turns, a warp of two 16 rows and 256
+// columns of each of its team's: fewer waits a byte than with all 16 warps on
+// every stage (16 rows, 128 columns), and twice the independent products.  Each
+// has its own slots (one whose team changed could be waited for a use too
+// early), so the ring's are even: for many tokens, where three fit, one team.
+constexpr int moe_teams(int max) { return max <= 2 ? 2 : 1; }
+// Buffers of the exchange, and how the finishing warps share the work: units by
+// turns where a unit is small, else each unit.
+constexpr bool moe_turns(int max) { return max <= 2; }
+constexpr int moe_buffers(int max) { return max == 1 ? 4 : max == 2 ? 3 : 1; }
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// The producer warp's side of a stage.
+template <bool UP, class Shape>
+struct MoeFetch {
+  static constexpr int lg = Shape::lg, slices = Shape::slices;
+  const MoeArgs& p;
+  const MoeShared& sh;
+  const CUtensorMap* map;
+  int lane;
+  // columns / 128 of the stage, and scale words
+  __device__ __forceinline__ int slices_of(const MoeStage& st) const {
+    return max(0, min(slices, (UP ? p.d : p.f) / 128 - st.chunk));
+  }
+  __device__ __forceinline__ int words_of(const MoeStage& st, int n) const { return ((st.chunk & 3) + n + 3) / 4; }
+  __device__ __forceinline__ uint32_t bytes(const MoeStage& st) const {
+    const int n = slices_of(st);
+    return n ? (uint32_t)(32768 + (words_of(st, n) << lg) * 64 + st.count * n * kMoeChunkBytes) : 0;
+  }
+  // 32 KB (slices past the last column come as zeros) and scale words
+  __device__ __forceinline__ void weights(uint32_t to, uint32_t bar, const MoeStage& st) const {
+    const int n = slices_of(st), cols = UP ? p.d : p.f, rows = UP ? 2 * p.f : p.d, e = sh.hit_expert[st.hit];
+    if (n == 0) return;
+    if (lane < (UP ? 2 : 1)) tma_load_3d(to + lane * 16384, map, bar, 0, e * rows + st.row + lane * p.f, st.chunk);
+    constexpr int run = (UP ? 8 : 16) << lg;
+    if (lane < (UP ? 2 : 1) * words_of(st, n)) {
+      const int w = UP ? lane >> 1 : lane;
+      const uint32_t* src = (UP ? p.up_sf : p.down_sf) +
+                            ((int64_t)e * ((cols + 511) / 512) + (st.chunk >> 2) + w) * rows + st.row +
+                            (UP && (lane & 1) ? p.f : 0);
+      bulk_load(to + 32768 + lane * run * 4, src, (uint32_t)run * 4, bar);
+    }
+  }
+  __device__ __forceinline__ void tokens(uint32_t to, uint32_t bar, const MoeStage& st) const {
+    const int n = slices_of(st), chunks = (UP ? p.d : p.f) / 128;
+    if (n == 0) return;
+    for (int t = lane; t < st.count; t += 32) {
+      const int at = UP ? sh.pair_token[st.first + t] : st.first + t;
+      bulk_load(to + 32768 + 512 + t * Shape::token_bytes,
+                (UP ? p.xh : p.hh) + ((int64_t)at * chunks + st.chunk) * kMoeChunkBytes, (uint32_t)n * kMoeChunkBytes, bar);
+    }
   }
 };
 
-// The tokens of a product: halves [row][cols] and their scales [row][cols / 128].
-struct Tokens {
-  const __half* h;
-  const float* s;
-  const int32_t* row;  // of token n (shared memory), or NULL: first + n
-  int first, count, cols;
-  __device__ __forceinline__ int at(int n) const { return row ? row[n] : first + n; }
-};
-
-// acc += a stage's 16 x 128 codes times the tokens' 128 columns.
-template <int NB>
-__device__ __forceinline__ void moe_stage(const uint8_t* stage, int chunk, const Tokens& t, int lane,
-                                          float (&acc)[NB][4]) {
+// acc += a warp's 16 rows x 128 PER columns (slices from `slice` on) of a stage
+// times its expert's tokens.
+template <bool UP, class Shape, int PER, int MAX>
+__device__ __forceinline__ void moe_multiply(const uint8_t* stage, int tile, int slice, int first_chunk, int chunks,
+                                             int count, int lane, float (&acc)[MAX][4]) {
+  constexpr int lg = Shape::lg;
   const int r = lane >> 2, q = lane & 3;
-  uint32_t a[8][4];
-  stream_decode<DecodeE4m3>(stage, lane, a);
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(stage + 2048);
-  const int shift = (chunk & 3) * 8;
-  const float s0 = scale_of_byte(words[r] >> shift & 0xFFu), s1 = scale_of_byte(words[8 + r] >> shift & 0xFFu);
+  // atoms of rows r and r + 8, in TMA's 128-byte swizzle: 16 bytes c of row r at c ^ r
+  const uint8_t* low = stage + slice * (UP ? 1024 << lg : 2048 << lg) + tile * (UP ? 1024 : 2048) + r * 128;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(stage + 32768) + (UP ? tile * 8 + r : tile * 16 + r);
+  // (columns of tokens that do not exist hold the last token's: nothing reads their sums)
+  const uint8_t* tokens = stage + 32768 + 512 + slice * kMoeChunkBytes;
+  const uint8_t* x = tokens + min(r, count - 1) * Shape::token_bytes + q * 16;
+  const uint8_t* x0 = tokens + min(2 * q, count - 1) * Shape::token_bytes + 256;
+  const uint8_t* x1 = tokens + min(2 * q + 1, count - 1) * Shape::token_bytes + 256;
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    uint4 b[4] = {};
-    const int n = nb * 8 + r;
-    if (n < t.count) {
-      const uint4* src = reinterpret_cast<const uint4*>(t.h + (int64_t)t.at(n) * t.cols + chunk * kStreamCols) + q;
+  for (int i = 0; i < PER; ++i) {
+    const int chunk = first_chunk + slice + i;
+    if (i && chunk >= chunks) break;
+    const uint8_t* lo = low + i * (UP ? 1024 << lg : 2048 << lg);
+    const uint8_t* hi = lo + (UP ? 16384 : 1024);
+    const uint32_t* word = words + ((chunk >> 2) - (first_chunk >> 2)) * (16 << lg);
+    const int shift = (chunk & 3) * 8;
+    const float s0 = scale_of_byte(word[0] >> shift & 0xFFu);
+    const float s1 = scale_of_byte(word[UP ? 8 << lg : 8] >> shift & 0xFFu);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = src[i * 4];
+    for (int h = 0; h < 2; ++h) {
+      uint32_t a[4][4];
+      const int c = ((2 * q + h) ^ r) * 16;
+      const uint4 g = *reinterpret_cast<const uint4*>(lo + c), u = *reinterpret_cast<const uint4*>(hi + c);
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        DecodeE4m3::four(gw[j], a[j][0], a[j][2]);
+        DecodeE4m3::four(uw[j], a[j][1], a[j][3]);
+      }
+#pragma unroll
+      for (int nb = 0; nb < MAX; ++nb) {
+        if (nb && nb * 8 >= count) break;
+        const uint8_t* xb = (nb ? tokens + min(nb * 8 + r, count - 1) * Shape::token_bytes + q * 16 : x) +
+                            i * kMoeChunkBytes + h * 128;
+        const uint4 b0 = *reinterpret_cast<const uint4*>(xb), b1 = *reinterpret_cast<const uint4*>(xb + 64);
+        const int m = nb * 8 + 2 * q;
+        const float t0 = *reinterpret_cast<const float*>(
+            (nb ? tokens + min(m, count - 1) * Shape::token_bytes + 256 : x0) + i * kMoeChunkBytes);
+        const float t1 = *reinterpret_cast<const float*>(
+            (nb ? tokens + min(m + 1, count - 1) * Shape::token_bytes + 256 : x1) + i * kMoeChunkBytes);
+        float d[4] = {};
+        mma_f16(d, a[0], b0.x, b0.y);
+        mma_f16(d, a[1], b0.z, b0.w);
+        mma_f16(d, a[2], b1.x, b1.y);
+        mma_f16(d, a[3], b1.z, b1.w);
+        acc[nb][0] = fmaf(d[0], s0 * t0, acc[nb][0]);
+        acc[nb][1] = fmaf(d[1], s0 * t1, acc[nb][1]);
+        acc[nb][2] = fmaf(d[2], s1 * t0, acc[nb][2]);
+        acc[nb][3] = fmaf(d[3], s1 * t1, acc[nb][3]);
+      }
     }
-    float d[4] = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      mma_f16(d, a[2 * i], b[i].x, b[i].y);
-      mma_f16(d, a[2 * i + 1], b[i].z, b[i].w);
-    }
-    const int m = nb * 8 + 2 * q;
-    const int chunks = t.cols / kStreamCols;
-    const float x0 = m < t.count ? t.s[t.at(m) * chunks + chunk] : 0.0f;
-    const float x1 = m + 1 < t.count ? t.s[t.at(m + 1) * chunks + chunk] : 0.0f;
-    acc[nb][0] = fmaf(d[0], s0 * x0, acc[nb][0]);
-    acc[nb][1] = fmaf(d[1], s0 * x1, acc[nb][1]);
-    acc[nb][2] = fmaf(d[2], s1 * x0, acc[nb][2]);
-    acc[nb][3] = fmaf(d[3], s1 * x1, acc[nb][3]);
   }
 }
 
-__device__ __forceinline__ void group_barrier(int id, int threads) {
+__device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// h of an octet of columns for a hit expert's tokens, from the sums of g (acc 0,
-// 1) and u (2, 3); the last of 16 octets brings their 128 columns into halves.
-template <int NB>
-__device__ __forceinline__ void moe_finish_up(const MoeArgs& p, int hit, int octet, int first, int count,
-                                              const float (&acc)[NB][4], int lane) {
+__device__ __forceinline__ void add4(float4& v, const float4& o) {
+  v.x += o.x;
+  v.y += o.y;
+  v.z += o.z;
+  v.w += o.w;
+}
+
+// h of an octet of columns for a hit expert's tokens, from the slices' sums of g
+// (x, y) and u (z, w), added in the slices' order.
+template <class Shape>
+__device__ __forceinline__ void moe_activate(const MoeArgs& p, const float4* sums, int blocks, int octet, int first,
+                                             int count, int lane) {
   const int r = lane >> 2, q = lane & 3;
+  for (int nb = 0; nb * 8 < count; ++nb) {
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int n = nb * 8 + 2 * q + i;
-      const float g = acc[nb][i], u = acc[nb][2 + i];
-      const float h = (p.activation == DG_ACT_SILU ? gate_act<DG_ACT_SILU>(g) : gate_act<DG_ACT_GELU_TANH>(g)) * u;
-      if (n < count) p.h[(int64_t)(first + n) * p.f + octet * 8 + r] = h;
+    for (int i = 0; i < Shape::slices; ++i) {
+      add4(v, sums[(i * blocks + nb) * 32]);
     }
-  __threadfence();
-  __syncwarp();
-  const int block = octet >> 4, blocks = p.f / 128;
-  int old = 0;
-  if (lane == 0) old = (int)atomicAdd(p.counter + kMoeBarrierWords + hit * blocks + block, 1u);
-  old = __shfl_sync(0xffffffffu, old, 0);
-  if (old != 15) return;
-  __threadfence();
+    const float2 g = make_float2(v.x, v.y), u = make_float2(v.z, v.w);
+    const float2 a = p.activation == DG_ACT_SILU
+                         ? make_float2(gate_act<DG_ACT_SILU>(g.x), gate_act<DG_ACT_SILU>(g.y))
+                         : make_float2(gate_act<DG_ACT_GELU_TANH>(g.x), gate_act<DG_ACT_GELU_TANH>(g.y));
+    const int n = nb * 8 + 2 * q;
+    float* h = p.h + (int64_t)(first + n) * p.f + octet * 8 + r;
+    if (n < count) __stcg(h, a.x * u.x);
+    if (n + 1 < count) __stcg(h + p.f, a.y * u.y);
+  }
+}
+
+// The 128 columns of h of a block, for a hit expert's tokens, as halves.
+__device__ __forceinline__ void moe_halves(const MoeArgs& p, int block, int first, int count, int lane) {
+  const int blocks = p.f / 128;
   for (int n = 0; n < count; ++n) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(p.h + (int64_t)(first + n) * p.f + block * 128) + lane);
     float m = fmaxf(fmaxf(finite_magnitude(v.x), finite_magnitude(v.y)), fmaxf(finite_magnitude(v.z), finite_magnitude(v.w)));
@@ -414,245 +573,467 @@ __device__ __forceinline__ void moe_finish_up(const MoeArgs& p, int hit, int oct
     uint2 w;
     w.x = *reinterpret_cast<const uint32_t*>(&a);
     w.y = *reinterpret_cast<const uint32_t*>(&b);
-    *reinterpret_cast<uint2*>(p.hh + (int64_t)(first + n) * p.f + block * 128 + stream_half_at(lane * 4)) = w;
-    if (lane == 0) p.hs[(int64_t)(first + n) * blocks + block] = s;
+    uint8_t* to = p.hh + ((int64_t)(first + n) * blocks + block) * kMoeChunkBytes;
+    *reinterpret_cast<uint2*>(to + 2 * moe_half_at(lane * 4)) = w;
+    if (lane == 0) *reinterpret_cast<float*>(to + 256) = s;
   }
 }
 
-struct Work {
-  const MoeArgs* p;
-  MoeShared* sh;
-  uint8_t* ring;     // the warp's
-  float* exchange;   // kMoeSlots x 16
-  int warp, lane;
+// Four results of y: their sums over the experts, and c.
+__device__ __forceinline__ void moe_store(const MoeArgs& p, int t, int64_t col, float4 v) {
+  const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float c = p.c ? __bfloat162float(p.c[(int64_t)t * p.ldc + col + i]) : 0.0f;
+    p.y[(int64_t)t * p.ldy + col + i] = __float2bfloat16_rn(f[i] + c);
+  }
+}
+
+// The stages of a CTA's units, one after another.  Units come from a counter;
+// the next one's number is asked for a unit ahead.  UP: (hit expert, rows), else
+// (rows, share of the hit experts).
+template <bool UP, int TEAMS>
+struct MoeWalk {
+  const MoeArgs& p;
+  int hits, units, parts, rows, slices, chunks;
+  uint32_t* claim;
+  int lane;
+  const MoeShared& sh;
+  int u, claimed, hit, hit_end, chunk, row, part, count, stages;
+  __device__ __forceinline__ void aim() {
+    if (u >= units) return;
+    claimed = 0;
+    if (lane == 0) claimed = (int)atomicAdd(claim, 1u);
+    chunk = count = 0;
+    if (UP) {
+      const int per = p.f / rows;
+      hit = u / per;
+      hit_end = hit + 1;
+      row = (u - hit * per) * rows;
+      part = 0;
+    } else {
+      const int tile = u / parts;
+      part = u - tile * parts;
+      hit = hits * part / parts;
+      hit_end = hits * (part + 1) / parts;
+      row = tile * rows;
+    }
+    // a multiple of the teams, so that each sees the unit's end
+    stages = ((hit_end - hit) * ((chunks + slices - 1) / slices) + TEAMS - 1) / TEAMS * TEAMS;
+  }
+  __device__ __forceinline__ void begin() {
+    u = blockIdx.x;
+    aim();
+  }
+  __device__ __forceinline__ bool done() const { return u >= units; }
+  __device__ __forceinline__ bool empty() const { return hit == hit_end; }
+  __device__ __forceinline__ MoeStage stage() const {
+    const int h = empty() ? hit - 1 : hit, first = sh.hit_first[h];
+    return MoeStage{(int16_t)h, count < TEAMS, count + TEAMS >= stages, empty() ? chunks : chunk, row, (int16_t)first,
+                    (uint8_t)(sh.hit_first[h + 1] - first), (uint8_t)part};
+  }
+  __device__ __forceinline__ void next() {
+    if (++count == stages) {
+      u = gridDim.x + __shfl_sync(0xffffffffu, claimed, 0);
+      aim();
+      return;
+    }
+    chunk += slices;
+    if (chunk >= chunks) {
+      chunk = 0;
+      ++hit;
+    }
+  }
 };
 
-// One unit of the first products: the sums of the warp's chunks, joined over the
-// group's warps, and the group's first warp finishes them.
-template <int NB, class Next>
-__device__ __forceinline__ void moe_up_unit(const Work& w, int hit, int octet, int c0, int c1, int& stage, Next next) {
-  const MoeArgs& p = *w.p;
-  const int first = w.sh->hit_first[hit], count = w.sh->hit_first[hit + 1] - first;
-  const Tokens t{p.xh, p.xs, w.sh->pair_token + first, 0, count, p.d};
-  float acc[NB][4] = {};
-  for (int c = c0; c < c1; ++c) {
-    next();
-    cp_async_wait<kMoeRing - 1>();
-    __syncwarp();
-    moe_stage<NB>(w.ring + stage * kStreamStageBytes, c, t, w.lane, acc);
-    __syncwarp();
-    stage = stage + 1 == kMoeRing ? 0 : stage + 1;
-  }
-  const int group = w.warp / kMoeSplit, rank = w.warp % kMoeSplit;
-  float4* x = reinterpret_cast<float4*>(w.exchange) + (group * kMoeSplit * 8) * 32 + w.lane;
-  if (rank)
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) x[(rank * 8 + nb) * 32] = make_float4(acc[nb][0], acc[nb][1], acc[nb][2], acc[nb][3]);
-  group_barrier(1 + group, 32 * kMoeSplit);
-  if (rank == 0) {
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-      for (int i = 1; i < kMoeSplit; ++i) {
-        const float4 v = x[(i * 8 + nb) * 32];
-        acc[nb][0] += v.x;
-        acc[nb][1] += v.y;
-        acc[nb][2] += v.z;
-        acc[nb][3] += v.w;
-      }
-  }
-  group_barrier(1 + group, 32 * kMoeSplit);  // read before it is written again
-  if (rank == 0) moe_finish_up<NB>(p, hit, octet, first, count, acc, w.lane);
-}
-
-// One item of the second product: 16 rows of Wd of a hit expert, the warp's
-// chunks, into the slots (part, pair).
-template <int NB, class Next>
-__device__ __forceinline__ void moe_down_item(const Work& w, int hit, int part, int c0, int c1, int& stage, Next next) {
-  const MoeArgs& p = *w.p;
-  const int first = w.sh->hit_first[hit], count = w.sh->hit_first[hit + 1] - first;
-  const Tokens t{p.hh, p.hs, nullptr, first, count, p.f};
-  float acc[NB][4] = {};
-  for (int c = c0; c < c1; ++c) {
-    next();
-    cp_async_wait<kMoeRing - 1>();
-    __syncwarp();
-    moe_stage<NB>(w.ring + stage * kStreamStageBytes, c, t, w.lane, acc);
-    __syncwarp();
-    stage = stage + 1 == kMoeRing ? 0 : stage + 1;
-  }
-  const int r = w.lane >> 2, q = w.lane & 3;
-  const int pairs = w.sh->hit_first[w.sh->hits];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int n = nb * 8 + 2 * q + i;
-      if (n < count) {
-        float* slot = w.exchange + (part * pairs + first + n) * 16;
-        slot[r] = acc[nb][i];
-        slot[8 + r] = acc[nb][2 + i];
-      }
-    }
-}
-
-#define MOE_BY_COUNT(count, call) \
-  do {                            \
-    if ((count) <= 8) call(1);    \
-    else if ((count) <= 16) call(2); \
-    else if ((count) <= 32) call(4); \
-    else call(8);                 \
-  } while (0)
-
-__global__ void __launch_bounds__(kMoeThreads, 1) moe_layer_kernel(const MoeArgs p) {
-  extern __shared__ uint8_t smem[];
+// MAX: blocks of 8 tokens an expert can have.
+template <int MAX>
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    moe_layer_kernel(const __grid_constant__ MoeArgs p, const __grid_constant__ CUtensorMap map_up,
+                     const __grid_constant__ CUtensorMap map_down) {
+  using Up = MoeShape<up_lg(MAX)>;
+  using Down = MoeShape<down_lg(MAX)>;
+  // a finishing warp waits for its next unit, kMoeFinishers later: that buffer's last use must be one it has seen end
+  static_assert(!moe_turns(MAX) || moe_buffers(MAX) >= kMoeFinishers, "a wait could pass a phase early");
+  constexpr int kTeams = moe_teams(MAX);
+  constexpr int kBuffers = moe_buffers(MAX), kUpRows = 8 << Up::lg, kDownRows = 16 << Down::lg;
+  extern __shared__ uint8_t smem_raw[];
   __shared__ MoeShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Work w{&p, &sh, smem + kMoeSlots * 64 + warp * (kMoeRing * kStreamStageBytes), reinterpret_cast<float*>(smem), warp, lane};
-  const uint32_t ring = smem_u32(w.ring);
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (base - smem_u32(smem_raw));
+  if (tid == 0) {
+    for (int i = 0; i < kMoeStages; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), kMoeWarps / moe_teams(MAX));
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&sh.summed[i]), kMoeWarps);
+      mbar_init(smem_u32(&sh.taken[i]), moe_turns(MAX) ? 1 : kMoeFinishers);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&map_up);
+    tma_prefetch_desc(&map_down);
+  }
   griddep_wait();
   const int live = live_tokens(p);
-  for (int t = warp; t < live; t += kMoeWarps) moe_pick(p, sh, t, lane);
-  if (blockIdx.x == 0)  // rows past the last token: no expert
-    for (int i = live * p.top_k + tid; i < p.tokens * p.top_k; i += kMoeThreads) {
-      p.chosen_out[i] = -1;
-      p.weight_out[i] = 0.0f;
-    }
-  if (tid == 0) sh.last = 0;
-  __syncthreads();
-  moe_sort(p, sh, live);
-  const int hits = sh.hits;
-  const int pairs = live * p.top_k;
+  moe_route(p, sh, live);
+  const int hits = sh.hits, most = sh.most_tokens, blocks = (most + 7) / 8;
+  volatile int* const abort_flag = &sh.abort;
 
-  int put = 0, stage = 0;  // ring slots to fill and to read
-  auto slot = [&]() {
-    const uint32_t to = ring + put * kStreamStageBytes;
-    put = put + 1 == kMoeRing ? 0 : put + 1;
-    return to;
+  // The exchange lies after the ring: sums of g and u ([tile][slice][8 tokens][lane]), then of y ([warp][token][16 rows]).
+  const int up_buffer = kMoeWarps * blocks * 128, down_buffer = kMoeWarps * live * 16;
+  const int exchange_bytes = kBuffers * 4 * max(up_buffer, down_buffer);
+  float* const exchange = reinterpret_cast<float*>(smem + kMoeSmem - exchange_bytes);
+  const int up_bytes = Up::stage_bytes(most), down_bytes = Down::stage_bytes(most);
+  const int up_stages = min((kMoeSmem - exchange_bytes) / up_bytes, kMoeStages) / kTeams * kTeams;
+  const int down_stages = min((kMoeSmem - exchange_bytes) / down_bytes, kMoeStages) / kTeams * kTeams;
+  const int tiles = p.d / kDownRows, up_chunks = p.d / 128, down_chunks = p.f / 128;
+  // Shares of the hit experts, each a unit of its own: a dozen units an SM, of four stages at least.
+  int parts = 1;
+  while (2 * parts <= hits && parts < kMoeMaxParts && tiles * parts < 12 * (int)gridDim.x &&
+         (int64_t)kDownRows * p.f * (hits / (2 * parts)) >= 4 * 32768)
+    parts *= 2;
+
+  uint32_t used = 0;  // bit s: parity of ring slot s's uses
+  if (warp == kMoeWarps) {
+    // ------------------------------------------------------------ fetch
+    int s = 0;
+    uint32_t armed = 0;  // bit s: slot s was filled
+    bool ok = true;
+    auto wait_free = [&]() {
+      return wait_bounded(smem_u32(&sh.empty[s]), (used >> s & 1u) ^ 1u, abort_flag, p.timeout_ns, p.err,
+                          kSiteProducerEmpty);
+    };
+    // says what slot s will hold, and how many bytes that is
+    auto arm = [&](const MoeStage& what, uint32_t bytes) {
+      if (lane == 0) {
+        sh.stage[s] = what;
+        mbar_arrive_expect_tx(smem_u32(&sh.full[s]), bytes);
+      }
+      __syncwarp();
+      used ^= 1u << s;
+      armed |= 1u << s;
+    };
+    const MoeStage none{-1, 0, 0, 0, 0, 0, 0, 0};
+    {
+      const MoeFetch<true, Up> fetch{p, sh, &map_up, lane};
+      MoeWalk<true, kTeams> walk{p, hits, hits * (p.f / kUpRows), 1, kUpRows, Up::slices, up_chunks, p.counter + 2, lane, sh};
+      int told = 0;
+      for (walk.begin(); ok; s = s + 1 == up_stages ? 0 : s + 1) {
+        if (!(ok = wait_free())) break;
+        if (walk.done()) {
+          arm(none, 0);  // to each team
+          if (++told == kTeams) break;
+          continue;
+        }
+        const MoeStage st = walk.stage();
+        arm(st, fetch.bytes(st));
+        fetch.weights(base + s * up_bytes, smem_u32(&sh.full[s]), st);
+        fetch.tokens(base + s * up_bytes, smem_u32(&sh.full[s]), st);
+        walk.next();
+      }
+    }
+    // the second product's stages lie elsewhere in the ring: all of the first's are read before
+    for (s = 0; s < up_stages && ok; ++s) ok = wait_free();
+    s = 0;
+    {
+      const MoeFetch<false, Down> fetch{p, sh, &map_down, lane};
+      MoeWalk<false, kTeams> walk{p, hits, hits ? tiles * parts : 0, parts, kDownRows, Down::slices, down_chunks, p.counter + 3, lane, sh};
+      walk.begin();
+      // Wd does not wait for h
+      int first = 0;
+      for (; ok && first < down_stages && !walk.done(); ++first) {
+        const MoeStage st = walk.stage();
+        s = first;
+        arm(st, fetch.bytes(st));
+        fetch.weights(base + s * down_bytes, smem_u32(&sh.full[s]), st);
+        walk.next();
+      }
+      // barrier over the grid: all of h is there.  All CTAs run at once (cooperative launch).
+      if (lane == 0 && ok) {
+        const uint64_t t0 = global_timer_ns();
+        for (uint32_t it = 1; ld_acquire_gpu(p.counter) < gridDim.x; ++it)
+          if ((it & 63u) == 0 && (*abort_flag || global_timer_ns() - t0 > p.timeout_ns || it >= (1u << 28))) {
+            record_error(p.err, DG_ERR_DEVICE_TIMEOUT, kSiteMoeBarrier);
+            sh.abort = 1;
+            break;
+          }
+        __threadfence();
+        asm volatile("fence.proxy.async;" ::: "memory");  // h was written by ordinary stores
+      }
+      __syncwarp();
+      griddep_launch_dependents();
+      for (int i = 0; i < first; ++i) {
+        const MoeStage st = sh.stage[i];
+        fetch.tokens(base + i * down_bytes, smem_u32(&sh.full[i]), st);
+      }
+      ok = ok && *abort_flag == 0;
+      int told = 0;
+      for (s = first == down_stages ? 0 : first; ok; s = s + 1 == down_stages ? 0 : s + 1) {
+        if (!(ok = wait_free())) break;
+        if (walk.done()) {
+          arm(none, 0);
+          if (++told == kTeams) break;
+          continue;
+        }
+        const MoeStage st = walk.stage();
+        arm(st, fetch.bytes(st));
+        fetch.weights(base + s * down_bytes, smem_u32(&sh.full[s]), st);
+        fetch.tokens(base + s * down_bytes, smem_u32(&sh.full[s]), st);
+        walk.next();
+      }
+    }
+    // no copy is in flight when the CTA ends
+    for (s = 0; s < kMoeStages; ++s)
+      if (armed >> s & 1u) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(smem_u32(&sh.full[s]), (used >> s & 1u) ^ 1u) && global_timer_ns() - t0 < p.timeout_ns) {
+        }
+      }
+    return;
+  }
+
+  if (warp > kMoeWarps) {
+    // ------------------------------------------------------------ finish units
+    constexpr bool kTurns = moe_turns(MAX);
+    constexpr int kTeam = kTurns ? 32 : 32 * kMoeFinishers;  // threads that share a unit
+    const int finisher = warp - kMoeWarps - 1, member = kTurns ? 0 : finisher, thread = kTurns ? lane : member * 32 + lane;
+    auto team_barrier = [&]() {
+      if (kTurns) __syncwarp();
+      else named_barrier(1, kTeam);
+    };
+    // The next unit that is this warp's; false where there is none (or a wait ran out).  A warp looks at its own units
+    // alone: their buffers stay until it gives them back.
+    constexpr int kStep = kTurns ? kMoeFinishers : 1;
+    int n = kTurns ? finisher : 0;
+    MoeStage st;
+    bool ok = true;
+    auto take = [&]() {
+      ok = wait_bounded(smem_u32(&sh.summed[n % kBuffers]), (n / kBuffers) & 1, abort_flag, p.timeout_ns, p.err,
+                        kSiteMoeSums);
+      if (ok) st = sh.unit[n % kBuffers];
+      return ok && st.hit >= 0;
+    };
+    auto give = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.taken[n % kBuffers]));
+      n += kStep;
+    };
+    while (take()) {
+      const int first = st.first, count = st.count;
+      const float4* sums = reinterpret_cast<const float4*>(exchange + n % kBuffers * up_buffer) + lane;
+      int octets = 0;
+      for (int tile = member; tile < 1 << Up::lg; tile += kTeam / 32, ++octets)
+        moe_activate<Up>(p, sums + tile * Up::slices * blocks * 32, blocks, st.row / 8 + tile, first, count, lane);
+      give();
+      // the last of 16 octets brings their 128 columns into halves
+      __threadfence();
+      __syncwarp();
+      const int block = st.row / 128;
+      int old = 0;
+      if (lane == 0)
+        old = (int)atomicAdd(p.counter + kMoeBarrierWords + st.hit * down_chunks + block, (uint32_t)octets);
+      old = __shfl_sync(0xffffffffu, old, 0);
+      if (old + octets == 16) {
+        __threadfence();
+        moe_halves(p, block, first, count, lane);
+      }
+    }
+    if (ok) {
+      give();
+      // the units of the second product are counted from st.row on
+      n = st.row + (kTurns ? (finisher + kMoeFinishers - st.row % kMoeFinishers) % kMoeFinishers : 0);
+    }
+    __threadfence();
+    named_barrier(2, 32 * kMoeFinishers);
+    if (tid == 32 * (kMoeWarps + 1)) {
+      __threadfence();
+      atomicAdd(p.counter, 1u);
+    }
+    const int64_t share = (int64_t)p.tokens * p.d;
+    while (ok && take()) {
+      // 4 neighbouring rows of a token a thread
+      const float* sums = exchange + n % kBuffers * down_buffer;
+      const int items = live * (kDownRows / 4);
+      for (int i = thread; i < items; i += kTeam) {
+        const int row = i % (kDownRows / 4) * 4, t = i / (kDownRows / 4);
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < Down::slices; ++k)  // warps k << lg + tile
+          add4(v, *reinterpret_cast<const float4*>(sums + (((k << Down::lg) + (row >> 4)) * live + t) * 16 + (row & 15)));
+        if (parts == 1) moe_store(p, t, st.row + row, v);
+        else __stcg(reinterpret_cast<float4*>(p.part + st.part * share + (int64_t)t * p.d + st.row + row), v);
+      }
+      give();
+      if (parts > 1) {
+        // the last of the shares adds them, in their order
+        __threadfence();
+        team_barrier();
+        int last = 0;
+        if (thread == 0) {
+          last = atomicAdd(p.counter + p.tile_counter + st.row / kDownRows, 1u) == (uint32_t)parts - 1;
+          if (!kTurns) sh.last = last;
+        }
+        team_barrier();
+        last = kTurns ? __shfl_sync(0xffffffffu, last, 0) : sh.last;
+        if (last) {
+          __threadfence();
+          for (int i = thread; i < items; i += kTeam) {
+            const int row = i % (kDownRows / 4) * 4, t = i / (kDownRows / 4);
+            const float* from = p.part + (int64_t)t * p.d + st.row + row;
+            float4 all[kMoeMaxParts];
+#pragma unroll
+            for (int k = 0; k < kMoeMaxParts; ++k)
+              all[k] = k < parts ? __ldcg(reinterpret_cast<const float4*>(from + k * share)) : make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 1; k < kMoeMaxParts; ++k) add4(all[0], all[k]);
+            moe_store(p, t, st.row + row, all[0]);
+          }
+        }
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- multiply
+  const int team = warp / (kMoeWarps / kTeams), member = warp % (kMoeWarps / kTeams);
+  int s = team, n = 0;  // ring slot; units so far
+  MoeStage st;
+  bool ok = true;
+  // the team's next stage, or false where there is none (or a wait ran out)
+  auto take = [&]() {
+    ok = wait_bounded(smem_u32(&sh.full[s]), used >> s & 1u, abort_flag, p.timeout_ns, p.err, kSiteMmaFull);
+    if (ok) st = sh.stage[s];
+    return ok && st.hit >= 0;
+  };
+  auto give = [&](int stages) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
+    used ^= 1u << s;
+    s = s + kTeams == stages + team ? team : s + kTeams;
+  };
+  // a buffer of the exchange is free / holds unit `now`'s sums
+  auto wait_taken = [&]() {
+    ok = wait_bounded(smem_u32(&sh.taken[n % kBuffers]), ((n / kBuffers) & 1) ^ 1, abort_flag, p.timeout_ns, p.err,
+                      kSiteMoeSums);
+  };
+  auto hand_over = [&](const MoeStage& now) {
+    if (tid == 0) sh.unit[n % kBuffers] = now;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.summed[n % kBuffers]));
+    ++n;
+  };
+  // tells each finishing warp that a product has no more units, and where the next one's count begins
+  auto finish = [&]() {
+    constexpr int kTold = moe_turns(MAX) ? kMoeFinishers : 1;
+    const int next = n + kTold;
+    for (int i = 0; i < kTold && ok; ++i) {
+      wait_taken();
+      if (ok) hand_over(MoeStage{-1, 0, 0, 0, next, 0, 0, 0});
+    }
+  };
+  float acc[MAX][4];
+  auto clear = [&]() {
+#pragma unroll
+    for (int nb = 0; nb < MAX; ++nb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nb][i] = 0.0f;
   };
   {
-    // ---- g, u and h
-    constexpr int kGroups = kMoeWarps / kMoeSplit;
-    const int octets = p.f / 8, chunks = p.d / kStreamCols;
-    const int units = hits * octets, step = gridDim.x * kGroups;
-    const int rank = warp % kMoeSplit, c0 = chunks * rank / kMoeSplit, c1 = chunks * (rank + 1) / kMoeSplit;
-    const int begin = blockIdx.x + gridDim.x * (warp / kMoeSplit);
-    int ahead = c0 < c1 ? begin : units, ac = c0;
-    Rows rows;
-    auto aim = [&]() {
-      if (ahead < units) {
-        const int e = sh.hit_expert[ahead / octets], o = ahead % octets * 8;
-        rows.set(p.up + (int64_t)e * 2 * p.f * p.d, p.up_sf + (int64_t)e * ((p.d + 511) / 512) * (2 * p.f), 2 * p.f, p.d,
-                 o, p.f + o, lane);
-      }
-    };
-    aim();
-    auto next = [&]() {
-      if (ahead < units) {
-        rows.copy(slot(), ac, lane);
-        if (++ac == c1) {
-          ac = c0;
-          ahead += step;
-          aim();
+    const int tile = member & ((1 << Up::lg) - 1), slice = member >> Up::lg;
+    while (take()) {
+      if (st.begin) clear();
+      if (st.chunk + kTeams * slice < up_chunks)
+        moe_multiply<true, Up, kTeams, MAX>(smem + s * up_bytes, tile, kTeams * slice, st.chunk, up_chunks, st.count,
+                                            lane, acc);
+      const MoeStage now = st;
+      give(up_stages);
+      if (!now.end) continue;
+      wait_taken();
+      if (!ok) break;
+      float4* sums = reinterpret_cast<float4*>(exchange + n % kBuffers * up_buffer) +
+                     (tile * Up::slices + team * (Up::slices / kTeams) + slice) * blocks * 32 + lane;
+#pragma unroll
+      for (int nb = 0; nb < MAX; ++nb)
+        if (nb * 8 < now.count) sums[nb * 32] = make_float4(acc[nb][0], acc[nb][1], acc[nb][2], acc[nb][3]);
+      hand_over(now);
+    }
+    if (ok) {
+      give(up_stages);
+      finish();
+    }
+    s = team;
+  }
+  const int tile = member & ((1 << Down::lg) - 1), slice = member >> Down::lg, r = lane >> 2, q = lane & 3;
+  bool fresh = true;  // nothing of this unit is in the exchange
+  while (ok && take()) {
+    if (st.chunk < kTeams * Down::slices) clear();  // the team's first stage of an expert
+    const bool real = st.chunk < down_chunks;
+    if (st.chunk + kTeams * slice < down_chunks)
+      moe_multiply<false, Down, kTeams, MAX>(smem + s * down_bytes, tile, kTeams * slice, st.chunk, down_chunks, st.count,
+                                             lane, acc);
+    const MoeStage now = st;
+    give(down_stages);
+    const bool last = real && now.chunk + kTeams * Down::slices >= down_chunks;  // the team's last of the expert
+    if (!last && !now.end) continue;
+    float* const mine = exchange + n % kBuffers * down_buffer + warp * live * 16;  // [token][16 rows]
+    if (fresh) {
+      wait_taken();
+      if (!ok) break;
+      for (int i = lane; i < live * 16; i += 32) mine[i] = 0.0f;
+      __syncwarp();
+    }
+    // an expert's sums, with the weight of each of its tokens
+    if (last) {
+#pragma unroll
+      for (int nb = 0; nb < MAX; ++nb) {
+        if (nb * 8 >= now.count) break;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int m = nb * 8 + 2 * q + i;
+          if (m < now.count) {
+            const int t = sh.pair_token[now.first + m];
+            const float w = sh.weight[t * p.top_k + sh.pair_slot[now.first + m]];
+            float* y = mine + t * 16 + r;
+            y[0] = fmaf(w, acc[nb][i], y[0]);
+            y[8] = fmaf(w, acc[nb][2 + i], y[8]);
+          }
         }
       }
-      cp_async_commit();
-    };
-    for (int i = 0; i < kMoeRing - 1; ++i) next();
-    for (int u = begin; u < units; u += step) {
-      const int hit = u / octets, octet = u % octets;
-      const int count = sh.hit_first[hit + 1] - sh.hit_first[hit];
-#define MOE_CALL(NB) moe_up_unit<NB>(w, hit, octet, c0, c1, stage, next)
-      MOE_BY_COUNT(count, MOE_CALL);
-#undef MOE_CALL
+      __syncwarp();
     }
-    cp_async_wait<0>();
-    __syncwarp();
-    put = stage = 0;
+    fresh = now.end != 0;
+    if (fresh) hand_over(now);
   }
-  // ---- y
-  const int tiles = p.d / 16, chunks = p.f / kStreamCols;
-  int parts = 1;  // of a hit expert's columns, so that every warp has some
-  while (parts < 16 && hits * parts < kMoeWarps && 2 * parts * pairs <= kMoeSlots && parts < chunks) parts *= 2;
-  const int items = hits * parts;
-  int at_tile = blockIdx.x, at_item = warp, ac = 0, ac1 = 0;
-  Rows rows;
-  auto aim = [&]() {
-    while (at_tile < tiles) {
-      for (; at_item < items; at_item += kMoeWarps) {
-        const int part = at_item % parts;
-        ac = chunks * part / parts;
-        ac1 = chunks * (part + 1) / parts;
-        if (ac < ac1) {
-          const int e = sh.hit_expert[at_item / parts];
-          rows.set(p.down + (int64_t)e * p.d * p.f, p.down_sf + (int64_t)e * ((p.f + 511) / 512) * p.d, p.d, p.f,
-                   at_tile * 16, at_tile * 16 + 8, lane);
-          return;
-        }
-      }
-      at_item = warp;
-      at_tile += gridDim.x;
-      if (warp >= items) at_tile = tiles;
-    }
-  };
-  aim();
-  auto next = [&]() {
-    if (at_tile < tiles) {
-      rows.copy(slot(), ac, lane);
-      if (++ac == ac1) {
-        at_item += kMoeWarps;
-        aim();
-      }
-    }
-    cp_async_commit();
-  };
-  // Wd does not wait for h
-  for (int i = 0; i < kMoeRing - 1; ++i) next();
-  // barrier over the grid: all of h is there.  All CTAs run at once (cooperative launch).
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) {
-    atomicAdd(p.counter, 1u);
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1; ld_acquire_gpu(p.counter) < gridDim.x; ++it)
-      if ((it & 63u) == 0 && (global_timer_ns() - t0 > p.timeout_ns || it >= (1u << 28))) {
-        record_error(p.err, DG_ERR_DEVICE_TIMEOUT, kSiteMoeBarrier);
-        sh.last = 1;
-        break;
-      }
-    __threadfence();
-  }
-  __syncthreads();
-  griddep_launch_dependents();
-  const bool failed = sh.last != 0;
-  for (int tile = blockIdx.x; tile < tiles && !failed; tile += gridDim.x) {
-    for (int item = warp; item < items; item += kMoeWarps) {
-      const int hit = item / parts, part = item % parts;
-      const int count = sh.hit_first[hit + 1] - sh.hit_first[hit];
-#define MOE_CALL(NB) \
-  moe_down_item<NB>(w, hit, part, chunks * part / parts, chunks * (part + 1) / parts, stage, next)
-      MOE_BY_COUNT(count, MOE_CALL);
-#undef MOE_CALL
-    }
-    __syncthreads();
-    for (int i = tid; i < live * 16; i += kMoeThreads) {
-      const int t = i >> 4, row = i & 15;
-      float v = 0.0f;
-      for (int j = 0; j < p.top_k; ++j) {
-        const int pair = sh.pair_of[t * p.top_k + j];
-        float s = 0.0f;
-        for (int k = 0; k < parts; ++k) s += w.exchange[(k * pairs + pair) * 16 + row];
-        v = fmaf(sh.weight[t * p.top_k + j], s, v);
-      }
-      const int64_t col = (int64_t)tile * 16 + row;
-      if (p.c) v += __bfloat162float(p.c[(int64_t)t * p.ldc + col]);
-      p.y[(int64_t)t * p.ldy + col] = __float2bfloat16_rn(v);
-    }
-    __syncthreads();
-  }
-  cp_async_wait<0>();
+  if (ok) finish();
 }
 
-constexpr size_t kMoeSmem = (size_t)kMoeSlots * 64 + (size_t)kMoeWarps * kMoeRing * kStreamStageBytes;
+template <int MAX>
+cudaError_t moe_layer_launch(const MoeArgs& p, const void* up, const void* down, MoeEncode encode, int sms,
+                             cudaStream_t stream) {
+  constexpr size_t smem = kMoeSmem + 1024;
+  CUtensorMap map_up, map_down;
+  if (!encode(&map_up, up, p.d, (uint64_t)p.experts * 2 * p.f, 8 << up_lg(MAX), MoeShape<up_lg(MAX)>::slices) ||
+      !encode(&map_down, down, p.f, (uint64_t)p.experts * p.d, 16 << down_lg(MAX), MoeShape<down_lg(MAX)>::slices))
+    return cudaErrorInvalidValue;
+  cudaError_t e = set_smem(moe_layer_kernel<MAX>, smem, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // sets itself up while the scores are computed
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms, 1, 1);
+  cfg.blockDim = dim3(kMoeThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, moe_layer_kernel<MAX>, p, map_up, map_down);
+}
 
 }  // namespace
 
@@ -665,19 +1046,20 @@ uint64_t moe_few_tokens_layout(MoeArgs& a, void* workspace) {
     return p;
   };
   const uint64_t hits = std::min<uint64_t>(e, pairs);
-  a.counters = (int32_t)(kMoeBarrierWords + hits * (f / 128));
+  a.tile_counter = (int32_t)(kMoeBarrierWords + hits * (f / 128));
+  a.counters = (int32_t)(a.tile_counter + d / 16);
   a.counter = reinterpret_cast<uint32_t*>(take((uint64_t)a.counters * 4));
-  a.logits = reinterpret_cast<double*>(take(t * e * 8));
-  a.select = reinterpret_cast<double*>(take(t * e * 8));
-  a.xh = reinterpret_cast<__half*>(take(t * d * 2));
-  a.xs = reinterpret_cast<float*>(take(t * (d / 128) * 4));
+  a.logits = reinterpret_cast<float2*>(take(t * e * 8));
+  a.keys = reinterpret_cast<uint64_t*>(take(t * e * 8));
+  a.xh = take(t * (d / 128) * kMoeChunkBytes);
   a.h = reinterpret_cast<float*>(take(pairs * f * 4));
-  a.hh = reinterpret_cast<__half*>(take(pairs * f * 2));
-  a.hs = reinterpret_cast<float*>(take(pairs * (f / 128) * 4));
+  a.hh = take(pairs * (f / 128) * kMoeChunkBytes);
+  a.part = reinterpret_cast<float*>(take(kMoeMaxParts * t * d * 4));
   return at;
 }
 
-cudaError_t moe_few_tokens_launch(MoeArgs p, bool router_fp32, int sms, bool pdl, cudaStream_t stream) {
+cudaError_t moe_few_tokens_launch(MoeArgs p, const void* up, const void* down, MoeEncode encode, bool router_fp32,
+                                  int sms, bool pdl, cudaStream_t stream) {
   cudaError_t e = error_word_address(&p.err);
   if (e != cudaSuccess) return e;
   const int groups = (p.tokens + kScoreTokens - 1) / kScoreTokens;
@@ -685,18 +1067,11 @@ cudaError_t moe_few_tokens_launch(MoeArgs p, bool router_fp32, int sms, bool pdl
   e = router_fp32 ? launch_op(moe_scores_kernel<float>, grid, kScoreThreads, 0, pdl, stream, p)
                   : launch_op(moe_scores_kernel<__nv_bfloat16>, grid, kScoreThreads, 0, pdl, stream, p);
   if (e != cudaSuccess) return e;
-  if ((e = set_smem(moe_layer_kernel, kMoeSmem, kMoeSmem)) != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sms, 1, 1);
-  cfg.blockDim = dim3(kMoeThreads, 1, 1);
-  cfg.dynamicSmemBytes = kMoeSmem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_layer_kernel, p);
+  // (an expert has at most all tokens)
+  if (p.tokens <= 8) return moe_layer_launch<1>(p, up, down, encode, sms, stream);
+  if (p.tokens <= 16) return moe_layer_launch<2>(p, up, down, encode, sms, stream);
+  if (p.tokens <= 32) return moe_layer_launch<4>(p, up, down, encode, sms, stream);
+  return moe_layer_launch<8>(p, up, down, encode, sms, stream);
 }
 
 }  // namespace dg

@@ -10,7 +10,6 @@
 // a row and instruction.  Product j (0..7) multiplies columns
 //   64 (j / 4) + 16 q + 4 (j % 4) + 0..3
 // of every q.  The tokens' halves are stored in that order: of each 128 columns
-// unit (j / 2), then q, then 8 halves (stream_half_at).
 #pragma once
 
 #include "dg_device.cuh"
@@ -19,12 +18,6 @@
 namespace dg {
 
 constexpr int kStreamCols = 128;                       // columns of a stage
-constexpr int kStreamStageBytes = 16 * kStreamCols + 64;  // 16 rows of codes, one scale word a row
-
-// Place of column k (0..127) among its 128 halves.
-__device__ __forceinline__ int stream_half_at(int k) {
-  return ((k >> 6) * 2 + ((k >> 3) & 1)) * 32 + ((k >> 4) & 3) * 8 + (k & 7);
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -56,19 +49,17 @@ struct DecodeInt8 {
   }
 };
 
-// The lane's codes of a stage, decoded: a[j] are the A registers of product j.
+// The lane's codes of half a stage (h = 0, 1: 64 columns), decoded: a[i] are the
+// A registers of product 4 h + i.
 template <class Decode>
-__device__ __forceinline__ void stream_decode(const uint8_t* stage, int lane, uint32_t (&a)[8][4]) {
+__device__ __forceinline__ void stream_decode(const uint8_t* stage, int h, int lane, uint32_t (&a)[4][4]) {
+  const uint4 g = *reinterpret_cast<const uint4*>(stage + h * 1024 + lane * 16);
+  const uint4 u = *reinterpret_cast<const uint4*>(stage + h * 1024 + 512 + lane * 16);
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const uint4 g = *reinterpret_cast<const uint4*>(stage + p * 1024 + lane * 16);
-    const uint4 u = *reinterpret_cast<const uint4*>(stage + p * 1024 + 512 + lane * 16);
-    const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      Decode::four(gw[i], a[p * 4 + i][0], a[p * 4 + i][2]);
-      Decode::four(uw[i], a[p * 4 + i][1], a[p * 4 + i][3]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    Decode::four(gw[i], a[i][0], a[i][2]);
+    Decode::four(uw[i], a[i][1], a[i][3]);
   }
 }
 
