@@ -8,10 +8,17 @@
 // addition takes the offset away: 5 instructions for 4 codes) and store them
 // where the MMA reads them, in its 128-byte swizzle.
 //
-// One persistent CTA per SM, 16 warps: 0 issues the MMAs, 4-7 scale and store a
+// What bounds it is shared memory: each half is written once and read by the
+// MMAs.  So large products run on CTA pairs (cta_group::2): 256 x 256 tiles in
+// which a CTA widens 128 rows of a and 128 of b, 64 KB a stage of 128 columns
+// where a CTA alone would need 96 for half the products.
+//
+// One persistent CTA per SM, 24 warps: 0 issues the MMAs (of a pair the first
+// CTA's; the second's passes on that its stages are ready), 4-7 scale and store a
 // tile's results from TMEM while the next tile's MMAs run (two accumulators),
-// 8-15 load and widen.  Loads are two stages ahead in registers, so that the
-// wait for a free stage does not put their latency into the chain.
+// 8-23 load and widen.  Loads are two stages ahead
+// in registers, so that the wait for a free stage does not put their latency
+// into the chain.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -26,30 +33,47 @@
 namespace dg {
 namespace {
 
-constexpr int kIgThreads = 512;
-constexpr int kIgProducers = 256;  // warps 8-15
-constexpr int kIgStages = 4;
-constexpr int kIgK = 64;  // columns of a stage: 128 bytes of halves
-constexpr int kIgBand = 16;  // row blocks of a band of tiles
+constexpr int kIgWiden = 16;  // producer warps, from warp 8 on
+constexpr int kIgThreads = 32 * (8 + kIgWiden);
+constexpr int kIgPass = 4 * kIgWiden;  // rows that they load at a time
+constexpr int kIgK = 128;          // columns of a stage: two swizzle atoms of 64 halves
+constexpr int kIgBand = 16;        // row blocks of a band of tiles
 
 // FP32 D (bits 4-5 = 1), FP16 A and B (format 0), both K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n) {
   return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
-template <int BN>
-constexpr int ig_stage_bytes() { return (128 + BN) * 128; }
-template <int BN>
-constexpr size_t ig_smem() { return 1024 + (size_t)kIgStages * ig_stage_bytes<BN>() + 4 * 128 + 256; }
+// A tile: 128 (a pair: 256) rows of a by BN of b; of a pair each CTA widens half
+// of both.
+template <int BN, bool PAIR>
+struct IgPlan {
+  static constexpr int kRowsB = PAIR ? BN / 2 : BN;  // of b that a CTA widens
+  static constexpr int kStage = (128 + kRowsB) * 256;
+  static constexpr int kTail = 4 * 128 + 256;        // channel scales, barriers
+  static constexpr int kFit = (232448 - 1024 - kTail) / kStage, kStages = kFit > 4 ? 4 : kFit;
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kTail;
+  static constexpr uint32_t kCols = 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;  // of TMEM
+  static_assert(kStages >= 2 && kRowsB % 8 == 0, "");
+};
 
 // Row block and column block of tile t: bands of kIgBand row blocks, in each
 // the column blocks one after another, so that the CTAs at work share both.
@@ -75,10 +99,86 @@ __device__ __forceinline__ void ig_widen(uint32_t tile, int row, int q, const ui
                : "memory");
 }
 
-template <int BN>
+// A producer thread's share of a stage: 16 codes of each kIgPass-th row.  A warp's load
+// covers 4 rows' 128 columns; within 8 lanes the stores reach all banks (2 rows,
+// half of the columns).
+template <int ROWS>
+struct IgRows {
+  static constexpr int kPieces = (ROWS + kIgPass - 1) / kIgPass;
+  const int8_t* src;  // the thread's first row, from its first column on
+  int64_t step;       // kIgPass rows
+  uint32_t on;        // bit i: row kIgPass i + row exists
+  __device__ __forceinline__ void aim(const int8_t* base, int64_t ld, int first, int end, int row, int col) {
+    on = 0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (kIgPass * i + row < ROWS && first + kIgPass * i + row < end) on |= 1u << i;
+    src = base + (int64_t)(on ? first + row : 0) * ld + col;
+    step = kIgPass * ld;
+  }
+  __device__ __forceinline__ void load(uint4 (&v)[kPieces], int k, bool in) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      v[i] = in && (on >> i & 1u) ? __ldg(reinterpret_cast<const uint4*>(src + i * step + k)) : make_uint4(0, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void store(const uint4 (&v)[kPieces], uint32_t tile, int row, int atom, int q) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (ROWS % kIgPass == 0 || kIgPass * i + row < ROWS)
+        ig_widen(tile + atom * (ROWS * 128), kIgPass * i + row, q, v[i]);
+  }
+};
+
+// 32 results of row m from column n0 on.
+__device__ __forceinline__ void ig_store(const Int8Args& p, const uint32_t (&acc)[32], float sa, const float* sbw, int m,
+                                         int n0) {
+  const int64_t at = (int64_t)m * p.ldd + n0, from = (int64_t)m * p.ldc + n0;
+  if (p.vector && n0 + 32 <= p.n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 cw = make_uint4(0, 0, 0, 0);
+      if (p.c) cw = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + from)[i];  // c may be d
+      const uint32_t ci[4] = {cw.x, cw.y, cw.z, cw.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 s = *reinterpret_cast<const float2*>(sbw + i * 8 + j * 2);
+        float2 cf = make_float2(0.0f, 0.0f);
+        if (p.c)
+          cf = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&ci[j]))
+                      : make_float2(bf16_lo(ci[j]), bf16_hi(ci[j]));
+        const float x = fmaf(__uint_as_float(acc[i * 8 + j * 2]) * sa, s.x, cf.x);
+        const float y = fmaf(__uint_as_float(acc[i * 8 + j * 2 + 1]) * sa, s.y, cf.y);
+        if (p.fp16) {
+          const __half2 v = __floats2half2_rn(x, y);
+          o[j] = *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+          o[j] = bf16x2_bits(x, y);
+        }
+      }
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (n0 + i < p.n) {
+        float v = __uint_as_float(acc[i]) * sa;
+        if (p.fp16) {
+          v = fmaf(v, sbw[i], p.c ? __half2float(static_cast<const __half*>(p.c)[from + i]) : 0.0f);
+          static_cast<__half*>(p.d)[at + i] = __float2half_rn(v);
+        } else {
+          v = fmaf(v, sbw[i], p.c ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.c)[from + i]) : 0.0f);
+          static_cast<__nv_bfloat16*>(p.d)[at + i] = __float2bfloat16_rn(v);
+        }
+      }
+    }
+  }
+}
+
+template <int BN, bool PAIR>
 __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args p) {
-  constexpr int STAGES = kIgStages, STAGE = ig_stage_bytes<BN>();
-  constexpr int NA = 2, NBP = BN / 64, NP = NA + NBP;  // 16-byte pieces of a producer thread
+  using Plan = IgPlan<BN, PAIR>;
+  constexpr int STAGES = Plan::kStages, STAGE = Plan::kStage, RB = Plan::kRowsB, kTileRows = PAIR ? 256 : 128;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const after = smem_raw + (base - smem_u32(smem_raw)) + STAGES * STAGE;
@@ -92,70 +192,111 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr uint32_t kCols = 2 * BN;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0, unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int units = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full(s), kIgProducers / 32);
+      mbar_init(full(s), kIgWiden + (PAIR && rank == 0 ? 1 : 0));  // and the second CTA's
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), 4);
+      mbar_init(tempty(b), PAIR ? 8 : 4);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc(smem_u32(tmem_slot), kCols);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), Plan::kCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), Plan::kCols);
+      tmem_relinquish();
+    }
     tc_fence_before();
   }
   griddep_wait();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // barriers of both CTAs initialised, TMEM allocated
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (threadIdx.x == 0) griddep_launch_dependents();
 
-  const int mb_all = (p.m + 127) / 128, nb_all = (p.n + BN - 1) / BN, tiles = mb_all * nb_all;
+  const int mb_all = (p.m + kTileRows - 1) / kTileRows, nb_all = (p.n + BN - 1) / BN, tiles = mb_all * nb_all;
   const int kbs = (p.k + kIgK - 1) / kIgK;
   const uint64_t tmo = p.timeout_ns;
+  // an arrival that the MMAs' issuer waits for
+  auto tell = [&](uint32_t bar) {
+    if constexpr (PAIR) mbar_arrive_cluster(mapa_shared(bar, 0));
+    else mbar_arrive(bar);
+  };
+  auto commit = [&](uint32_t bar) {
+    if constexpr (PAIR) tc_commit_pair(bar);
+    else tc_commit(bar);
+  };
+  auto told = [&](uint32_t bar, uint32_t parity, uint32_t site) {
+    if constexpr (PAIR) return wait_bounded_cluster(bar, parity, abort_flag, tmo, p.err, site);
+    else return wait_bounded(bar, parity, abort_flag, tmo, p.err, site);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      int s = 0;
-      uint32_t phase = 0, pass = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++pass) {
-        const uint32_t buf = pass & 1u;
-        if (!wait_bounded(tempty(buf), ((pass >> 1) & 1u) ^ 1u, abort_flag, tmo, p.err, kSiteMmaTmemEmpty)) break;
-        tc_fence_after();
-        for (int kb = 0; kb < kbs; ++kb) {
-          if (!wait_bounded(full(s), phase, abort_flag, tmo, p.err, kSiteMmaFull)) {
-            ok = false;
-            break;
-          }
+      if (rank == 0) {
+        int s = 0;
+        uint32_t phase = 0, pass = 0;
+        bool ok = true;
+        for (int t = unit; t < tiles && ok; t += units, ++pass) {
+          const uint32_t buf = pass & 1u;
+          if (!told(tempty(buf), ((pass >> 1) & 1u) ^ 1u, kSiteMmaTmemEmpty)) break;
           tc_fence_after();
-          const uint64_t ad = smem_desc_kmajor_sw128(base + s * STAGE);
-          const uint64_t bd = smem_desc_kmajor_sw128(base + s * STAGE + 16384);
+          for (int kb = 0; kb < kbs; ++kb) {
+            if (!told(full(s), phase, kSiteMmaFull)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            tc_mma_f16(tmem + buf * BN, ad + 2 * j, bd + 2 * j, idesc_f16(128, BN), kb != 0 || j != 0);
-          tc_commit(empty(s));
-          if (++s == STAGES) {
-            s = 0;
-            phase ^= 1u;
+            for (int atom = 0; atom < 2; ++atom) {
+              const uint64_t ad = smem_desc_kmajor_sw128(base + s * STAGE + atom * 16384);
+              const uint64_t bd = smem_desc_kmajor_sw128(base + s * STAGE + 32768 + atom * (RB * 128));
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tc_mma_f16<PAIR>(tmem + buf * BN, ad + 2 * j, bd + 2 * j, idesc_f16(kTileRows, BN),
+                                 kb != 0 || atom != 0 || j != 0);
+            }
+            commit(empty(s));
+            if (++s == STAGES) {
+              s = 0;
+              phase ^= 1u;
+            }
           }
+          if (ok) commit(tfull(buf));
         }
-        if (ok) tc_commit(tfull(buf));
+        commit(drain);
+      } else {
+        // the second CTA's stages, for the first: one arrival across the cluster a stage, not one a warp (each waits
+        // for the warp's own loads in flight)
+        int s = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = unit; t < tiles && ok; t += units)
+          for (int kb = 0; kb < kbs; ++kb) {
+            if (!(ok = wait_bounded(full(s), phase, abort_flag, tmo, p.err, kSiteMmaFull))) break;
+            mbar_arrive_cluster(mapa_shared(full(s), 0));
+            if (++s == STAGES) {
+              s = 0;
+              phase ^= 1u;
+            }
+          }
       }
       // the MMAs in flight end before the memory they use is given back
-      tc_commit(drain);
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(drain, 0))
-        if (global_timer_ns() - t0 > tmo) {
+        if (global_timer_ns() - t0 > 2 * tmo + 1000000000ull) {
           record_error(p.err, DG_ERR_DEVICE_TIMEOUT, kSiteDrain);
           break;
         }
@@ -163,40 +304,40 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------ load and widen
-    const int pt = threadIdx.x - (kIgThreads - kIgProducers), row = pt >> 2, q = pt & 3;
-    const int8_t* src[NP];
-    uint32_t on = 0;  // bit i: piece i's row exists
-    int lt = blockIdx.x, lk = 0;
+    const int q = lane & 3, atom = lane >> 3 & 1;
+    const int row = (warp - 8) * 4 + (lane >> 4) * 2 + (lane >> 2 & 1);
+    const int col = atom * 64 + q * 16;
+    IgRows<128> a;
+    IgRows<RB> b;
+    int lt = unit, lk = 0;
     auto aim = [&]() {
-      on = 0;
-      if (lt >= tiles) return;
+      if (lt >= tiles) {
+        a.on = b.on = 0;
+        return;
+      }
       int mb, nb;
       ig_tile(lt, mb_all, nb_all, mb, nb);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int rr = i < NA ? mb * 128 + i * 64 + row : nb * BN + (i - NA) * 64 + row;
-        const bool in = rr < (i < NA ? p.m : p.n);
-        on |= (uint32_t)in << i;
-        src[i] = (i < NA ? p.a : p.b) + (int64_t)(in ? rr : 0) * (i < NA ? p.lda : p.ldb) + q * 16;
-      }
+      a.aim(p.a, p.lda, mb * kTileRows + rank * 128, p.m, row, col);
+      b.aim(p.b, p.ldb, nb * BN + rank * RB, p.n, row, col);
     };
-    auto load = [&](uint4 (&v)[NP]) {
+    auto load = [&](uint4 (&va)[IgRows<128>::kPieces], uint4 (&vb)[IgRows<RB>::kPieces]) {
       const int k = lk * kIgK;
-      const bool in = k + q * 16 < p.k;
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-        v[i] = in && (on >> i & 1u) ? __ldg(reinterpret_cast<const uint4*>(src[i] + k)) : make_uint4(0, 0, 0, 0);
+      const bool in = k + col < p.k;
+      a.load(va, k, in);
+      b.load(vb, k, in);
       if (++lk == kbs) {
         lk = 0;
-        lt += gridDim.x;
+        lt += units;
         aim();
       }
     };
+    a.src = b.src = p.a;
+    a.step = b.step = 0;
     aim();
-    uint4 v[2][NP];
-    load(v[0]);
-    load(v[1]);
-    const int mine = (int)blockIdx.x < tiles ? (tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    uint4 va[2][IgRows<128>::kPieces], vb[2][IgRows<RB>::kPieces];
+    load(va[0], vb[0]);
+    load(va[1], vb[1]);
+    const int mine = unit < tiles ? (tiles - 1 - unit) / units + 1 : 0;
     const int64_t stages = (int64_t)mine * kbs;
     int s = 0;
     uint32_t phase = 0;
@@ -209,14 +350,12 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
           ok = false;
           break;
         }
-        const uint32_t at = base + s * STAGE;
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-          ig_widen(i < NA ? at : at + 16384, (i < NA ? i : i - NA) * 64 + row, q, v[h][i]);
+        a.store(va[h], base + s * STAGE, row, atom, q);
+        b.store(vb[h], base + s * STAGE + 32768, row, atom, q);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full(s));
-        load(v[h]);
+        load(va[h], vb[h]);
         if (++s == STAGES) {
           s = 0;
           phase ^= 1u;
@@ -228,11 +367,11 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
     const int quarter = warp & 3;
     float* const sbw = sb_row + quarter * 32;
     uint32_t pass = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++pass) {
+    for (int t = unit; t < tiles; t += units, ++pass) {
       int mb, nb;
       ig_tile(t, mb_all, nb_all, mb, nb);
       const uint32_t buf = pass & 1u;
-      const int m = mb * 128 + quarter * 32 + lane;
+      const int m = mb * kTileRows + rank * 128 + quarter * 32 + lane;
       const float sa = m < p.m ? __ldg(p.sa + m) : 0.0f;
       if (!wait_bounded(tfull(buf), (pass >> 1) & 1u, abort_flag, tmo, p.err, kSiteEpilogueTmemFull)) break;
       tc_fence_after();
@@ -247,68 +386,52 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
         if (ch == BN / 32 - 1) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(tempty(buf));
+          if (lane == 0) tell(tempty(buf));
         }
         if (m >= p.m || n0 >= p.n) continue;
-        const int64_t at = (int64_t)m * p.ldd + n0, from = (int64_t)m * p.ldc + n0;
-        if (p.vector && n0 + 32 <= p.n) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 cw = make_uint4(0, 0, 0, 0);
-            if (p.c) cw = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + from)[i];  // c may be d
-            const uint32_t ci[4] = {cw.x, cw.y, cw.z, cw.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 s = *reinterpret_cast<const float2*>(sbw + i * 8 + j * 2);
-              float2 cf = make_float2(0.0f, 0.0f);
-              if (p.c)
-                cf = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&ci[j]))
-                            : make_float2(bf16_lo(ci[j]), bf16_hi(ci[j]));
-              const float x = fmaf(__uint_as_float(acc[i * 8 + j * 2]) * sa, s.x, cf.x);
-              const float y = fmaf(__uint_as_float(acc[i * 8 + j * 2 + 1]) * sa, s.y, cf.y);
-              if (p.fp16) {
-                const __half2 v = __floats2half2_rn(x, y);
-                o[j] = *reinterpret_cast<const uint32_t*>(&v);
-              } else {
-                o[j] = bf16x2_bits(x, y);
-              }
-            }
-            reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at)[i] = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (n0 + i < p.n) {
-              float v = __uint_as_float(acc[i]) * sa;
-              if (p.fp16) {
-                v = fmaf(v, sbw[i], p.c ? __half2float(static_cast<const __half*>(p.c)[from + i]) : 0.0f);
-                static_cast<__half*>(p.d)[at + i] = __float2half_rn(v);
-              } else {
-                v = fmaf(v, sbw[i], p.c ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.c)[from + i]) : 0.0f);
-                static_cast<__nv_bfloat16*>(p.d)[at + i] = __float2bfloat16_rn(v);
-              }
-            }
-          }
-        }
+        ig_store(p, acc, sa, sbw, m, n0);
       }
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // both CTAs are done with every role
+  else __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, Plan::kCols);
+    else tmem_dealloc(tmem, Plan::kCols);
   }
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 cudaError_t ig_launch(const Int8Args& p, bool pdl, cudaStream_t stream) {
-  cudaError_t e = set_smem(int8_gemm_kernel<BN>, ig_smem<BN>(), ig_smem<BN>());
+  using Plan = IgPlan<BN, PAIR>;
+  cudaError_t e = set_smem(int8_gemm_kernel<BN, PAIR>, Plan::kSmem, Plan::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)((p.m + 127) / 128) * ((p.n + BN - 1) / BN);
-  return launch_op(int8_gemm_kernel<BN>, dim3((unsigned)std::min<int64_t>(tiles, p.sms)), kIgThreads, ig_smem<BN>(), pdl,
-                   stream, p);
+  const int64_t tiles = (int64_t)((p.m + (PAIR ? 255 : 127)) / (PAIR ? 256 : 128)) * ((p.n + BN - 1) / BN);
+  const int64_t units = std::min<int64_t>(tiles, PAIR ? p.sms / 2 : p.sms);
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (PAIR) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(PAIR ? 2 * units : units), 1, 1);
+  cfg.blockDim = dim3(kIgThreads, 1, 1);
+  cfg.dynamicSmemBytes = Plan::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<BN, PAIR>, p);
 }
 
 }  // namespace
@@ -316,10 +439,26 @@ cudaError_t ig_launch(const Int8Args& p, bool pdl, cudaStream_t stream) {
 cudaError_t int8_gemm_launch(Int8Args p, bool pdl, cudaStream_t stream) {
   cudaError_t e = error_word_address(&p.err);
   if (e != cudaSuccess) return e;
+  // Pairs where their tiles fill most of the SMs: the width whose last wave is
+  // fullest, by the columns that the waves pass over.
+  const int64_t mb2 = (p.m + 255) / 256, pairs = p.sms / 2;
+  if (pairs > 0 && mb2 * ((p.n + 255) / 256) * 4 >= pairs * 3) {
+    int best = 256;
+    int64_t least = INT64_MAX;
+    for (int bn : {256, 224, 192}) {
+      const int64_t waves = (mb2 * ((p.n + bn - 1) / bn) + pairs - 1) / pairs, cost = waves * bn;
+      if (cost < least) {
+        least = cost;
+        best = bn;
+      }
+    }
+    if (best == 192) return ig_launch<192, true>(p, pdl, stream);
+    if (best == 224) return ig_launch<224, true>(p, pdl, stream);
+    return ig_launch<256, true>(p, pdl, stream);
+  }
   const int64_t mb = (p.m + 127) / 128;
-  if (mb * ((p.n + 255) / 256) >= p.sms) return ig_launch<256>(p, pdl, stream);
-  if (mb * ((p.n + 127) / 128) >= p.sms) return ig_launch<128>(p, pdl, stream);
-  return ig_launch<64>(p, pdl, stream);
+  if (mb * ((p.n + 127) / 128) >= p.sms) return ig_launch<128, false>(p, pdl, stream);
+  return ig_launch<64, false>(p, pdl, stream);
 }
 
 }  // namespace dg
