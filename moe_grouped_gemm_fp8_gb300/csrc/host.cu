@@ -1774,8 +1774,10 @@ dg_status dg_int8_gemm_nt(const void* a, const float* sa, const void* b, const f
   p.sms = sms;
   p.timeout_ns = g_timeout_ns.load();
   const bool pdl = g_pdl.load() != 0;
-  return from_cuda(m <= int8_stream_max_tokens() ? int8_stream_launch(p, pdl, static_cast<cudaStream_t>(stream))
-                                                 : int8_gemm_launch(p, pdl, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (int8_stream_takes(p)) return from_cuda(int8_stream_launch(p, pdl, st));
+  if (int8_decode_takes(p)) return from_cuda(int8_decode_launch(p, pdl, st));
+  return from_cuda(int8_gemm_launch(p, pdl, st));
 }
 
 dg_status dg_quantize_int8(const void* x, int32_t dtype, void* q, float* scales, int64_t rows, int64_t cols,

@@ -28,39 +28,12 @@
 #include "dg_device.cuh"
 #include "dg_ops.cuh"
 #include "int8_gemm.h"
-#include "stream_mma.cuh"
+#include "int8_tile.cuh"
 
 namespace dg {
 namespace {
 
-constexpr int kIgWiden = 16;  // producer warps, from warp 8 on
-constexpr int kIgThreads = 32 * (8 + kIgWiden);
-constexpr int kIgPass = 4 * kIgWiden;  // rows that they load at a time
-constexpr int kIgK = 128;          // columns of a stage: two swizzle atoms of 64 halves
-constexpr int kIgBand = 16;        // row blocks of a band of tiles
-
-// FP32 D (bits 4-5 = 1), FP16 A and B (format 0), both K-major.
-__host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n) {
-  return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
-}
-template <bool PAIR>
-__device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
+constexpr int kIgBand = 16;  // row blocks of a band of tiles
 
 // A tile: 128 (a pair: 256) rows of a by BN of b; of a pair each CTA widens half
 // of both.
@@ -68,7 +41,8 @@ template <int BN, bool PAIR>
 struct IgPlan {
   static constexpr int kRowsB = PAIR ? BN / 2 : BN;  // of b that a CTA widens
   static constexpr int kStage = (128 + kRowsB) * 256;
-  static constexpr int kTail = 4 * 128 + 256;        // channel scales, barriers
+  // channel scales and a 32 x 33 tile of each storing warp, barriers
+  static constexpr int kTail = 4 * (BN + 32 * 33) * 4 + 256;
   static constexpr int kFit = (232448 - 1024 - kTail) / kStage, kStages = kFit > 4 ? 4 : kFit;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kTail;
   static constexpr uint32_t kCols = 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;  // of TMEM
@@ -84,94 +58,63 @@ __device__ __forceinline__ void ig_tile(int t, int mb_all, int nb_all, int& mb, 
   mb = first + in - nb * height;
 }
 
-// 16 codes at the 16-byte chunks 2 q and 2 q + 1 of a row of 128 bytes of halves.
-__device__ __forceinline__ void ig_widen(uint32_t tile, int row, int q, const uint4& c) {
-  uint32_t h[8];
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) DecodeInt8::four(w[i], h[2 * i], h[2 * i + 1]);
-  const uint32_t line = tile + row * 128, x = row & 7;
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + (((2 * q) ^ x) << 4)), "r"(h[0]), "r"(h[1]),
-               "r"(h[2]), "r"(h[3])
-               : "memory");
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + (((2 * q + 1) ^ x) << 4)), "r"(h[4]), "r"(h[5]),
-               "r"(h[6]), "r"(h[7])
-               : "memory");
-}
-
-// A producer thread's share of a stage: 16 codes of each kIgPass-th row.  A warp's load
-// covers 4 rows' 128 columns; within 8 lanes the stores reach all banks (2 rows,
-// half of the columns).
-template <int ROWS>
-struct IgRows {
-  static constexpr int kPieces = (ROWS + kIgPass - 1) / kIgPass;
-  const int8_t* src;  // the thread's first row, from its first column on
-  int64_t step;       // kIgPass rows
-  uint32_t on;        // bit i: row kIgPass i + row exists
-  __device__ __forceinline__ void aim(const int8_t* base, int64_t ld, int first, int end, int row, int col) {
-    on = 0;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (kIgPass * i + row < ROWS && first + kIgPass * i + row < end) on |= 1u << i;
-    src = base + (int64_t)(on ? first + row : 0) * ld + col;
-    step = kIgPass * ld;
-  }
-  __device__ __forceinline__ void load(uint4 (&v)[kPieces], int k, bool in) const {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      v[i] = in && (on >> i & 1u) ? __ldg(reinterpret_cast<const uint4*>(src + i * step + k)) : make_uint4(0, 0, 0, 0);
-  }
-  static __device__ __forceinline__ void store(const uint4 (&v)[kPieces], uint32_t tile, int row, int atom, int q) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (ROWS % kIgPass == 0 || kIgPass * i + row < ROWS)
-        ig_widen(tile + atom * (ROWS * 128), kIgPass * i + row, q, v[i]);
-  }
-};
-
-// 32 results of row m from column n0 on.
+// 32 results of row m from column n0 on, all there and on 16 bytes.
 __device__ __forceinline__ void ig_store(const Int8Args& p, const uint32_t (&acc)[32], float sa, const float* sbw, int m,
                                          int n0) {
   const int64_t at = (int64_t)m * p.ldd + n0, from = (int64_t)m * p.ldc + n0;
-  if (p.vector && n0 + 32 <= p.n) {
+  uint4 all[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint4 cw = make_uint4(0, 0, 0, 0);
-      if (p.c) cw = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + from)[i];  // c may be d
-      const uint32_t ci[4] = {cw.x, cw.y, cw.z, cw.w};
-      uint32_t o[4];
+  for (int i = 0; i < 4; ++i)  // c may be d
+    all[i] = p.c ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + from)[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 s = *reinterpret_cast<const float2*>(sbw + i * 8 + j * 2);
-        float2 cf = make_float2(0.0f, 0.0f);
-        if (p.c)
-          cf = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&ci[j]))
-                      : make_float2(bf16_lo(ci[j]), bf16_hi(ci[j]));
-        const float x = fmaf(__uint_as_float(acc[i * 8 + j * 2]) * sa, s.x, cf.x);
-        const float y = fmaf(__uint_as_float(acc[i * 8 + j * 2 + 1]) * sa, s.y, cf.y);
-        if (p.fp16) {
-          const __half2 v = __floats2half2_rn(x, y);
-          o[j] = *reinterpret_cast<const uint32_t*>(&v);
-        } else {
-          o[j] = bf16x2_bits(x, y);
-        }
-      }
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at)[i] = make_uint4(o[0], o[1], o[2], o[3]);
-    }
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    const uint4 cw = all[i];
+    const uint32_t ci[4] = {cw.x, cw.y, cw.z, cw.w};
+    uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (n0 + i < p.n) {
-        float v = __uint_as_float(acc[i]) * sa;
-        if (p.fp16) {
-          v = fmaf(v, sbw[i], p.c ? __half2float(static_cast<const __half*>(p.c)[from + i]) : 0.0f);
-          static_cast<__half*>(p.d)[at + i] = __float2half_rn(v);
-        } else {
-          v = fmaf(v, sbw[i], p.c ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.c)[from + i]) : 0.0f);
-          static_cast<__nv_bfloat16*>(p.d)[at + i] = __float2bfloat16_rn(v);
-        }
+    for (int j = 0; j < 4; ++j) {
+      const float2 s = *reinterpret_cast<const float2*>(sbw + i * 8 + j * 2);
+      float2 cf = make_float2(0.0f, 0.0f);
+      if (p.c)
+        cf = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&ci[j]))
+                    : make_float2(bf16_lo(ci[j]), bf16_hi(ci[j]));
+      const float x = fmaf(__uint_as_float(acc[i * 8 + j * 2]) * sa, s.x, cf.x);
+      const float y = fmaf(__uint_as_float(acc[i * 8 + j * 2 + 1]) * sa, s.y, cf.y);
+      if (p.fp16) {
+        const __half2 v = __floats2half2_rn(x, y);
+        o[j] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        o[j] = bf16x2_bits(x, y);
       }
     }
+    reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// The same where rows are on no boundary or the columns end: by way of shared
+// memory, so that a warp writes a row's 32 columns at once (a lane's own row, value
+// by value, would touch 32 rows an instruction: 333 x 1001 x 1552 23 us against
+// 17).
+__device__ __forceinline__ void ig_store_ragged(const Int8Args& p, const uint32_t (&acc)[32], float sa, const float* sbw,
+                                                float* turn, int m0, int n0, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = __uint_as_float(acc[i]) * sa;
+  __syncwarp();
+  const int n = n0 + lane;
+  if (n >= p.n) return;
+  const float sb = sbw[lane];
+  const int rows = min(32, p.m - m0);
+#pragma unroll 8
+  for (int i = 0; i < rows; ++i) {
+    const int64_t at = (int64_t)(m0 + i) * p.ldd + n, from = (int64_t)(m0 + i) * p.ldc + n;
+    const float v = turn[i * 33 + lane];
+    if (p.fp16)
+      static_cast<__half*>(p.d)[at] =
+          __float2half_rn(fmaf(v, sb, p.c ? __half2float(static_cast<const __half*>(p.c)[from]) : 0.0f));
+    else
+      static_cast<__nv_bfloat16*>(p.d)[at] =
+          __float2bfloat16_rn(fmaf(v, sb, p.c ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.c)[from]) : 0.0f));
   }
 }
 
@@ -182,8 +125,8 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const after = smem_raw + (base - smem_u32(smem_raw)) + STAGES * STAGE;
-  float* const sb_row = reinterpret_cast<float*>(after);  // [4 warps][32]
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(after + 4 * 128);
+  float* const sb_row = reinterpret_cast<float*>(after);  // [4 warps][BN]
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(after + 4 * (BN + 32 * 33) * 4);
   auto full = [&](int s) { return smem_u32(bars + s); };
   auto empty = [&](int s) { return smem_u32(bars + STAGES + s); };
   auto tfull = [&](int s) { return smem_u32(bars + 2 * STAGES + s); };
@@ -238,8 +181,8 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
     else tc_commit(bar);
   };
   auto told = [&](uint32_t bar, uint32_t parity, uint32_t site) {
-    if constexpr (PAIR) return wait_bounded_cluster(bar, parity, abort_flag, tmo, p.err, site);
-    else return wait_bounded(bar, parity, abort_flag, tmo, p.err, site);
+    if constexpr (PAIR) return wait_quick<true>(bar, parity, abort_flag, tmo, p.err, site);
+    else return wait_quick(bar, parity, abort_flag, tmo, p.err, site);
   };
 
   if (warp == 0) {
@@ -258,6 +201,7 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
               ok = false;
               break;
             }
+            fence_proxy_async_smem();
             tc_fence_after();
 #pragma unroll
             for (int atom = 0; atom < 2; ++atom) {
@@ -285,7 +229,8 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
         bool ok = true;
         for (int t = unit; t < tiles && ok; t += units)
           for (int kb = 0; kb < kbs; ++kb) {
-            if (!(ok = wait_bounded(full(s), phase, abort_flag, tmo, p.err, kSiteMmaFull))) break;
+            if (!(ok = wait_quick(full(s), phase, abort_flag, tmo, p.err, kSiteMmaFull))) break;
+            fence_proxy_async_smem();
             mbar_arrive_cluster(mapa_shared(full(s), 0));
             if (++s == STAGES) {
               s = 0;
@@ -304,8 +249,7 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------ load and widen
-    const int q = lane & 3, atom = lane >> 3 & 1;
-    const int row = (warp - 8) * 4 + (lane >> 4) * 2 + (lane >> 2 & 1);
+    const int q = lane & 3, atom = lane >> 2 & 1, row = (warp - 8) * 4 + (lane >> 3);
     const int col = atom * 64 + q * 16;
     IgRows<128> a;
     IgRows<RB> b;
@@ -323,8 +267,8 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
     auto load = [&](uint4 (&va)[IgRows<128>::kPieces], uint4 (&vb)[IgRows<RB>::kPieces]) {
       const int k = lk * kIgK;
       const bool in = k + col < p.k;
-      a.load(va, k, in);
-      b.load(vb, k, in);
+      a.load(va, p.lda, k, in);
+      b.load(vb, p.ldb, k, in);
       if (++lk == kbs) {
         lk = 0;
         lt += units;
@@ -332,27 +276,25 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
       }
     };
     a.src = b.src = p.a;
-    a.step = b.step = 0;
     aim();
-    uint4 va[2][IgRows<128>::kPieces], vb[2][IgRows<RB>::kPieces];
-    load(va[0], vb[0]);
-    load(va[1], vb[1]);
+    uint4 va[kIgAhead][IgRows<128>::kPieces], vb[kIgAhead][IgRows<RB>::kPieces];
+#pragma unroll
+    for (int h = 0; h < kIgAhead; ++h) load(va[h], vb[h]);
     const int mine = unit < tiles ? (tiles - 1 - unit) / units + 1 : 0;
-    const int64_t stages = (int64_t)mine * kbs;
+    const int stages = mine * kbs;
     int s = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int64_t it = 0; it < stages && ok; it += 2) {
+    for (int it = 0; it < stages && ok; it += kIgAhead) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kIgAhead; ++h) {
         if (it + h >= stages || !ok) break;
-        if (!wait_bounded(empty(s), phase ^ 1u, abort_flag, tmo, p.err, kSiteProducerEmpty)) {
+        if (!wait_quick(empty(s), phase ^ 1u, abort_flag, tmo, p.err, kSiteProducerEmpty)) {
           ok = false;
           break;
         }
         a.store(va[h], base + s * STAGE, row, atom, q);
         b.store(vb[h], base + s * STAGE + 32768, row, atom, q);
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full(s));
         load(va[h], vb[h]);
@@ -365,7 +307,8 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
   } else if (warp >= 4) {
     // ------------------------------------------------------------ scale and store
     const int quarter = warp & 3;
-    float* const sbw = sb_row + quarter * 32;
+    float* const sbw = sb_row + quarter * BN;
+    float* const turn = sb_row + 4 * BN + quarter * 32 * 33;
     uint32_t pass = 0;
     for (int t = unit; t < tiles; t += units, ++pass) {
       int mb, nb;
@@ -373,23 +316,27 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_gemm_kernel(const Int8Args
       const uint32_t buf = pass & 1u;
       const int m = mb * kTileRows + rank * 128 + quarter * 32 + lane;
       const float sa = m < p.m ? __ldg(p.sa + m) : 0.0f;
-      if (!wait_bounded(tfull(buf), (pass >> 1) & 1u, abort_flag, tmo, p.err, kSiteEpilogueTmemFull)) break;
+      __syncwarp();  // the last tile's scales are read
+#pragma unroll
+      for (int i = 0; i < BN; i += 32) sbw[i + lane] = nb * BN + i + lane < p.n ? __ldg(p.sb + nb * BN + i + lane) : 0.0f;
+      __syncwarp();
+      if (!wait_quick(tfull(buf), (pass >> 1) & 1u, abort_flag, tmo, p.err, kSiteEpilogueTmemFull)) break;
       tc_fence_after();
       for (int ch = 0; ch < BN / 32; ++ch) {
         const int n0 = nb * BN + ch * 32;
         uint32_t acc[32];
         tc_ld_32x32b_x32(tmem + buf * BN + ch * 32 + ((uint32_t)(quarter * 32) << 16), acc);
-        __syncwarp();  // the last chunk's scales are read
-        sbw[lane] = n0 + lane < p.n ? __ldg(p.sb + n0 + lane) : 0.0f;
-        __syncwarp();
         tc_wait_ld_regs(acc);
         if (ch == BN / 32 - 1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) tell(tempty(buf));
         }
-        if (m >= p.m || n0 >= p.n) continue;
-        ig_store(p, acc, sa, sbw, m, n0);
+        if (p.vector && n0 + 32 <= p.n) {
+          if (m < p.m) ig_store(p, acc, sa, sbw + ch * 32, m, n0);
+        } else if (n0 < p.n && m - lane < p.m) {
+          ig_store_ragged(p, acc, sa, sbw + ch * 32, turn, m - lane, n0, lane);
+        }
       }
     }
   }

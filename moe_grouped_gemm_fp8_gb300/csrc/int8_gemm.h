@@ -23,9 +23,12 @@ struct Int8Args {
   unsigned long long* err;
 };
 
-// int8_stream.cu: up to int8_stream_max_tokens() rows of a
-int int8_stream_max_tokens();
+// int8_stream.cu: a few rows of a, without widening them in memory
+bool int8_stream_takes(const Int8Args& p);
 cudaError_t int8_stream_launch(const Int8Args& p, bool pdl, cudaStream_t stream);
+// int8_decode.cu: up to 128 rows of a, operand roles swapped
+bool int8_decode_takes(const Int8Args& p);
+cudaError_t int8_decode_launch(Int8Args p, bool pdl, cudaStream_t stream);
 // int8_gemm.cu: tiles on the tensor cores
 cudaError_t int8_gemm_launch(Int8Args p, bool pdl, cudaStream_t stream);
 

@@ -21,25 +21,24 @@ namespace {
 
 constexpr int kQiItems = 32;  // values a thread keeps (16-bit types; FP32: 16)
 
+// Values 4 i to 4 i + 3 of a thread's words.
 template <class T>
-__device__ __forceinline__ float qi_float(T v) {
-  if constexpr (std::is_same<T, float>::value) return v;
-  else if constexpr (std::is_same<T, __half>::value) return __half2float(v);
-  else return __bfloat162float(v);
-}
-template <class T>
-__device__ __forceinline__ void qi_unpack(const uint4& a, float* v) {
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void qi_unpack(const uint32_t* w, int i, float (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(w[i]);
-    else if constexpr (std::is_same<T, __half>::value) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    } else {
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
+    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(w[4 * i + j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t b = w[2 * i + j];
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b));
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      } else {
+        v[2 * j] = bf16_lo(b);
+        v[2 * j + 1] = bf16_hi(b);
+      }
     }
   }
 }
@@ -71,7 +70,7 @@ __device__ __noinline__ int qi_tiny(float v, float amax) { return (int)rint(127.
 
 // Four values -> four codes in a word.  far: the largest distance of an
 // estimate from its integer.
-__device__ __forceinline__ uint32_t qi_four(const float* v, float inv, float& far) {
+__device__ __forceinline__ uint32_t qi_four(const float (&v)[4], float inv, float& far) {
   const float2 magic = make_float2(12582912.0f, 12582912.0f), back = make_float2(-12582912.0f, -12582912.0f);
   const float2 t0 = mul2(make_float2(v[0], v[1]), inv), t1 = mul2(make_float2(v[2], v[3]), inv);
   const float2 u0 = add2(t0, magic), u1 = add2(t1, magic);
@@ -92,7 +91,7 @@ constexpr float kQiTiny = 1e-30f;  // below it 127 / amax may overflow
 // W warps a row.  VEC: rows of x on 16 bytes and of codes on 16 / sizeof(T);
 // else a value at a time.
 template <class T, int W, bool VEC>
-__global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W)
+__global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W, W <= 8 ? 4 : 2)
     quantize_int8_kernel(const T* __restrict__ x, int8_t* __restrict__ q, float* __restrict__ scales, int64_t rows,
                          int cols, int64_t ldx) {
   constexpr int E = 16 / sizeof(T), V = kQiItems * 2 / sizeof(T) / E, PER = E * V;
@@ -107,23 +106,29 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W)
   const T* xr = x + (on ? row : 0) * ldx;
   const int n = on ? cols : 0;
   constexpr int kWide = 32 * W * PER;  // columns of a pass; more than one only at the widest W
-  float v[PER];
+  uint32_t x4[V * 4];  // the values as they came
   float m = 0.0f;
   auto load = [&](int c0) {
     if constexpr (VEC) {
-      uint4 w[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = c0 + (i * 32 * W + at) * E;
-        w[i] = c < n ? ld_stream_u4(xr + c) : make_uint4(0, 0, 0, 0);
+        const uint4 w = c < n ? ld_stream_u4(xr + c) : make_uint4(0, 0, 0, 0);
+        x4[4 * i] = w.x;
+        x4[4 * i + 1] = w.y;
+        x4[4 * i + 2] = w.z;
+        x4[4 * i + 3] = w.w;
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) qi_unpack<T>(w[i], v + i * E);
     } else {
+      using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+      const Bits* bits = reinterpret_cast<const Bits*>(xr);
+      constexpr int kPack = 4 / sizeof(T);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int c = c0 + i * 32 * W + at;
-        v[i] = c < n ? qi_float(xr[c]) : 0.0f;
+        const uint32_t one = c < n ? (uint32_t)bits[c] : 0u;
+        if (i % kPack == 0) x4[i / kPack] = one;
+        else x4[i / kPack] |= one << 16;
       }
     }
   };
@@ -131,7 +136,11 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W)
   for (int c0 = 0; c0 == 0 || c0 < cols; c0 += kWide) {
     load(c0);
 #pragma unroll
-    for (int i = 0; i < PER; i += 2) m = qi_max(m, v[i], v[i + 1]);
+    for (int i = 0; i < PER / 4; ++i) {
+      float v[4];
+      qi_unpack<T>(x4, i, v);
+      m = qi_max(qi_max(m, v[0], v[1]), v[2], v[3]);
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = qi_max(m, __shfl_xor_sync(0xffffffffu, m, o), 0.0f);
@@ -153,27 +162,37 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W)
     if (!once) load(c0);
     if (!finite) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[i] = 0.0f;
+      for (int i = 0; i < V * 4; ++i) x4[i] = 0;
     }
     float far = 0.0f;
     uint32_t w[PER / 4];
 #pragma unroll
-    for (int i = 0; i < PER / 4; ++i) w[i] = qi_four(v + 4 * i, inv, far);
+    for (int i = 0; i < PER / 4; ++i) {
+      float v[4];
+      qi_unpack<T>(x4, i, v);
+      w[i] = qi_four(v, inv, far);
+    }
     if (far > kQiSafe) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const float t = v[i] * inv;
-        if (fabsf(t - rintf(t)) > kQiSafe) {
-          const int shift = 8 * (i % 4);
-          w[i / 4] = (w[i / 4] & ~(0xFFu << shift)) | ((uint32_t)qi_settle(v[i], m, inv) & 0xFFu) << shift;
+      for (int i = 0; i < PER / 4; ++i) {
+        float v[4];
+        qi_unpack<T>(x4, i, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float t = v[j] * inv;
+          if (fabsf(t - rintf(t)) > kQiSafe)
+            w[i] = (w[i] & ~(0xFFu << (8 * j))) | ((uint32_t)qi_settle(v[j], m, inv) & 0xFFu) << (8 * j);
         }
       }
     }
     if (tiny && m > 0.0f) {
 #pragma unroll
       for (int i = 0; i < PER / 4; ++i) {
+        float v[4];
+        qi_unpack<T>(x4, i, v);
         w[i] = 0;
-        for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)qi_tiny(v[4 * i + j], m) & 0xFFu) << (8 * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i] |= ((uint32_t)qi_tiny(v[j], m) & 0xFFu) << (8 * j);
       }
     }
     if constexpr (VEC) {

@@ -167,13 +167,17 @@ cudaError_t is_launch(const Int8Args& p, bool pdl, cudaStream_t stream) {
 
 }  // namespace
 
-int int8_stream_max_tokens() { return 64; }
+// Measured against the kernel with swapped operand roles (us in a graph, weights
+// from HBM, this kernel / that one): 4096 x 7168 (256 units of 16 rows): 8 tokens
+// 11.9 / 18.9, 32 17.2 / 19.6, 64 26.6 / 20.3; 7168 x 2048: 32 tokens 11.0 / 14.5,
+// 64 17.5 / 15.8; 1001 x 1552: 32 tokens 6.1 / 7.0, 64 9.9 / 7.6; 24576 x 1536: 32
+// tokens 19.0 / 34.2, 64 34.0 / 37.5.
+bool int8_stream_takes(const Int8Args& p) { return p.m <= 32; }
 
 cudaError_t int8_stream_launch(const Int8Args& p, bool pdl, cudaStream_t stream) {
   if (p.m <= 8) return is_launch<1>(p, pdl, stream);
   if (p.m <= 16) return is_launch<2>(p, pdl, stream);
-  if (p.m <= 32) return is_launch<4>(p, pdl, stream);
-  return is_launch<8>(p, pdl, stream);
+  return is_launch<4>(p, pdl, stream);
 }
 
 }  // namespace dg

@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     uint32_t armed = 0;  // bit s: slot s was filled
     bool ok = true;
     auto wait_free = [&]() {
-      return wait_bounded(smem_u32(&sh.empty[s]), (used >> s & 1u) ^ 1u, abort_flag, p.timeout_ns, p.err,
+      return wait_quick(smem_u32(&sh.empty[s]), (used >> s & 1u) ^ 1u, abort_flag, p.timeout_ns, p.err,
                           kSiteProducerEmpty);
     };
     // says what slot s will hold, and how many bytes that is
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     MoeStage st;
     bool ok = true;
     auto take = [&]() {
-      ok = wait_bounded(smem_u32(&sh.summed[n % kBuffers]), (n / kBuffers) & 1, abort_flag, p.timeout_ns, p.err,
+      ok = wait_quick(smem_u32(&sh.summed[n % kBuffers]), (n / kBuffers) & 1, abort_flag, p.timeout_ns, p.err,
                         kSiteMoeSums);
       if (ok) st = sh.unit[n % kBuffers];
       return ok && st.hit >= 0;
@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   bool ok = true;
   // the team's next stage, or false where there is none (or a wait ran out)
   auto take = [&]() {
-    ok = wait_bounded(smem_u32(&sh.full[s]), used >> s & 1u, abort_flag, p.timeout_ns, p.err, kSiteMmaFull);
+    ok = wait_quick(smem_u32(&sh.full[s]), used >> s & 1u, abort_flag, p.timeout_ns, p.err, kSiteMmaFull);
     if (ok) st = sh.stage[s];
     return ok && st.hit >= 0;
   };
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   };
   // a buffer of the exchange is free / holds unit `now`'s sums
   auto wait_taken = [&]() {
-    ok = wait_bounded(smem_u32(&sh.taken[n % kBuffers]), ((n / kBuffers) & 1) ^ 1, abort_flag, p.timeout_ns, p.err,
+    ok = wait_quick(smem_u32(&sh.taken[n % kBuffers]), ((n / kBuffers) & 1) ^ 1, abort_flag, p.timeout_ns, p.err,
                       kSiteMoeSums);
   };
   auto hand_over = [&](const MoeStage& now) {
