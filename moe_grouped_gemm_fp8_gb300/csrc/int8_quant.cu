@@ -3,9 +3,10 @@
 // on how a division or a reciprocal rounds).
 //
 // Bound by HBM.  A row is read once and stays in registers between its maximum
-// and its codes.  The quotient is estimated as x (127 / amax), off by at most
-// 2^-16 at 127; only where it lies nearer than that to a half integer are
-// 254 |x| and (2 n + 1) amax compared, exactly.
+// and its codes.  127 / amax is bracketed by two FP32 numbers, 2^-22 below and above
+// its rounded value; where x times both rounds to one integer, so does the exact
+// quotient.  Only elsewhere (6 values in 100,000) are 254 |x| and (2 n + 1) amax
+// compared, exactly.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -50,12 +51,12 @@ __device__ __forceinline__ float qi_max(float m, float a, float b) {
   return r;
 }
 
-// The code of v where its estimate lies near a half integer: 254 |v| against
-// (2 n + 1) amax, n below that half.  Both products are kept exactly as an FP32
-// and its rounding error; near each other, their difference is exact too.
-__device__ __forceinline__ int qi_settle(float v, float amax, float inv) {
+// The code of v where the bracket holds a half integer: 254 |v| against (2 n + 1)
+// amax, n the lower integer.  Both products are kept exactly as an FP32 and its
+// rounding error; near each other, their difference is exact too.
+__device__ __forceinline__ int qi_settle(float v, float amax, float low) {
   // (2^-8 of both: 255 amax may be too large; every bit stays above 2^-149, as amax >= kQiTiny)
-  const float n = floorf(fabsf(v) * inv), odd = fmaf(2.0f, n, 1.0f);
+  const float n = rintf(fabsf(v) * low), odd = fmaf(2.0f, n, 1.0f);
   const float a = fabsf(v) * 0.00390625f;
   amax *= 0.00390625f;
   const float p = __fmul_rn(254.0f, a), m = __fmul_rn(odd, amax);
@@ -68,24 +69,39 @@ __device__ __forceinline__ int qi_settle(float v, float amax, float inv) {
 // rounding cannot reach a half integer (a 31-bit number over one of 24).
 __device__ __noinline__ int qi_tiny(float v, float amax) { return (int)rint(127.0 * (double)v / (double)amax); }
 
-// Four values -> four codes in a word.  far: the largest distance of an
-// estimate from its integer.
-__device__ __forceinline__ uint32_t qi_four(const float (&v)[4], float inv, float& far) {
-  const float2 magic = make_float2(12582912.0f, 12582912.0f), back = make_float2(-12582912.0f, -12582912.0f);
-  const float2 t0 = mul2(make_float2(v[0], v[1]), inv), t1 = mul2(make_float2(v[2], v[3]), inv);
-  const float2 u0 = add2(t0, magic), u1 = add2(t1, magic);
-  const float2 n0 = add2(u0, back), n1 = add2(u1, back);
-  const float2 f0 = fma2(n0, make_float2(-1.0f, -1.0f), t0), f1 = fma2(n1, make_float2(-1.0f, -1.0f), t1);
-  far = abs_max3(abs_max3(far, f0.x, f0.y), f1.x, f1.y);
-  const uint32_t a = __byte_perm(__float_as_uint(u0.x), __float_as_uint(u0.y), 0x0040);
-  const uint32_t b = __byte_perm(__float_as_uint(u1.x), __float_as_uint(u1.y), 0x0040);
-  return __byte_perm(a, b, 0x5410);
+// Adding it rounds to an integer, which the low bits hold.
+constexpr float kQiMagic = 12582912.0f;  // 1.5 2^23
+
+// Four values -> four codes in a word; open: nonzero where the bracket's ends round
+// to different integers.
+__device__ __forceinline__ uint32_t qi_four(const float (&v)[4], float low, float high, uint32_t& open) {
+  const float2 magic = make_float2(kQiMagic, kQiMagic), l = make_float2(low, low), h = make_float2(high, high);
+  const float2 a = make_float2(v[0], v[1]), b = make_float2(v[2], v[3]);
+  const float2 al = fma2(a, l, magic), ah = fma2(a, h, magic), bl = fma2(b, l, magic), bh = fma2(b, h, magic);
+  open |= __float_as_uint(al.x) ^ __float_as_uint(ah.x);
+  open |= __float_as_uint(al.y) ^ __float_as_uint(ah.y);
+  open |= __float_as_uint(bl.x) ^ __float_as_uint(bh.x);
+  open |= __float_as_uint(bl.y) ^ __float_as_uint(bh.y);
+  const uint32_t x = __byte_perm(__float_as_uint(al.x), __float_as_uint(al.y), 0x0040);
+  const uint32_t y = __byte_perm(__float_as_uint(bl.x), __float_as_uint(bl.y), 0x0040);
+  return __byte_perm(x, y, 0x5410);
 }
 
-// Estimates off by more than this from a half integer round as the exact
-// quotient does: 127 (2^-24 + 2^-24) < 2^-16 for the reciprocal's and the
-// product's rounding.
-constexpr float kQiSafe = 0.5f - 1.0f / 32768.0f;
+// max(m, magnitudes of a word's values), NaN where one is: pairs of halves, or an FP32.
+template <class T>
+__device__ __forceinline__ void qi_max_word(uint32_t& m, uint32_t w) {
+  if constexpr (sizeof(T) == 4) {
+    m = __float_as_uint(qi_max(__uint_as_float(m), __uint_as_float(w), 0.0f));
+  } else if constexpr (std::is_same<T, __half>::value) {
+    const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&m), __habs2(*reinterpret_cast<const __half2*>(&w)));
+    m = *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                         __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+    m = *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
 constexpr float kQiTiny = 1e-30f;  // below it 127 / amax may overflow
 
 // W warps a row.  VEC: rows of x on 16 bytes and of codes on 16 / sizeof(T);
@@ -107,7 +123,7 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W, W <= 8 ? 4 : 2)
   const int n = on ? cols : 0;
   constexpr int kWide = 32 * W * PER;  // columns of a pass; more than one only at the widest W
   uint32_t x4[V * 4];  // the values as they came
-  float m = 0.0f;
+  uint32_t most = 0;
   auto load = [&](int c0) {
     if constexpr (VEC) {
 #pragma unroll
@@ -136,11 +152,16 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W, W <= 8 ? 4 : 2)
   for (int c0 = 0; c0 == 0 || c0 < cols; c0 += kWide) {
     load(c0);
 #pragma unroll
-    for (int i = 0; i < PER / 4; ++i) {
-      float v[4];
-      qi_unpack<T>(x4, i, v);
-      m = qi_max(qi_max(m, v[0], v[1]), v[2], v[3]);
-    }
+    for (int i = 0; i < V * 4; ++i) qi_max_word<T>(most, x4[i]);
+  }
+  float m;
+  if constexpr (sizeof(T) == 4) {
+    m = __uint_as_float(most);
+  } else {
+    const uint32_t pair[2] = {most, 0};
+    float v[4];
+    qi_unpack<T>(pair, 0, v);
+    m = qi_max(0.0f, v[0], v[1]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = qi_max(m, __shfl_xor_sync(0xffffffffu, m, o), 0.0f);
@@ -157,6 +178,7 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W, W <= 8 ? 4 : 2)
   if (at == 0) scales[row] = finite ? m / 127.0f : __uint_as_float(0x7FC00000u);
   const bool tiny = m < kQiTiny;
   const float inv = finite && !tiny ? 127.0f / m : 0.0f;
+  const float low = inv * (1.0f - 0x1p-22f), high = inv * (1.0f + 0x1p-22f);
   int8_t* qr = q + row * cols;
   for (int c0 = 0; c0 == 0 || c0 < cols; c0 += kWide) {
     if (!once) load(c0);
@@ -164,25 +186,23 @@ __global__ void __launch_bounds__(W <= 8 ? 256 : 32 * W, W <= 8 ? 4 : 2)
 #pragma unroll
       for (int i = 0; i < V * 4; ++i) x4[i] = 0;
     }
-    float far = 0.0f;
+    uint32_t open = 0;
     uint32_t w[PER / 4];
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i) {
       float v[4];
       qi_unpack<T>(x4, i, v);
-      w[i] = qi_four(v, inv, far);
+      w[i] = qi_four(v, low, high, open);
     }
-    if (far > kQiSafe) {
+    if (open) {
 #pragma unroll
       for (int i = 0; i < PER / 4; ++i) {
         float v[4];
         qi_unpack<T>(x4, i, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float t = v[j] * inv;
-          if (fabsf(t - rintf(t)) > kQiSafe)
-            w[i] = (w[i] & ~(0xFFu << (8 * j))) | ((uint32_t)qi_settle(v[j], m, inv) & 0xFFu) << (8 * j);
-        }
+        for (int j = 0; j < 4; ++j)
+          if (fmaf(v[j], low, kQiMagic) != fmaf(v[j], high, kQiMagic))
+            w[i] = (w[i] & ~(0xFFu << (8 * j))) | ((uint32_t)qi_settle(v[j], m, low) & 0xFFu) << (8 * j);
       }
     }
     if (tiny && m > 0.0f) {
