@@ -1728,6 +1728,11 @@ dg_status dg_fp8_moe_few_tokens(const void* x, int64_t ldx, const void* router, 
   if ((s = get_encoder()) != DG_OK) return s;
   const MoeEncode map = [](CUtensorMap* to, const void* base, uint64_t cols, uint64_t rows,
                            uint32_t box_rows, uint32_t slices) {
+    if (box_rows == 0) {
+      const uint64_t dims[2] = {cols, rows}, strides[1] = {cols * 8};
+      const uint32_t box[2] = {slices, 1};
+      return encode(to, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) == DG_OK;
+    }
     const uint64_t dims[3] = {128, rows, cols / 128}, strides[2] = {cols, 128};
     const uint32_t box[3] = {128, box_rows, slices};
     return encode(to, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == DG_OK;

@@ -12,11 +12,12 @@ namespace dg {
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxTopK = 16;
 constexpr int kMoeMaxExperts = 512;
-constexpr int kMoeMaxParts = 16;       // shares of the hit experts in the second product
+constexpr int kMoeMaxParts = 8;        // shares of the hit experts in the second product
 constexpr int kMoeBarrierWords = 32;  // the grid barrier's counter and those of the units
 
 // Encodes weights of `rows` rows and `cols` columns as bytes [cols / 128][rows][128]
-// in boxes of slices x box_rows x 128, 128-byte swizzle.
+// in boxes of slices x box_rows x 128, 128-byte swizzle; with box_rows 0, words of 8
+// bytes [rows][cols] in boxes of one row x slices.
 using MoeEncode = bool (*)(CUtensorMap* to, const void* base, uint64_t cols, uint64_t rows,
                            uint32_t box_rows, uint32_t slices);
 
@@ -45,7 +46,7 @@ struct MoeArgs {
   uint64_t* keys;              // [tokens, experts]: ordered as what the choice goes by
   uint8_t* xh;                 // [tokens, d / 128] chunks as the products read them
   float* h;                    // [tokens * top_k, f], pairs in the order of their experts
-  uint8_t* hh;                 // [tokens * top_k, f / 128] chunks
+  uint8_t* hh;                 // by hit expert [f / 128][its tokens] chunks
   float* part;                 // [shares, tokens, d]
 };
 

@@ -35,16 +35,19 @@ constexpr int kMoeWarps = 16;     // that multiply
 constexpr int kMoeFinishers = 3;  // that finish units; one more fetches
 constexpr int kMoeThreads = 32 * (kMoeWarps + kMoeFinishers + 1);
 constexpr int kMoeStages = 6;        // at most
-constexpr int kMoeSmem = 209 * 1024;  // ring and exchange
+constexpr int kMoeSmem = 210 * 1024;  // ring and exchange
 constexpr int kScoreThreads = 256;
 constexpr int kScoreTokens = 8;  // tokens of a CTA of the first kernel
 
 // A token's 128 columns: 128 halves in the order in which the lanes read them,
-// then their scale, and nothing up to a multiple of 16 bytes.  Lane (r, q) of a
+// then their scale, and nothing up to a multiple of 16 bytes.  x lies by token,
+// since its experts are not known yet: [token][columns / 128].  h lies by expert,
+// so that a stage's tokens are one copy: [hit expert][columns / 128][its token], the
+// pieces 320 bytes apart (8 lanes, two tokens, then read all banks).  Lane (r, q) of a
 // warp holds, of weight rows r and r + 8, columns 32 q to 32 q + 31; product j
 // (0..7) multiplies columns 32 q + 4 j + 0..3 of every q.  Of the halves, unit
 // j / 2 comes first, then q, then 8 columns.
-constexpr int kMoeChunkBytes = 272;
+constexpr int kMoeChunkBytes = 272, kMoeHiddenBytes = 320;
 __device__ __forceinline__ int moe_half_at(int k) { return ((k >> 3) & 3) * 32 + (k >> 5) * 8 + (k & 7); }
 
 // ---------------------------------------------------------------- scores, and x as halves
@@ -395,16 +398,25 @@ __device__ __forceinline__ void moe_route(const MoeArgs& p, MoeShared& sh, int l
 // tokens of one expert at least three stages of 32 rows fit, with 64 two of 128.
 constexpr int up_lg(int max) { return max == 1 ? 1 : max <= 4 ? 2 : 3; }
 constexpr int down_lg(int max) { return max == 1 ? 0 : max <= 4 ? 2 : 3; }
-template <int LG>
+// GATHER: the tokens come four at a time by TMA gathers, packed.
+template <bool UP, int LG, bool GATHER>
 struct MoeShape {
   static constexpr int lg = LG, slices = kMoeWarps >> LG;
-  static constexpr int kBytes = slices * kMoeChunkBytes;
-  // a token's place: its chunks, and up to 64 past a multiple of 128 (no bank conflicts)
-  static constexpr int token_bytes = kBytes + ((64 - kBytes) & 127);
+  // room of a token in a stage; from one 128 columns to the next, from one token to the next
+  static constexpr int token_bytes = slices * (UP ? kMoeChunkBytes : kMoeHiddenBytes);
+  static constexpr int kPlace = UP ? token_bytes + (GATHER ? 0 : (64 - token_bytes) & 127) : token_bytes;
+  static __device__ __forceinline__ int slice_step(int count) { return UP ? kMoeChunkBytes : count * kMoeHiddenBytes; }
+  static constexpr int token_step = UP ? kPlace : kMoeHiddenBytes;
   static __device__ __forceinline__ int stage_bytes(int most_tokens) {
-    return (32768 + 512 + most_tokens * token_bytes + 1023) & ~1023;
+    const int n = GATHER ? (most_tokens + 3) & ~3 : most_tokens;
+    return (32768 + 512 + n * kPlace + 1023) & ~1023;
   }
 };
+
+// A copy takes the TMA unit about 90 cycles however small it is: where an expert can
+// have many tokens, x comes four rows a copy (40 tokens to 16 experts: 288 us without,
+// 266 with; 16 tokens to 64, mostly one to three each: 400 and 422).
+constexpr bool moe_gathers(int max) { return max >= 4; }
 // Teams of warps that take the stages by turns, a warp of two 16 rows and 256
 // columns of each of its team's: fewer waits a byte than with all 16 warps on
 // every stage (16 rows, 128 columns), and twice the independent products.  Each
@@ -416,6 +428,9 @@ constexpr int moe_teams(int max) { return max <= 2 ? 2 : 1; }
 constexpr bool moe_turns(int max) { return max <= 2; }
 constexpr int moe_buffers(int max) { return max == 1 ? 4 : max == 2 ? 3 : 1; }
 
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -423,12 +438,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // The producer warp's side of a stage.
-template <bool UP, class Shape>
+template <bool UP, bool GATHER, class Shape>
 struct MoeFetch {
   static constexpr int lg = Shape::lg, slices = Shape::slices;
   const MoeArgs& p;
   const MoeShared& sh;
   const CUtensorMap* map;
+  const CUtensorMap* map_x;  // GATHER
   int lane;
   // columns / 128 of the stage, and scale words
   __device__ __forceinline__ int slices_of(const MoeStage& st) const {
@@ -437,7 +453,10 @@ struct MoeFetch {
   __device__ __forceinline__ int words_of(const MoeStage& st, int n) const { return ((st.chunk & 3) + n + 3) / 4; }
   __device__ __forceinline__ uint32_t bytes(const MoeStage& st) const {
     const int n = slices_of(st);
-    return n ? (uint32_t)(32768 + (words_of(st, n) << lg) * 64 + st.count * n * kMoeChunkBytes) : 0;
+    if (n == 0) return 0;
+    const int tokens = GATHER ? ((st.count + 3) & ~3) * Shape::token_bytes
+                              : st.count * n * (UP ? kMoeChunkBytes : kMoeHiddenBytes);
+    return (uint32_t)(32768 + (words_of(st, n) << lg) * 64 + tokens);
   }
   // 32 KB (slices past the last column come as zeros) and scale words
   __device__ __forceinline__ void weights(uint32_t to, uint32_t bar, const MoeStage& st) const {
@@ -456,10 +475,29 @@ struct MoeFetch {
   __device__ __forceinline__ void tokens(uint32_t to, uint32_t bar, const MoeStage& st) const {
     const int n = slices_of(st), chunks = (UP ? p.d : p.f) / 128;
     if (n == 0) return;
-    for (int t = lane; t < st.count; t += 32) {
-      const int at = UP ? sh.pair_token[st.first + t] : st.first + t;
-      bulk_load(to + 32768 + 512 + t * Shape::token_bytes,
-                (UP ? p.xh : p.hh) + ((int64_t)at * chunks + st.chunk) * kMoeChunkBytes, (uint32_t)n * kMoeChunkBytes, bar);
+    to += 32768 + 512;
+    if constexpr (!UP) {
+      if (lane == 0)
+        bulk_load(to, p.hh + ((int64_t)st.first * chunks + (int64_t)st.chunk * st.count) * kMoeHiddenBytes,
+                  (uint32_t)(n * st.count) * kMoeHiddenBytes, bar);
+    } else if constexpr (GATHER) {
+      // (the last four filled up with the last token)
+      if (lane * 4 < st.count) {
+        int row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = sh.pair_token[st.first + min(lane * 4 + i, st.count - 1)];
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(to + lane * 4 * Shape::token_bytes),
+            "l"(reinterpret_cast<uint64_t>(map_x)), "r"(st.chunk * (kMoeChunkBytes / 8)), "r"(row[0]), "r"(row[1]),
+            "r"(row[2]), "r"(row[3]), "r"(bar)
+            : "memory");
+      }
+    } else {
+      for (int t = lane; t < st.count; t += 32)
+        bulk_load(to + t * Shape::kPlace,
+                  p.xh + ((int64_t)sh.pair_token[st.first + t] * chunks + st.chunk) * kMoeChunkBytes,
+                  (uint32_t)n * kMoeChunkBytes, bar);
     }
   }
 };
@@ -475,10 +513,11 @@ __device__ __forceinline__ void moe_multiply(const uint8_t* stage, int tile, int
   const uint8_t* low = stage + slice * (UP ? 1024 << lg : 2048 << lg) + tile * (UP ? 1024 : 2048) + r * 128;
   const uint32_t* words = reinterpret_cast<const uint32_t*>(stage + 32768) + (UP ? tile * 8 + r : tile * 16 + r);
   // (columns of tokens that do not exist hold the last token's: nothing reads their sums)
-  const uint8_t* tokens = stage + 32768 + 512 + slice * kMoeChunkBytes;
-  const uint8_t* x = tokens + min(r, count - 1) * Shape::token_bytes + q * 16;
-  const uint8_t* x0 = tokens + min(2 * q, count - 1) * Shape::token_bytes + 256;
-  const uint8_t* x1 = tokens + min(2 * q + 1, count - 1) * Shape::token_bytes + 256;
+  const int step = Shape::slice_step(count);
+  const uint8_t* tokens = stage + 32768 + 512 + slice * step;
+  const uint8_t* x = tokens + min(r, count - 1) * Shape::token_step + q * 16;
+  const uint8_t* x0 = tokens + min(2 * q, count - 1) * Shape::token_step + 256;
+  const uint8_t* x1 = tokens + min(2 * q + 1, count - 1) * Shape::token_step + 256;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int chunk = first_chunk + slice + i;
@@ -503,14 +542,14 @@ __device__ __forceinline__ void moe_multiply(const uint8_t* stage, int tile, int
 #pragma unroll
       for (int nb = 0; nb < MAX; ++nb) {
         if (nb && nb * 8 >= count) break;
-        const uint8_t* xb = (nb ? tokens + min(nb * 8 + r, count - 1) * Shape::token_bytes + q * 16 : x) +
-                            i * kMoeChunkBytes + h * 128;
+        const uint8_t* xb = (nb ? tokens + min(nb * 8 + r, count - 1) * Shape::token_step + q * 16 : x) +
+                            i * step + h * 128;
         const uint4 b0 = *reinterpret_cast<const uint4*>(xb), b1 = *reinterpret_cast<const uint4*>(xb + 64);
         const int m = nb * 8 + 2 * q;
         const float t0 = *reinterpret_cast<const float*>(
-            (nb ? tokens + min(m, count - 1) * Shape::token_bytes + 256 : x0) + i * kMoeChunkBytes);
+            (nb ? tokens + min(m, count - 1) * Shape::token_step + 256 : x0) + i * step);
         const float t1 = *reinterpret_cast<const float*>(
-            (nb ? tokens + min(m + 1, count - 1) * Shape::token_bytes + 256 : x1) + i * kMoeChunkBytes);
+            (nb ? tokens + min(m + 1, count - 1) * Shape::token_step + 256 : x1) + i * step);
         float d[4] = {};
         mma_f16(d, a[0], b0.x, b0.y);
         mma_f16(d, a[1], b0.z, b0.w);
@@ -573,7 +612,7 @@ __device__ __forceinline__ void moe_halves(const MoeArgs& p, int block, int firs
     uint2 w;
     w.x = *reinterpret_cast<const uint32_t*>(&a);
     w.y = *reinterpret_cast<const uint32_t*>(&b);
-    uint8_t* to = p.hh + ((int64_t)(first + n) * blocks + block) * kMoeChunkBytes;
+    uint8_t* to = p.hh + ((int64_t)first * blocks + (int64_t)block * count + n) * kMoeHiddenBytes;
     *reinterpret_cast<uint2*>(to + 2 * moe_half_at(lane * 4)) = w;
     if (lane == 0) *reinterpret_cast<float*>(to + 256) = s;
   }
@@ -650,9 +689,9 @@ struct MoeWalk {
 template <int MAX>
 __global__ void __launch_bounds__(kMoeThreads, 1)
     moe_layer_kernel(const __grid_constant__ MoeArgs p, const __grid_constant__ CUtensorMap map_up,
-                     const __grid_constant__ CUtensorMap map_down) {
-  using Up = MoeShape<up_lg(MAX)>;
-  using Down = MoeShape<down_lg(MAX)>;
+                     const __grid_constant__ CUtensorMap map_down, const __grid_constant__ CUtensorMap map_x) {
+  using Up = MoeShape<true, up_lg(MAX), moe_gathers(MAX)>;
+  using Down = MoeShape<false, down_lg(MAX), false>;
   // a finishing warp waits for its next unit, kMoeFinishers later: that buffer's last use must be one it has seen end
   static_assert(!moe_turns(MAX) || moe_buffers(MAX) >= kMoeFinishers, "a wait could pass a phase early");
   constexpr int kTeams = moe_teams(MAX);
@@ -665,7 +704,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kMoeStages; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
-      mbar_init(smem_u32(&sh.empty[i]), kMoeWarps / moe_teams(MAX));
+      mbar_init(smem_u32(&sh.empty[i]), kMoeWarps);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&sh.summed[i]), kMoeWarps);
@@ -675,6 +714,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&map_up);
     tma_prefetch_desc(&map_down);
+    if (moe_gathers(MAX)) tma_prefetch_desc(&map_x);
   }
   griddep_wait();
   const int live = live_tokens(p);
@@ -688,11 +728,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
   float* const exchange = reinterpret_cast<float*>(smem + kMoeSmem - exchange_bytes);
   const int up_bytes = Up::stage_bytes(most), down_bytes = Down::stage_bytes(most);
   const int up_stages = min((kMoeSmem - exchange_bytes) / up_bytes, kMoeStages) / kTeams * kTeams;
-  const int down_stages = min((kMoeSmem - exchange_bytes) / down_bytes, kMoeStages) / kTeams * kTeams;
+  const int down_stages = min((kMoeSmem - exchange_bytes) / down_bytes, kMoeStages);
   const int tiles = p.d / kDownRows, up_chunks = p.d / 128, down_chunks = p.f / 128;
-  // Shares of the hit experts, each a unit of its own: a dozen units an SM, of four stages at least.
+  // Shares of the hit experts, each a unit of its own, until there are two units an SM, of four stages at least.  (More
+  // cost more in partial sums than finer units win: 16 shares where 4 do take 40 tokens' second product from 80 to
+  // 125 us.)
   int parts = 1;
-  while (2 * parts <= hits && parts < kMoeMaxParts && tiles * parts < 12 * (int)gridDim.x &&
+  while (2 * parts <= hits && parts < kMoeMaxParts && tiles * parts < 2 * (int)gridDim.x &&
          (int64_t)kDownRows * p.f * (hits / (2 * parts)) >= 4 * 32768)
     parts *= 2;
 
@@ -718,7 +760,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     };
     const MoeStage none{-1, 0, 0, 0, 0, 0, 0, 0};
     {
-      const MoeFetch<true, Up> fetch{p, sh, &map_up, lane};
+      const MoeFetch<true, moe_gathers(MAX), Up> fetch{p, sh, &map_up, &map_x, lane};
       MoeWalk<true, kTeams> walk{p, hits, hits * (p.f / kUpRows), 1, kUpRows, Up::slices, up_chunks, p.counter + 2, lane, sh};
       int told = 0;
       for (walk.begin(); ok; s = s + 1 == up_stages ? 0 : s + 1) {
@@ -739,8 +781,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     for (s = 0; s < up_stages && ok; ++s) ok = wait_free();
     s = 0;
     {
-      const MoeFetch<false, Down> fetch{p, sh, &map_down, lane};
-      MoeWalk<false, kTeams> walk{p, hits, hits ? tiles * parts : 0, parts, kDownRows, Down::slices, down_chunks, p.counter + 3, lane, sh};
+      const MoeFetch<false, false, Down> fetch{p, sh, &map_down, nullptr, lane};
+      MoeWalk<false, 1> walk{p, hits, hits ? tiles * parts : 0, parts, kDownRows, Down::slices, down_chunks, p.counter + 3, lane, sh};
       walk.begin();
       // Wd does not wait for h
       int first = 0;
@@ -770,13 +812,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         fetch.tokens(base + i * down_bytes, smem_u32(&sh.full[i]), st);
       }
       ok = ok && *abort_flag == 0;
-      int told = 0;
       for (s = first == down_stages ? 0 : first; ok; s = s + 1 == down_stages ? 0 : s + 1) {
         if (!(ok = wait_free())) break;
         if (walk.done()) {
           arm(none, 0);
-          if (++told == kTeams) break;
-          continue;
+          break;
         }
         const MoeStage st = walk.stage();
         arm(st, fetch.bytes(st));
@@ -908,11 +948,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     if (ok) st = sh.stage[s];
     return ok && st.hit >= 0;
   };
-  auto give = [&](int stages) {
+  auto give = [&](int stages, int step) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[s]));
+    if (lane == 0) mbar_arrive_n(smem_u32(&sh.empty[s]), (uint32_t)step);
     used ^= 1u << s;
-    s = s + kTeams == stages + team ? team : s + kTeams;
+    s = s + step >= stages ? s + step - stages : s + step;
   };
   // a buffer of the exchange is free / holds unit `now`'s sums
   auto wait_taken = [&]() {
@@ -949,7 +989,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         moe_multiply<true, Up, kTeams, MAX>(smem + s * up_bytes, tile, kTeams * slice, st.chunk, up_chunks, st.count,
                                             lane, acc);
       const MoeStage now = st;
-      give(up_stages);
+      give(up_stages, kTeams);
       if (!now.end) continue;
       wait_taken();
       if (!ok) break;
@@ -961,23 +1001,23 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       hand_over(now);
     }
     if (ok) {
-      give(up_stages);
+      give(up_stages, kTeams);
       finish();
     }
-    s = team;
+    // the other team's slots have been used as often as this one's
+    if (kTeams == 2) used = team == 0 ? used | used << 1 : used | used >> 1;
+    s = 0;
   }
-  const int tile = member & ((1 << Down::lg) - 1), slice = member >> Down::lg, r = lane >> 2, q = lane & 3;
+  // (in the second product, where each expert's sums are taken out one by one, all warps take every stage)
+  const int tile = warp & ((1 << Down::lg) - 1), slice = warp >> Down::lg, r = lane >> 2, q = lane & 3;
   bool fresh = true;  // nothing of this unit is in the exchange
   while (ok && take()) {
-    if (st.chunk < kTeams * Down::slices) clear();  // the team's first stage of an expert
-    const bool real = st.chunk < down_chunks;
-    if (st.chunk + kTeams * slice < down_chunks)
-      moe_multiply<false, Down, kTeams, MAX>(smem + s * down_bytes, tile, kTeams * slice, st.chunk, down_chunks, st.count,
-                                             lane, acc);
+    if (st.chunk == 0) clear();
+    if (st.chunk + slice < down_chunks)
+      moe_multiply<false, Down, 1, MAX>(smem + s * down_bytes, tile, slice, st.chunk, down_chunks, st.count, lane, acc);
     const MoeStage now = st;
-    give(down_stages);
-    const bool last = real && now.chunk + kTeams * Down::slices >= down_chunks;  // the team's last of the expert
-    if (!last && !now.end) continue;
+    give(down_stages, 1);
+    if (now.chunk + Down::slices < down_chunks) continue;
     float* const mine = exchange + n % kBuffers * down_buffer + warp * live * 16;  // [token][16 rows]
     if (fresh) {
       wait_taken();
@@ -986,24 +1026,22 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       __syncwarp();
     }
     // an expert's sums, with the weight of each of its tokens
-    if (last) {
 #pragma unroll
-      for (int nb = 0; nb < MAX; ++nb) {
-        if (nb * 8 >= now.count) break;
+    for (int nb = 0; nb < MAX; ++nb) {
+      if (nb * 8 >= now.count) break;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int m = nb * 8 + 2 * q + i;
-          if (m < now.count) {
-            const int t = sh.pair_token[now.first + m];
-            const float w = sh.weight[t * p.top_k + sh.pair_slot[now.first + m]];
-            float* y = mine + t * 16 + r;
-            y[0] = fmaf(w, acc[nb][i], y[0]);
-            y[8] = fmaf(w, acc[nb][2 + i], y[8]);
-          }
+      for (int i = 0; i < 2; ++i) {
+        const int m = nb * 8 + 2 * q + i;
+        if (m < now.count) {
+          const int t = sh.pair_token[now.first + m];
+          const float w = sh.weight[t * p.top_k + sh.pair_slot[now.first + m]];
+          float* y = mine + t * 16 + r;
+          y[0] = fmaf(w, acc[nb][i], y[0]);
+          y[8] = fmaf(w, acc[nb][2 + i], y[8]);
         }
       }
-      __syncwarp();
     }
+    __syncwarp();
     fresh = now.end != 0;
     if (fresh) hand_over(now);
   }
@@ -1014,9 +1052,13 @@ template <int MAX>
 cudaError_t moe_layer_launch(const MoeArgs& p, const void* up, const void* down, MoeEncode encode, int sms,
                              cudaStream_t stream) {
   constexpr size_t smem = kMoeSmem + 1024;
-  CUtensorMap map_up, map_down;
-  if (!encode(&map_up, up, p.d, (uint64_t)p.experts * 2 * p.f, 8 << up_lg(MAX), MoeShape<up_lg(MAX)>::slices) ||
-      !encode(&map_down, down, p.f, (uint64_t)p.experts * p.d, 16 << down_lg(MAX), MoeShape<down_lg(MAX)>::slices))
+  CUtensorMap map_up, map_down, map_x = {};
+  if (!encode(&map_up, up, p.d, (uint64_t)p.experts * 2 * p.f, 8 << up_lg(MAX), kMoeWarps >> up_lg(MAX)) ||
+      !encode(&map_down, down, p.f, (uint64_t)p.experts * p.d, 16 << down_lg(MAX), kMoeWarps >> down_lg(MAX)))
+    return cudaErrorInvalidValue;
+  // x as words of 8 bytes [tokens][d / 128 * 34], a row's slices a box (box_rows 0: not weights)
+  if (moe_gathers(MAX) && !encode(&map_x, p.xh, (uint64_t)(p.d / 128) * (kMoeChunkBytes / 8), p.tokens, 0,
+                                  (kMoeWarps >> up_lg(MAX)) * (kMoeChunkBytes / 8)))
     return cudaErrorInvalidValue;
   cudaError_t e = set_smem(moe_layer_kernel<MAX>, smem, smem);
   if (e != cudaSuccess) return e;
@@ -1032,7 +1074,7 @@ cudaError_t moe_layer_launch(const MoeArgs& p, const void* up, const void* down,
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, moe_layer_kernel<MAX>, p, map_up, map_down);
+  return cudaLaunchKernelEx(&cfg, moe_layer_kernel<MAX>, p, map_up, map_down, map_x);
 }
 
 }  // namespace
@@ -1053,7 +1095,7 @@ uint64_t moe_few_tokens_layout(MoeArgs& a, void* workspace) {
   a.keys = reinterpret_cast<uint64_t*>(take(t * e * 8));
   a.xh = take(t * (d / 128) * kMoeChunkBytes);
   a.h = reinterpret_cast<float*>(take(pairs * f * 4));
-  a.hh = take(pairs * (f / 128) * kMoeChunkBytes);
+  a.hh = take(pairs * (f / 128) * kMoeHiddenBytes);
   a.part = reinterpret_cast<float*>(take(kMoeMaxParts * t * d * 4));
   return at;
 }
