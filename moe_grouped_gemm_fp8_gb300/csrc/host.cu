@@ -1776,6 +1776,7 @@ dg_status dg_int8_gemm_nt(const void* a, const float* sa, const void* b, const f
   p.k = (int32_t)k;
   p.fp16 = out_dtype == DG_DTYPE_FP16;
   p.vector = aligned16(d) && ldd % 8 == 0 && (!c || (aligned16(c) && ldc % 8 == 0));
+  if (p.vector && aligned_to(d, 32) && ldd % 16 == 0) p.vector = 2;
   p.sms = sms;
   p.timeout_ns = g_timeout_ns.load();
   const bool pdl = g_pdl.load() != 0;

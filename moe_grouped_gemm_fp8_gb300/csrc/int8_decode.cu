@@ -20,7 +20,6 @@
 namespace dg {
 namespace {
 
-constexpr int kIdAhead = 3;  // stages whose loads are in flight
 
 template <int TN>
 struct IdPlan {
@@ -34,6 +33,7 @@ template <int TN>
 __global__ void __launch_bounds__(kIgThreads, 1) int8_decode_kernel(const Int8Args p, const int split) {
   using Plan = IdPlan<TN>;
   constexpr int STAGES = Plan::kStages, STAGE = Plan::kStage;
+  constexpr int kAhead = TN <= 64 ? 3 : 2;  // stages whose loads are in flight in registers
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem_raw + (base - smem_u32(smem_raw)) + STAGES * STAGE);
@@ -110,15 +110,15 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_decode_kernel(const Int8Ar
       t.load(vt, p.lda, k, in);
       ++lk;
     };
-    uint4 vw[kIdAhead][IgRows<128>::kPieces], vt[kIdAhead][IgRows<TN>::kPieces];
+    uint4 vw[kAhead][IgRows<128>::kPieces], vt[kAhead][IgRows<TN>::kPieces];
 #pragma unroll
-    for (int h = 0; h < kIdAhead; ++h) load(vw[h], vt[h]);
+    for (int h = 0; h < kAhead; ++h) load(vw[h], vt[h]);
     int s = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int kb = 0; kb < kbs && ok; kb += kIdAhead) {
+    for (int kb = 0; kb < kbs && ok; kb += kAhead) {
 #pragma unroll
-      for (int h = 0; h < kIdAhead; ++h) {
+      for (int h = 0; h < kAhead; ++h) {
         if (kb + h >= kbs || !ok) break;
         if (!wait_quick(empty(s), phase ^ 1u, abort_flag, tmo, p.err, kSiteProducerEmpty)) {
           ok = false;

@@ -66,6 +66,7 @@ __device__ __forceinline__ void ig_store(const Int8Args& p, const uint32_t (&acc
 #pragma unroll
   for (int i = 0; i < 4; ++i)  // c may be d
     all[i] = p.c ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.c) + from)[i] : make_uint4(0, 0, 0, 0);
+  uint4 out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint4 cw = all[i];
@@ -87,7 +88,15 @@ __device__ __forceinline__ void ig_store(const Int8Args& p, const uint32_t (&acc
         o[j] = bf16x2_bits(x, y);
       }
     }
-    reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + at)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  uint16_t* d = static_cast<uint16_t*>(p.d) + at;
+  if (p.vector == 2) {
+    st_global_32(d, out[0], out[1]);
+    st_global_32(d + 16, out[2], out[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(d)[i] = out[i];
   }
 }
 

@@ -17,7 +17,7 @@ struct Int8Args {
   int64_t lda, ldb, ldc, ldd;
   int32_t m, n, k;
   int32_t fp16;      // the result's type: FP16, else BF16
-  int32_t vector;    // rows of d (and c) may be accessed 16 bytes at a time
+  int32_t vector;    // rows of d and c may be accessed 16 bytes at a time; 2: rows of d are on 32
   int32_t sms;
   uint64_t timeout_ns;
   unsigned long long* err;

@@ -568,6 +568,20 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// A barrier of `threads` threads; whether `mine` holds for all of them.
+__device__ __forceinline__ bool all_agree(int id, int threads, bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(threads), "r"((uint32_t)mine)
+      : "memory");
+  return all != 0;
+}
+
 __device__ __forceinline__ void add4(float4& v, const float4& o) {
   v.x += o.x;
   v.y += o.y;
@@ -829,7 +843,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     for (s = 0; s < kMoeStages; ++s)
       if (armed >> s & 1u) {
         const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(smem_u32(&sh.full[s]), (used >> s & 1u) ^ 1u) && global_timer_ns() - t0 < p.timeout_ns) {
+        while (!mbar_try_wait(smem_u32(&sh.full[s]), (used >> s & 1u) ^ 1u) &&
+               global_timer_ns() - t0 < p.timeout_ns + 1000000000ull) {
         }
       }
     return;
@@ -853,6 +868,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     auto take = [&]() {
       ok = wait_quick(smem_u32(&sh.summed[n % kBuffers]), (n / kBuffers) & 1, abort_flag, p.timeout_ns, p.err,
                         kSiteMoeSums);
+      // (warps that share units meet at barriers: all go on, or none)
+      if (!kTurns) ok = all_agree(1, kTeam, ok);
       if (ok) st = sh.unit[n % kBuffers];
       return ok && st.hit >= 0;
     };
