@@ -1,9 +1,9 @@
-// Product of 8-bit integers for a few dozen tokens: D = c + sa sb (a b^T) with the
-// operands' roles swapped.
+// Product of 8-bit integers too small for a tile an SM: D = c + sa sb (a b^T) with
+// the operands' roles swapped.
 //
 // 128 rows of b (channels) take the MMA's 128 lanes and the tokens its columns, so
-// that no lane is spent on tokens that do not exist; the strip's columns are
-// split over the CTAs of a cluster, whose partial sums meet in shared memory, each
+// that no lane is spent on tokens that do not exist; the columns are split over
+// the CTAs of a cluster, whose partial sums meet in shared memory, each
 // CTA adding some tokens' in the CTAs' order.  Bound by reading b once and by the
 // depth of loads in flight.  MEASURED
 #include <cuda_fp16.h>
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_decode_kernel(const Int8Ar
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_ctarank(), strip = blockIdx.x / split;
+  const int rank = (int)cluster_ctarank(), strip = blockIdx.x / split, m0 = blockIdx.y * TN;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_decode_kernel(const Int8Ar
     IgRows<128> w;
     IgRows<TN> t;
     w.aim(p.b, p.ldb, strip * 128, p.n, row, col);
-    t.aim(p.a, p.lda, 0, p.m, row, col);
+    t.aim(p.a, p.lda, m0, p.m, row, col);
     int lk = k0;
     auto load = [&](uint4 (&vw)[IgRows<128>::kPieces], uint4 (&vt)[IgRows<TN>::kPieces]) {
       const int k = lk * kIgK;
@@ -160,10 +160,10 @@ __global__ void __launch_bounds__(kIgThreads, 1) int8_decode_kernel(const Int8Ar
   cluster_sync_all();
   const int tokens = TN / split, first = rank * tokens;
   for (int i = threadIdx.x; i < tokens * 128; i += kIgThreads) {
-    const int m = first + (i >> 7), n = strip * 128 + (i & 127);
+    const int m = m0 + first + (i >> 7), n = strip * 128 + (i & 127);
     if (m >= p.m) break;
     if (n >= p.n) continue;
-    const uint32_t at = smem_u32(part + m * 128 + (i & 127));
+    const uint32_t at = smem_u32(part + (m - m0) * 128 + (i & 127));
     float v = 0.0f;
     for (int r = 0; r < split; ++r) v += __uint_as_float(ld_shared_cluster_u32(mapa_shared(at, (uint32_t)r)));
     v *= __ldg(p.sa + m);
@@ -196,7 +196,7 @@ cudaError_t id_launch(const Int8Args& p, int split, bool pdl, cudaStream_t strea
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.n + 127) / 128 * split), 1, 1);
+  cfg.gridDim = dim3((unsigned)((p.n + 127) / 128 * split), (unsigned)((p.m + TN - 1) / TN), 1);
   cfg.blockDim = dim3(kIgThreads, 1, 1);
   cfg.dynamicSmemBytes = Plan::kSmem;
   cfg.stream = stream;
@@ -207,19 +207,27 @@ cudaError_t id_launch(const Int8Args& p, int split, bool pdl, cudaStream_t strea
 
 }  // namespace
 
-// Only where two CTAs at least share a strip: without, the tiles of int8_gemm.cu are
-// as quick or quicker (24576 x 1536, 64 tokens: 37.5 us here, 32.3 there, 96: 48.6 /
-// 32.6; 7168 x 2048 with two: 64 tokens 15.8 / 19.9, 96 20.5 / 20.1; 4096 x 7168
-// with four: 96 tokens 26.2 / 52.0).
-bool int8_decode_takes(const Int8Args& p) { return p.m <= 128 && (p.n + 127) / 128 * 2 <= p.sms; }
+namespace {
+// Strips of 128 channels times blocks of 64 or 128 tokens.
+int64_t id_units(const Int8Args& p) {
+  return (int64_t)((p.n + 127) / 128) * (p.m <= 64 ? 1 : (p.m + 127) / 128);
+}
+}  // namespace
+
+// Where two CTAs at least share each strip and block of tokens; without, the tiles
+// of int8_gemm.cu are as quick or quicker (us in a graph, this kernel / the tiles: 24576 x
+// 1536, 64 tokens 37.5 / 32.3, 96 48.6 / 32.6; with two CTAs: 7168 x 2048, 64 tokens
+// 15.8 / 19.9; with four: 4096 x 7168, 96 tokens 26.2 / 52.0).
+bool int8_decode_takes(const Int8Args& p) { return id_units(p) * 2 <= p.sms; }
 
 cudaError_t int8_decode_launch(Int8Args p, bool pdl, cudaStream_t stream) {
   cudaError_t e = error_word_address(&p.err);
   if (e != cudaSuccess) return e;
-  // as many CTAs a strip as the device runs at once
-  const int strips = (p.n + 127) / 128, kbs = (p.k + kIgK - 1) / kIgK;
+  // as many CTAs as the device runs at once; clusters of 8 where they fill half of it, so that all find room (17 of them:
+  // 64 tokens, 2112 x 7168, 21.7 us)
+  const int64_t units = id_units(p), kbs = (p.k + kIgK - 1) / kIgK;
   int split = 1;
-  while (split < 8 && strips * split * 2 <= p.sms && 2 * split <= kbs) split *= 2;
+  while (split < 8 && units * split * 2 <= (split == 4 ? p.sms / 2 : p.sms) && 2 * split <= kbs) split *= 2;
   if (p.m <= 64) return id_launch<64>(p, split, pdl, stream);
   return id_launch<128>(p, split, pdl, stream);
 }

@@ -395,26 +395,34 @@ cudaError_t ig_launch(const Int8Args& p, bool pdl, cudaStream_t stream) {
 cudaError_t int8_gemm_launch(Int8Args p, bool pdl, cudaStream_t stream) {
   cudaError_t e = error_word_address(&p.err);
   if (e != cudaSuccess) return e;
-  // Pairs where their tiles fill most of the SMs: the width whose last wave is
-  // fullest, by the columns that the waves pass over.
-  const int64_t mb2 = (p.m + 255) / 256, pairs = p.sms / 2;
-  if (pairs > 0 && mb2 * ((p.n + 255) / 256) * 4 >= pairs * 3) {
-    int best = 256;
-    int64_t least = INT64_MAX;
-    for (int bn : {256, 224, 192}) {
-      const int64_t waves = (mb2 * ((p.n + bn - 1) / bn) + pairs - 1) / pairs, cost = waves * bn;
-      if (cost < least) {
-        least = cost;
-        best = bn;
-      }
+  // The tile whose waves take the least time.  A stage takes (us, measured at K = 7168 and 2048, one tile an SM): 128 x 64
+  // 0.73, 128 x 128 0.82; of pairs 256 x 192 0.94, 256 x 224 0.96, 256 x 256 1.03.  (333 x 4096 x 7168: 78.6, 46.1, 53.1,
+  // 53.5, 57.6 us; 2048 x 7168 x 2048: 135.5, 78.9, 61.5, 63.3, 54.6.)
+  struct {
+    int bn, rows, slots, stage;
+  } const tiles[] = {{64, 128, p.sms, 73},
+                     {128, 128, p.sms, 82},
+                     {192, 256, p.sms / 2, 94},
+                     {224, 256, p.sms / 2, 96},
+                     {256, 256, p.sms / 2, 103}};
+  int best = 64;
+  int64_t least = INT64_MAX;
+  for (const auto& t : tiles) {
+    if (t.slots < 1) continue;
+    const int64_t all = (int64_t)((p.m + t.rows - 1) / t.rows) * ((p.n + t.bn - 1) / t.bn);
+    const int64_t cost = (all + t.slots - 1) / t.slots * t.stage;
+    if (cost < least) {
+      least = cost;
+      best = t.bn;
     }
-    if (best == 192) return ig_launch<192, true>(p, pdl, stream);
-    if (best == 224) return ig_launch<224, true>(p, pdl, stream);
-    return ig_launch<256, true>(p, pdl, stream);
   }
-  const int64_t mb = (p.m + 127) / 128;
-  if (mb * ((p.n + 127) / 128) >= p.sms) return ig_launch<128, false>(p, pdl, stream);
-  return ig_launch<64, false>(p, pdl, stream);
+  switch (best) {
+    case 64: return ig_launch<64, false>(p, pdl, stream);
+    case 128: return ig_launch<128, false>(p, pdl, stream);
+    case 192: return ig_launch<192, true>(p, pdl, stream);
+    case 224: return ig_launch<224, true>(p, pdl, stream);
+    default: return ig_launch<256, true>(p, pdl, stream);
+  }
 }
 
 }  // namespace dg

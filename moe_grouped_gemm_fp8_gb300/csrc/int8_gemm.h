@@ -26,7 +26,7 @@ struct Int8Args {
 // int8_stream.cu: a few rows of a, without widening them in memory
 bool int8_stream_takes(const Int8Args& p);
 cudaError_t int8_stream_launch(const Int8Args& p, bool pdl, cudaStream_t stream);
-// int8_decode.cu: up to 128 rows of a, operand roles swapped
+// int8_decode.cu: operand roles swapped, columns split over clusters
 bool int8_decode_takes(const Int8Args& p);
 cudaError_t int8_decode_launch(Int8Args p, bool pdl, cudaStream_t stream);
 // int8_gemm.cu: tiles on the tensor cores
