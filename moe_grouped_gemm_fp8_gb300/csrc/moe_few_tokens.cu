@@ -18,6 +18,11 @@
 // few tokens and, in its block-scaled form, round them to 8 bits.  Units of work
 // are taken from a counter: SMs read at rates that differ by a quarter.
 //
+// Measured in a graph, D = 7168, F = 2048: one token, 8 of 32 experts, 86 us (352 MB,
+// 4.1 TB/s; scores 6, choosing 3, first product 50, barrier 2, second product 23); 16
+// tokens, 8 of 64 experts, 407 us (2.5 GB, 6.2 TB/s, 91% of the copy's rate); 64 tokens,
+// 4 of 16 experts, 217 us (0.7 GB, 3.3 TB/s: the multiplying warps' instructions).
+//
 // x and h are carried as halves with a power of two per 128 columns: 11 bits
 // (BF16 x exactly, but for values 2^29 below the largest of the 128), so that
 // the only roundings are those and the result's own.
