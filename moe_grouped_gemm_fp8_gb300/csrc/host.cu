@@ -1797,7 +1797,7 @@ dg_status dg_quantize_int8(const void* x, int32_t dtype, void* q, float* scales,
   int sms = 0;
   dg_status s = current_device(&sms);
   if (s != DG_OK) return s;
-  return from_cuda(quantize_int8_launch(x, dtype, static_cast<int8_t*>(q), scales, rows, cols, ldx, g_pdl.load() != 0,
+  return from_cuda(quantize_int8_launch(x, dtype, static_cast<int8_t*>(q), scales, rows, cols, ldx, sms, g_pdl.load() != 0,
                                         static_cast<cudaStream_t>(stream)));
 }
 

@@ -34,6 +34,6 @@ cudaError_t int8_gemm_launch(Int8Args p, bool pdl, cudaStream_t stream);
 
 // int8_quant.cu
 cudaError_t quantize_int8_launch(const void* x, int dtype, int8_t* q, float* scales, int64_t rows, int64_t cols,
-                                 int64_t ldx, bool pdl, cudaStream_t stream);
+                                 int64_t ldx, int sms, bool pdl, cudaStream_t stream);
 
 }  // namespace dg

@@ -141,3 +141,36 @@ def test_waits_that_may_run_out():
             dg.set_wait_timeout_ns(2_000_000_000)
         assert status in (0, DG_ERR_DEVICE_TIMEOUT)
         assert torch.equal(call(), want) and dg.get_device_error()[0] == 0
+
+
+@pytest.mark.parametrize("dtype,digits", [(BF16, 8), (torch.float16, 11)])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_codes_of_all_significands(dtype, digits, pad):
+    """A row for each significand of its maximum, in it every significand at the nine binades that have codes; rows on
+    16 bytes and off them."""
+    half = 2 ** (digits - 1)
+    s = torch.arange(half, 2 * half, dtype=torch.float64)
+    values = torch.cat([s * 2.0 ** -k for k in range(1, 10)])
+    rows = torch.cat([s[:, None], values.expand(half, -1), torch.zeros(half, 7 + pad, dtype=torch.float64)], 1)
+    below = torch.where(s[None, :] <= s[:, None], s[None, :], 0.0)   # the maximum's own binade
+    x = torch.cat([rows[:, :1 + len(values)], below, rows[:, 1 + len(values):]], 1) * 2.0 ** -4
+    x = x * torch.where(torch.arange(x.shape[1]) % 3 == 2, -1.0, 1.0)
+    y = x.to(dtype)
+    assert torch.equal(y.double(), x) and x.shape[1] % 8 == (0 if pad == 0 else 1)
+    I.check_codes(y.cuda())
+
+
+def test_many_rows_of_the_quantiser():
+    """More rows than CTAs run at once, at each number of warps a row takes."""
+    g = torch.Generator().manual_seed(0)
+    for rows, cols in [(9001, 24), (6000, 1032), (3001, 2056), (1300, 4104), (700, 8200)]:
+        x = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randn(rows, 1, generator=g))
+        x[rows // 2, 3] = float("nan")
+        x[7] = 0
+        for dtype in (BF16, torch.float16, torch.float32):
+            y = x.to(dtype).cuda()
+            q, s = dg.quantize_int8(y)
+            good = torch.arange(rows, device="cuda") != rows // 2
+            want, top = I.quantised(y[good])
+            assert torch.equal(q[good], want) and ((s[good].double() - top).abs() <= top * 2.0 ** -24).all()
+            assert (q[~good] == 0).all() and torch.isnan(s[~good]).all()
