@@ -163,7 +163,7 @@ def test_codes_of_all_significands(dtype, digits, pad):
 def test_many_rows_of_the_quantiser():
     """More rows than CTAs run at once, at each number of warps a row takes."""
     g = torch.Generator().manual_seed(0)
-    for rows, cols in [(9001, 24), (6000, 1032), (3001, 2056), (1300, 4104), (700, 8200)]:
+    for rows, cols in [(9001, 24), (6000, 1032), (3001, 2056), (1300, 4104), (700, 8200), (400, 16400), (160, 33000)]:
         x = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randn(rows, 1, generator=g))
         x[rows // 2, 3] = float("nan")
         x[7] = 0
