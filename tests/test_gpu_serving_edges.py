@@ -174,3 +174,13 @@ def test_many_rows_of_the_quantiser():
             want, top = I.quantised(y[good])
             assert torch.equal(q[good], want) and ((s[good].double() - top).abs() <= top * 2.0 ** -24).all()
             assert (q[~good] == 0).all() and torch.isnan(s[~good]).all()
+
+
+def test_quantiser_on_fewer_sms():
+    x = torch.randn(500, 1032, generator=torch.Generator().manual_seed(0)).to(BF16).cuda()
+    try:
+        for n in (1, 5):
+            dg.set_num_sms(n)
+            I.check_codes(x)
+    finally:
+        dg.set_num_sms(0)
