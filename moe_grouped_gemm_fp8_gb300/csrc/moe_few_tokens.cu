@@ -80,6 +80,12 @@ __device__ __forceinline__ float finite_magnitude(float v) {
   return a < INFINITY ? a : 0.0f;
 }
 
+// exp(hi + lo), lo far below 1: hi alone costs a logit of -80 the 2^-19 of the result that it lacks.
+__device__ __forceinline__ float exp_of(float hi, float lo) {
+  const float e = expf(hi);
+  return e > 0.0f ? fmaf(e, lo, e) : e;  // (next to an infinity lo is no number)
+}
+
 // The row count of a padded batch; out of range: an error, and the nearest.
 __device__ __forceinline__ int live_tokens(const MoeArgs& p) {
   if (!p.num_tokens) return p.tokens;
@@ -314,7 +320,18 @@ __device__ void moe_pick(const MoeArgs& p, MoeShared& sh, int t, int lane) {
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     w /= sum;
   } else {
-    w = on ? 1.0f / (1.0f + expf(-l.x)) : 0.0f;
+    // exp(min(l, 0)) / (1 + exp(-|l|)), which no l takes out of range; to be divided by their sum, all times
+    // exp(-m), m the largest of the chosen l where that is below 0, so that the sum is 1/2 at least.
+    float m = 0.0f;
+    if (p.renormalize) {
+      m = on ? l.x : -INFINITY;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      m = fminf(m, 0.0f);
+    }
+    float2 low = l.x < 0.0f ? l : make_float2(0.0f, 0.0f);
+    add_exactly(low.x, low.y, -m);
+    w = on ? exp_of(low.x, low.y) / (1.0f + expf(-fabsf(l.x))) : 0.0f;
     if (p.renormalize) {
       float sum = w;
 #pragma unroll
