@@ -495,7 +495,8 @@ typedef enum dg_score { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
  *   up, up_sf    E4M3 [num_experts, 2f, d] (gate rows, then up rows) and packed
  *            scales int32 [num_experts, ceil(d/512), 2f]
  *   down, down_sf  E4M3 [num_experts, d, f], int32 [num_experts, ceil(f/512), d]
- *   c        BF16 [tokens, d], row stride ldc, or NULL; may be y or x
+ *   c        BF16 [tokens, d], row stride ldc, or NULL; may be x, and y when
+ *            ldc == ldy
  *   num_tokens  int32 on the device or NULL: only rows below it are tokens
  *            (the rest of a captured graph's batch); y's other rows are not
  *            written.  Outside [0, tokens]: DG_ERR_DEVICE_BAD_INDEX is

@@ -1696,6 +1696,8 @@ dg_status dg_fp8_moe_few_tokens(const void* x, int64_t ldx, const void* router, 
   if (activation != DG_ACT_SILU && activation != DG_ACT_GELU_TANH) return DG_ERR_INVALID_ARG;
   if (ldx < d || ldy < d || (c && ldc < d)) return DG_ERR_INVALID_ARG;
   if (tokens == 0) return DG_OK;
+  // a row of y would be stored over another's c, which may not be read yet
+  if (c && c == y && ldc != ldy && tokens > 1) return DG_ERR_INVALID_ARG;
   if (!x || !router || !up || !up_sf || !down || !down_sf || !y || !experts || !weights || !workspace)
     return DG_ERR_INVALID_ARG;
   if (ldx % 8 != 0 || !aligned16(x) || !aligned16(router) || !aligned16(up) || !aligned16(down) ||

@@ -71,7 +71,7 @@ def fp8_moe_few_tokens(x: torch.Tensor, router: torch.Tensor, up: torch.Tensor, 
 
     c: BF16 [T, D] to add (the residual).  num_tokens: int32 [1] on the device;
     rows past it are not computed and not written (a captured graph's padded
-    batch).  d: a preallocated y; it may be c or x."""
+    batch).  d: a preallocated y; it may be x, or c with c's strides."""
     if stream is not None:
         return MoeOutput(*_under(stream, fp8_moe_few_tokens, x, router, up, up_sf, down, down_sf, top_k, router_bias,
                                  score, renormalize, scale, activation, c, num_tokens, d))
