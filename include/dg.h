@@ -532,8 +532,12 @@ dg_status dg_fp8_moe_few_tokens_workspace_size(int32_t tokens, int64_t d, int64_
  *   b        int8 [n, k], row stride ldb likewise;  sb  float [n], one per row (channel)
  *   c        [m, n] of out_dtype, row stride ldc >= n, or NULL; may be d when ldc == ldd
  *   d        [m, n] of out_dtype (DG_DTYPE_BF16 or DG_DTYPE_FP16), row stride ldd >= n
- * k % 16 == 0, any m and n, all 256 codes.  Products are exact, sums FP32, one
- * rounding.  (Rows of d and c on 16 bytes are written 16 bytes at a time.) */
+ * k % 16 == 0, any m and n, all 256 codes.  Products are exact; sums are FP32:
+ * exact within 2^24 (always up to k = 1024), beyond with FP32's error next to the
+ * largest partial sum, of up to one step every 16 columns; then times sa, times
+ * sb (the sum times sa has to stay below 2^128), plus C, in FP32, and rounded
+ * once.  (The kernel for more than a few tokens accesses rows of d and c that lie
+ * on 16 bytes 16 bytes at a time.) */
 dg_status dg_int8_gemm_nt(const void* a, const float* sa, const void* b, const float* sb, const void* c,
                           void* d, int64_t m, int64_t n, int64_t k, int64_t lda, int64_t ldb, int64_t ldc,
                           int64_t ldd, int32_t out_dtype, void* stream);

@@ -2,8 +2,13 @@
 //
 // sm_103a's tcgen05 has no integer kind, but an 8-bit integer is a half exactly
 // and so is a product of two in FP32: kind::f16, at its rate, gives what integer
-// products would (sums past 2^24 round as FP32 sums do, far below the result's
-// 16 bits).  Nothing is widened in memory: warps load the codes, turn them into
+// products would while sums stay within 2^24, so always up to K = 1024.  Beyond, every 16
+// columns the sum so far is cut to FP32's 24 bits, which is little next to the largest
+// partial sum but not next to what is left where they cancel: of +-2^25.6 at
+// K = 8192 results of up to 2^14.7 were off by 400 here, by 9 where warps share the columns.
+// (The quantising of such a row itself leaves thousands.)
+//
+// Nothing is widened in memory: warps load the codes, turn them into
 // halves in registers (1024 + 128 + c is a half whose low byte is c + 128; an
 // addition takes the offset away: 5 instructions for 4 codes) and store them
 // where the MMA reads them, in its 128-byte swizzle.

@@ -186,7 +186,7 @@ def int8_gemm_nt(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.T
     with FP32 scales [N] (quantize_int8's), K % 16 == 0, any M and N.
 
     out_dtype BF16 or FP16, also c's and d's; c may be d.  Products are exact,
-    sums FP32."""
+    sums FP32: exact within 2^24, always up to K = 1024."""
     if stream is not None:
         return _under(stream, int8_gemm_nt, a, sa, b, sb, d, c, out_dtype)
     if out_dtype not in _OUT:
