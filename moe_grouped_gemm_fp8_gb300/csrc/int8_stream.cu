@@ -1,8 +1,9 @@
 // Product of 8-bit integers for a few tokens: D = c + sa sb (a b^T).
 //
 // Bound by reading b once: its rows go through the tensor cores 16 at a time
-// with all tokens (stream_mma.cuh), several warps sharing the columns of 16 rows
-// and joining their sums in shared memory in a fixed order.  A code is exact as
+// with all tokens, 128 columns a stage, by asynchronous copies through the warp's own
+// ring in shared memory; several warps share the columns of 16 rows and join their
+// sums in shared memory in a fixed order.  A code is exact as
 // a half, so is every product in FP32.  Up to 32 tokens: mma.sync with its columns of
 // 8 tokens takes what there is, where a tile of tcgen05 would spend 128 lanes or
 // a cluster's joining of sums on them.  One token, 7168 x 2048: 7.3 us in a graph, 2.0
@@ -23,9 +24,28 @@ namespace {
 
 constexpr int kIsWarps = 16;
 constexpr int kIsThreads = 32 * kIsWarps;
-constexpr int kIsStage = 16 * kStreamCols;  // no scale words
+constexpr int kStreamCols = 128;             // columns of a stage
+constexpr int kIsStage = 16 * kStreamCols;
 constexpr int is_ring(int nb) { return nb <= 2 ? 6 : 4; }
 constexpr size_t is_smem(int nb) { return (size_t)kIsWarps * (is_ring(nb) * kIsStage + nb * 512); }
+
+// Which 4 columns of the 128 a lane holds for a product is free as long as b and a
+// agree.  Lane (r, q) = (lane / 4, lane % 4) takes, of rows r and r + 8, the 16 bytes
+// at columns 16 q and at 64 + 16 q: whole 64-byte pieces a row and instruction.
+// Product j (0..7) multiplies columns 64 (j / 4) + 16 q + 4 (j % 4) + 0..3 of every q.
+//
+// The lane's codes of half a stage (h = 0, 1: 64 columns), decoded: a[i] are the A
+// registers of product 4 h + i.
+__device__ __forceinline__ void stream_decode(const uint8_t* stage, int h, int lane, uint32_t (&a)[4][4]) {
+  const uint4 g = *reinterpret_cast<const uint4*>(stage + h * 1024 + lane * 16);
+  const uint4 u = *reinterpret_cast<const uint4*>(stage + h * 1024 + 512 + lane * 16);
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    DecodeInt8::four(gw[i], a[i][0], a[i][2]);
+    DecodeInt8::four(uw[i], a[i][1], a[i][3]);
+  }
+}
 
 template <int NB>
 __global__ void __launch_bounds__(kIsThreads, 1) int8_stream_kernel(const Int8Args p, const int split) {
@@ -34,7 +54,6 @@ __global__ void __launch_bounds__(kIsThreads, 1) int8_stream_kernel(const Int8Ar
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, q = lane & 3;
   uint8_t* const ring = smem + warp * RING * kIsStage;
   float4* const exchange = reinterpret_cast<float4*>(smem + kIsWarps * RING * kIsStage) + lane;  // [warp][NB][lane]
-  const uint32_t ring_s = smem_u32(ring);
   griddep_wait();
   griddep_launch_dependents();
 
@@ -99,7 +118,7 @@ __global__ void __launch_bounds__(kIsThreads, 1) int8_stream_kernel(const Int8Ar
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[4][4];
-        stream_decode<DecodeInt8>(at, h, lane, w);
+        stream_decode(at, h, lane, w);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           if constexpr (NB > 2) tokens(nb, x[0]);

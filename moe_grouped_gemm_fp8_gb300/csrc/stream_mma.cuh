@@ -1,23 +1,11 @@
-// Products of many weight rows with a few tokens, as a warp's stream: 16 rows of
-// 8-bit weights, 128 columns at a time, go by asynchronous copies through the
-// warp's own ring in shared memory, are decoded to halves in registers (exact:
-// every E4M3 value and every 8-bit integer is a half) and multiplied with the
-// tokens' halves by mma m16n8k16 with FP32 sums.
-//
-// Which 4 columns of the 128 a lane holds for a product is free as long as
-// weights and tokens agree.  Lane (r, q) = (lane / 4, lane % 4) takes, of rows r
-// and r + 8, the 16 bytes at columns 16 q and at 64 + 16 q: whole 64-byte pieces
-// a row and instruction.  Product j (0..7) multiplies columns
-//   64 (j / 4) + 16 q + 4 (j % 4) + 0..3
-// of every q.  The tokens' halves are stored in that order: of each 128 columns
+// 8-bit weights as halves in registers, and mma m16n8k16 of halves with FP32 sums:
+// every E4M3 value and every 8-bit integer is a half exactly.
 #pragma once
 
 #include "dg_device.cuh"
 #include "dg_ops.cuh"
 
 namespace dg {
-
-constexpr int kStreamCols = 128;                       // columns of a stage
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -48,19 +36,5 @@ struct DecodeInt8 {
     hi = *reinterpret_cast<const uint32_t*>(&b);
   }
 };
-
-// The lane's codes of half a stage (h = 0, 1: 64 columns), decoded: a[i] are the
-// A registers of product 4 h + i.
-template <class Decode>
-__device__ __forceinline__ void stream_decode(const uint8_t* stage, int h, int lane, uint32_t (&a)[4][4]) {
-  const uint4 g = *reinterpret_cast<const uint4*>(stage + h * 1024 + lane * 16);
-  const uint4 u = *reinterpret_cast<const uint4*>(stage + h * 1024 + 512 + lane * 16);
-  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    Decode::four(gw[i], a[i][0], a[i][2]);
-    Decode::four(uw[i], a[i][1], a[i][3]);
-  }
-}
 
 }  // namespace dg
