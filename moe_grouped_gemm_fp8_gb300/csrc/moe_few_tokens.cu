@@ -484,6 +484,9 @@ struct MoeFetch {
   __device__ __forceinline__ void weights(uint32_t to, uint32_t bar, const MoeStage& st) const {
     const int n = slices_of(st), cols = UP ? p.d : p.f, rows = UP ? 2 * p.f : p.d, e = sh.hit_expert[st.hit];
     if (n == 0) return;
+    DG_CHECK(p.err, e >= 0 && e < p.experts && st.chunk >= 0 && st.chunk + n <= cols / 128 && st.row >= 0 &&
+                        st.row + ((UP ? 8 : 16) << lg) <= (UP ? p.f : p.d),
+             kSiteCheckLoadB);
     if (lane < (UP ? 2 : 1)) tma_load_3d(to + lane * 16384, map, bar, 0, e * rows + st.row + lane * p.f, st.chunk);
     constexpr int run = (UP ? 8 : 16) << lg;
     if (lane < (UP ? 2 : 1) * words_of(st, n)) {
@@ -497,6 +500,9 @@ struct MoeFetch {
   __device__ __forceinline__ void tokens(uint32_t to, uint32_t bar, const MoeStage& st) const {
     const int n = slices_of(st), chunks = (UP ? p.d : p.f) / 128;
     if (n == 0) return;
+    DG_CHECK(p.err, st.first >= 0 && st.count >= 1 && st.first + st.count <= p.tokens * p.top_k &&
+                        sh.pair_token[st.first + min(lane, st.count - 1)] < p.tokens,
+             kSiteCheckLoadA);
     to += 32768 + 512;
     if constexpr (!UP) {
       if (lane == 0)
@@ -629,6 +635,7 @@ __device__ __forceinline__ void moe_activate(const MoeArgs& p, const float4* sum
                          : make_float2(gate_act<DG_ACT_GELU_TANH>(g.x), gate_act<DG_ACT_GELU_TANH>(g.y));
     const int n = nb * 8 + 2 * q;
     float* h = p.h + (int64_t)(first + n) * p.f + octet * 8 + r;
+    DG_CHECK(p.err, first + count <= p.tokens * p.top_k && octet * 8 + r < p.f, kSiteCheckStore);
     if (n < count) __stcg(h, a.x * u.x);
     if (n + 1 < count) __stcg(h + p.f, a.y * u.y);
   }
@@ -637,6 +644,7 @@ __device__ __forceinline__ void moe_activate(const MoeArgs& p, const float4* sum
 // The 128 columns of h of a block, for a hit expert's tokens, as halves.
 __device__ __forceinline__ void moe_halves(const MoeArgs& p, int block, int first, int count, int lane) {
   const int blocks = p.f / 128;
+  DG_CHECK(p.err, block < blocks && first + count <= p.tokens * p.top_k, kSiteCheckStore);
   for (int n = 0; n < count; ++n) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(p.h + (int64_t)(first + n) * p.f + block * 128) + lane);
     float m = fmaxf(fmaxf(finite_magnitude(v.x), finite_magnitude(v.y)), fmaxf(finite_magnitude(v.z), finite_magnitude(v.w)));
@@ -657,6 +665,7 @@ __device__ __forceinline__ void moe_halves(const MoeArgs& p, int block, int firs
 // Four results of y: their sums over the experts, and c.
 __device__ __forceinline__ void moe_store(const MoeArgs& p, int t, int64_t col, float4 v) {
   const float f[4] = {v.x, v.y, v.z, v.w};
+  DG_CHECK(p.err, t < p.tokens && col + 4 <= p.d, kSiteCheckStore);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float c = p.c ? __bfloat162float(p.c[(int64_t)t * p.ldc + col + i]) : 0.0f;
@@ -785,7 +794,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                           kSiteProducerEmpty);
     };
     // says what slot s will hold, and how many bytes that is
-    auto arm = [&](const MoeStage& what, uint32_t bytes) {
+    auto arm = [&](const MoeStage& what, uint32_t bytes, int room = kMoeSmem) {
+      DG_CHECK(p.err, bytes <= (uint32_t)room, kSiteCheckLoadA);
       if (lane == 0) {
         sh.stage[s] = what;
         mbar_arrive_expect_tx(smem_u32(&sh.full[s]), bytes);
@@ -807,7 +817,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           continue;
         }
         const MoeStage st = walk.stage();
-        arm(st, fetch.bytes(st));
+        arm(st, fetch.bytes(st), up_bytes);
         fetch.weights(base + s * up_bytes, smem_u32(&sh.full[s]), st);
         fetch.tokens(base + s * up_bytes, smem_u32(&sh.full[s]), st);
         walk.next();
@@ -825,7 +835,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
       for (; ok && first < down_stages && !walk.done(); ++first) {
         const MoeStage st = walk.stage();
         s = first;
-        arm(st, fetch.bytes(st));
+        arm(st, fetch.bytes(st), down_bytes);
         fetch.weights(base + s * down_bytes, smem_u32(&sh.full[s]), st);
         walk.next();
       }
@@ -855,7 +865,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
           break;
         }
         const MoeStage st = walk.stage();
-        arm(st, fetch.bytes(st));
+        arm(st, fetch.bytes(st), down_bytes);
         fetch.weights(base + s * down_bytes, smem_u32(&sh.full[s]), st);
         fetch.tokens(base + s * down_bytes, smem_u32(&sh.full[s]), st);
         walk.next();
