@@ -487,8 +487,9 @@ typedef enum dg_score { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
  *   h = act(x Wg^T) * (x Wu^T) of each chosen expert,
  *   y = c + sum over the chosen of w h Wd^T.
  * Logits are summed so exactly (about 48 bits) that near scores keep their
- * order; x and h enter the products with 11 bits at least (no rounding to 8
- * bits), all sums are FP32 and y is rounded once.
+ * order; weights are FP32's; x and h enter the products as halves with a power of
+ * two per 128 columns (x exactly, h with 11 bits; values below 2^-28 of the
+ * largest of those columns lose some), all sums are FP32 and y is rounded once.
  *   x        BF16 [tokens, d], row stride ldx (ldx >= d, ldx % 8 == 0)
  *   router   [num_experts, d] of router_dtype (DG_DTYPE_FP32 or _BF16)
  *   router_bias  float [num_experts] or NULL; only with DG_SCORE_SIGMOID

@@ -13,13 +13,16 @@
 // addition takes the offset away: 5 instructions for 4 codes) and store them
 // where the MMA reads them, in its 128-byte swizzle.
 //
-// What bounds it is shared memory: each half is written once and read by the
-// MMAs.  So large products run on CTA pairs (cta_group::2): 256 x 256 tiles in
-// which a CTA widens 128 rows of a and 128 of b, 64 KB a stage of 128 columns
-// where a CTA alone would need 96 for half the products.  At 4096 x 4096 x 7168 the
-// MMAs alone take 115 us, widening alone 119, both 202: their shared-memory traffic
-// adds up.  Measured in a graph: 4096 x 4096 x 7168 202 us (1.19 PFLOP/s, 63% of the
-// BF16 library product's), 4096 x 24576 x 1536 251 us (1.23).  Codes brought raw into
+// What bounds it is the widening: every code is widened again in each tile that uses
+// it (of 4096 x 4096 a's 19 times, b's 16).  So large products run on CTA pairs
+// (cta_group::2): 256 x 256 tiles in which a CTA widens 128 rows of a and 128 of b, 64 KB
+// a stage of 128 columns where a CTA alone would need 96 for half the products.  At 4096 x
+// 4096 x 7168 the MMAs alone take 115 us, widening alone 119, both 202: they hardly
+// overlap, although neither the tensor pipe (53%) nor shared memory (59%) is full; a
+// first kernel that widens once is not tried.  Measured in a graph: 4096 x 4096 x 7168 202
+// us (1.19 PFLOP/s, 63% of the measured BF16 burst), 4096 x 24576 x 1536 244 us (1.27).
+// With little K the results take longer than the products: a warp stores 32 rows an
+// instruction (4096 x 16384 x 128 80 us, with c 144, for 20 and 40 of bytes).  Codes brought raw into
 // shared memory by TMA and widened from there were slower (253: they pass through
 // it once more), loads three stages ahead too (234: registers spill).
 //
@@ -423,7 +426,8 @@ cudaError_t int8_gemm_launch(Int8Args p, bool pdl, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // The tile whose waves take the least time.  A stage takes (us, measured at K = 7168 and 2048, one tile an SM): 128 x 64
   // 0.73, 128 x 128 0.82; of pairs 256 x 192 0.94, 256 x 224 0.96, 256 x 256 1.03.  (333 x 4096 x 7168: 78.6, 46.1, 53.1,
-  // 53.5, 57.6 us; 2048 x 7168 x 2048: 135.5, 78.9, 61.5, 63.3, 54.6.)
+  // 53.5, 57.6 us; 2048 x 7168 x 2048: 135.5, 78.9, 61.5, 63.3, 54.6.)  What a tile's results take is not counted: below K of
+  // about 700 they decide, and the choice there is not measured.
   struct {
     int bn, rows, slots, stage;
   } const tiles[] = {{64, 128, p.sms, 73},

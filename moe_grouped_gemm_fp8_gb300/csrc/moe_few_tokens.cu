@@ -14,18 +14,22 @@
 // copies of 32 KB of weights and of their expert's tokens in flight; 16 warps
 // decode E4M3 to halves in registers (exact) and multiply by mma m16n8k16 with
 // all tokens of the expert at once, 16 rows x 128 columns a warp and stage.
-// tcgen05 would read the tokens' side at a 128-column tile's price for one to a
-// few tokens and, in its block-scaled form, round them to 8 bits.  Units of work
+// tcgen05 would take the weights as they are in its block-scaled form, but each
+// token's side as two (h: three) 8-bit pieces so as not to round it; for many tokens,
+// where the multiplying warps bound this kernel, that is not tried.  Units of work
 // are taken from a counter: SMs read at rates that differ by a quarter.
 //
-// Measured in a graph, D = 7168, F = 2048: one token, 8 of 32 experts, 86 us (352 MB,
+// Measured in a graph, D = 7168, F = 2048: one token, 8 of 32 experts, 85.5 us (352 MB,
 // 4.1 TB/s; scores 6, choosing 3, first product 50, barrier 2, second product 23); 16
-// tokens, 8 of 64 experts, 407 us (2.5 GB, 6.2 TB/s, 91% of the copy's rate); 64 tokens,
-// 4 of 16 experts, 217 us (0.7 GB, 3.3 TB/s: the multiplying warps' instructions).
+// tokens, 8 of 64 experts, 408 us (2.5 GB, 6.2 TB/s, 91% of the copy's rate); 64 tokens,
+// 4 of 16 experts, 215 us (0.7 GB, 3.3 TB/s: the multiplying warps' instructions).
+// (Models with more experts at this width are tested for their results, at 512 experts
+// of small widths and 150 large ones, but have no figure.)
 //
 // x and h are carried as halves with a power of two per 128 columns: 11 bits
-// (BF16 x exactly, but for values 2^29 below the largest of the 128), so that
-// the only roundings are those and the result's own.
+// (BF16 x exactly, but for values 2^29 below the largest of the 128; h with fewer
+// bits below 2^-28 of it), so that the only roundings are those and the result's own:
+// y is off by about 2^-12 of itself before it is rounded, an eighth of what BF16 rounds.
 #include <algorithm>
 
 #include "dg_device.cuh"
