@@ -23,8 +23,8 @@
 // 4.1 TB/s; scores 6, choosing 3, first product 50, barrier 2, second product 23); 16
 // tokens, 8 of 64 experts, 408 us (2.5 GB, 6.2 TB/s, 91% of the copy's rate); 64 tokens,
 // 4 of 16 experts, 215 us (0.7 GB, 3.3 TB/s: the multiplying warps' instructions).
-// (Models with more experts at this width are tested for their results, at 512 experts
-// of small widths and 150 large ones, but have no figure.)
+// 8 of 256 experts: 1 token 88 us, 16 (107 experts hit) 761 (1.09 of their bytes' time),
+// 64 (221 hit) 1687 (1.17).
 //
 // x and h are carried as halves with a power of two per 128 columns: 11 bits
 // (BF16 x exactly, but for values 2^29 below the largest of the 128; h with fewer
