@@ -646,8 +646,8 @@ dg_status dg_plan_m_grouped_fp8_gemm_nt_masked(int32_t num_groups, int64_t max_m
                                                int32_t* cta_pair);
 
 /* Upper bound on the SMs the persistent GEMM grid uses; 0 = all SMs of the
- * device.  The gated products keep it too.  Process-wide; returns
- * DG_ERR_INVALID_ARG for n < 0. */
+ * device.  The gated products, the integer product and the few-token experts'
+ * products keep it too.  Process-wide; returns DG_ERR_INVALID_ARG for n < 0. */
 dg_status dg_set_num_sms(int32_t n);
 int32_t dg_get_num_sms(void);
 
